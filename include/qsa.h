@@ -350,11 +350,126 @@ qsa_status qsa_split_reduce_static(const float* partial_max, const float* partia
                                    const uint16_t* partial_out, int32_t G, int32_t R, int32_t B,
                                    int32_t C, float* out, qsa_stream_t stream);
 
+/* ------------------------------------------------ the paged 8-bit cache
+ *
+ * Keys and values in blocks of `block` tokens, one e4m3 code per element and
+ * one fp32 scale per (block, KV head) for keys and one for values: an element
+ * stands for scale * code. Block i of sequence b lies in page
+ * page_table[b, i]. The pages do not specify a cache; this is what the
+ * selected block ids index and what the block keys are made from.
+ *
+ *   k, v        e4m3 codes [n_pages, Hkv, block, D], device, 16-byte aligned;
+ *               page_stride bytes (a multiple of 16, at least Hkv*block*D)
+ *               from one page to the next.
+ *   k_scale, v_scale  f32 [n_pages, Hkv], positive and finite.
+ *   page_table  int32 [B, max_blocks]; entries past a sequence's blocks are
+ *               not read. Sequences may share pages that are only read.
+ *   lens        int32 [B]: tokens of each sequence, the n rows of the call
+ *               included. Row j of sequence b stands at position
+ *               lens[b] - n_new[b] + j; a row with j >= n_new[b] or a
+ *               negative position does not exist.
+ *   n_new       int32 [B], or NULL: all n rows of every sequence.
+ * Supported: D 64 or 128; block 16, 32, 64 or 128; max_blocks * block <= 2^30;
+ * Hkv <= 65535. The table, lens, n_new and ids are device data the host does
+ * not see: a page outside [0, n_pages), a block past max_blocks or a position
+ * past the angle table is skipped (no memory outside the buffers is touched)
+ * and recorded; qsa_device_status then returns QSA_ERR_INVALID_ARG.
+ */
+typedef enum { QSA_F16 = 0, QSA_BF16 = 1 } qsa_dtype;
+
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* n_new;
+  int64_t page_stride;
+  int32_t n_pages, max_blocks, B, Hkv, block, D;
+} qsa_kv_cache;
+
+/* Rows [B, n, heads, D] of 16-bit floats in device memory, D contiguous;
+ * strides in elements, multiples of 8 (0 repeats), data 16-byte aligned. */
+typedef struct {
+  const void* data;
+  int64_t stride_b, stride_n, stride_h;
+} qsa_rows;
+
+/*
+ * qsa_kv_append - rotate, quantise and store the new tokens' keys and values.
+ *
+ *   k, v   [B, n, Hkv, D] of `dtype`; q (optional) [B, n, Hq, D].
+ *   cos, sin  f32 [max_pos, rot / 2], 16-byte aligned: the angles of each
+ *          position. The first `rot` elements of a key (and query) are rotated
+ *          in pairs: elements i and i + rot/2, or 2i and 2i + 1 when
+ *          `interleaved` is nonzero: x cos - y sin and y cos + x sin, in fp32,
+ *          each product and sum rounded to nearest. rot: a multiple of 16, at
+ *          most D; 0 rotates nothing (cos and sin may be NULL).
+ *   q_out  with q: [B, n, Hq, D] of `dtype`, contiguous, 16-byte aligned: the
+ *          rotated queries, rounded once; rows that do not exist are zero.
+ *   kb     optional f16 [B, Hkv, max_blocks, D]: the mean of the stored keys
+ *          of every block this call wrote to (block keys for
+ *          qsa_select_step_batched with a kb for each head); other blocks keep
+ *          theirs.
+ * Scales: s_new = the smallest power of two >= 2^-100 with max|x| <= 448 s_new
+ * over the call's new tokens of the block and head (NaN left out, infinities
+ * as the largest finite number). A block whose first token is new takes s_new;
+ * otherwise max(its scale, s_new), and when that is larger the codes it had are
+ * rounded again to the new scale. code = e4m3(x / scale) to nearest even;
+ * infinities are stored as +-448, NaN as NaN. Appending tokens one by one or
+ * together gives the same scales.
+ * A page that the call writes must appear once in the table rows of the call's
+ * sequences. No buffer may overlap another.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED_GEOMETRY,
+ * QSA_ERR_MISALIGNED, as for the sizes and pointers above. B == 0 or n == 0
+ * returns QSA_OK without a launch.
+ */
+qsa_status qsa_kv_append(const qsa_kv_cache* cache, const qsa_rows* k, const qsa_rows* v,
+                         const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                         const float* cos, const float* sin, int32_t rot, int32_t max_pos,
+                         int32_t interleaved, void* q_out, uint16_t* kb, qsa_stream_t stream);
+
+/*
+ * qsa_kv_attend - attention of the n rows over the cache, whole (ids NULL) or
+ * over chosen blocks.
+ *
+ *   q      [B, n, Hq, D] of `dtype`; heads h*R .. h*R + R-1 read KV head h,
+ *          R = Hq / Hkv <= 32.
+ *   A row at position p sees the tokens at positions <= p of every block
+ *   (ids NULL) or of the blocks its list names:
+ *   ids    int32 [B, n_lists, n, k], n_lists 1 (every head the same list) or
+ *          Hkv; negative entries name no block; a block named twice counts
+ *          twice. What qsa_select_step and its relatives return fits.
+ *   out    [B, n, Hq, D] of `dtype`, contiguous, 16-byte aligned:
+ *          sum_t p_t v_t with p = softmax(scale * q.k) over the tokens seen,
+ *          rounded once. Sums and softmax statistics are fp32.
+ *   lse    optional f32 [B, n, Hq]: ln sum_t exp(scale * q.k_t).
+ *          A row that does not exist or sees no token gives out 0, lse -inf.
+ *   workspace  device, 16-byte aligned, at least
+ *          qsa_kv_attend_workspace_bytes bytes; needs no initialisation.
+ *          Calls that may run at the same time need separate ones.
+ * Codes and scales of tokens that a row does not see do not reach its result,
+ * NaN codes included; blocks that no row sees are not read. A NaN in a query
+ * row, or in what it sees, makes that row NaN (a value code: the dimension it
+ * stands in); so does an infinite query.
+ * Results do not depend on timing: repeating a call repeats its bits.
+ * Errors as for qsa_kv_append; QSA_ERR_INVALID_ARG also for a scale that is
+ * not finite, a cache without pages or blocks, or a short workspace.
+ */
+size_t qsa_kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
+qsa_status qsa_kv_attend(const qsa_kv_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,
+                         qsa_dtype dtype, float scale, const int32_t* ids, int32_t n_lists,
+                         int32_t k, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, qsa_stream_t stream);
+
 /*
  * qsa_device_status - synchronizes `stream`, then reads the current device's
- * status word, where kernels record a bounded wait that ran out. Returns
- * QSA_OK if it is clear, QSA_ERR_TIMEOUT if not (and clears it when `clear`
- * is nonzero), or QSA_ERR_CUDA if the synchronization itself failed. The
+ * status word, where kernels record a bounded wait that ran out and a cache
+ * index outside its buffers. Returns QSA_OK if it is clear,
+ * QSA_ERR_INVALID_ARG if it holds the cache index bit (bit 5) alone,
+ * QSA_ERR_TIMEOUT otherwise (and clears it when `clear` is nonzero), or
+ * QSA_ERR_CUDA if the synchronization itself failed. The
  * word's raw bits are stored in *bits when bits is not NULL.
  */
 qsa_status qsa_device_status(int clear, uint32_t* bits, qsa_stream_t stream);

@@ -1,0 +1,406 @@
+// kv_append.cu - appending keys and values to the paged 8-bit cache.
+//
+// For each new token (position p) the key's rotated pairs are
+//     x' = x cos[p] - y sin[p],  y' = y cos[p] + x sin[p]
+// in fp32, each product and each sum rounded (no fused multiply-add), so the
+// stored codes are a fixed function of the inputs. The new tokens of one
+// (block, head) share one scale: the smallest power of two s with
+// max|x| <= 448 s, and at least the block's scale so far when older tokens
+// stand in the block; code = e4m3(x / s), round to nearest even. A power of
+// two makes x / s exact and costs e4m3 no precision (its relative step does
+// not depend on the scale), and when a block's scale grows the older codes
+// are multiplied by a power of two: exact unless they fall below 2^-6, where
+// they are rounded again.
+// The block key is the mean of the block's stored keys, s * sum(codes) / n.
+// Every partial sum of up to 64 codes is a multiple of 2^-9 below 2^15, exact
+// in fp32 in any order.
+//
+// What bounds it: bytes. One CTA owns one (block, head, K or V): it holds the
+// block's new values in registers between the maximum and the rounding, so
+// each input byte is read once and each code written once, and nobody else
+// writes the block's scale.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_internal.h"
+#include "qsa_device.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeadsPerThread = 4;  // query heads that share one load of the angles
+
+struct AppendArgs {
+  KvCacheArgs c;
+  KvRows k, v, q;
+  const float* cos;
+  const float* sin;
+  void* q_out;
+  uint16_t* kb;
+  uint32_t* status;
+  int64_t units;
+  int32_t n, Hq, rot, max_pos, blocks_per_seq;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t off, float (&x)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t off, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread holds two runs of 8 elements of one row. In the rotated part they
+// are the two members of 8 half-split pairs, or 4 + 4 interleaved pairs.
+struct Lane {
+  int off0, off1;  // element offsets of the two runs
+  int ang0, ang1;  // offsets of the angles (half-split: 8 at ang0; interleaved: 4 at each)
+  bool turns;
+};
+
+template <int TPT>
+__device__ __forceinline__ Lane lane_of(int sub, int rot, bool interleaved) {
+  Lane l;
+  l.turns = sub < rot / 16;
+  if (l.turns) {
+    l.off0 = 8 * sub;
+    l.off1 = rot / 2 + 8 * sub;
+    l.ang0 = interleaved ? 4 * sub : 8 * sub;
+    l.ang1 = rot / 4 + 4 * sub;
+  } else {
+    l.off0 = rot + 16 * (sub - rot / 16);
+    l.off1 = l.off0 + 8;
+    l.ang0 = l.ang1 = 0;
+  }
+  return l;
+}
+
+struct Angles {
+  float c[8], s[8];
+};
+
+template <bool PAIRS>
+__device__ __forceinline__ void load_angles(const float* cos, const float* sin, int64_t row, const Lane& l,
+                                            Angles& a) {
+  const int o[2] = {l.ang0, PAIRS ? l.ang1 : l.ang0 + 4};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cos + row + o[i]));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(sin + row + o[i]));
+    a.c[4 * i] = c.x, a.c[4 * i + 1] = c.y, a.c[4 * i + 2] = c.z, a.c[4 * i + 3] = c.w;
+    a.s[4 * i] = s.x, a.s[4 * i + 1] = s.y, a.s[4 * i + 2] = s.z, a.s[4 * i + 3] = s.w;
+  }
+}
+
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+  x = u;
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const Angles& a) {
+  if (PAIRS) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(x[2 * i], x[2 * i + 1], a.c[i], a.s[i]);
+      turn(y[2 * i], y[2 * i + 1], a.c[4 + i], a.s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(x[i], y[i], a.c[i], a.s[i]);
+  }
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv, bool pow2) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
+  uint2 r;
+  r.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+  r.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
+  return r;
+}
+
+__device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x & 0xFFFFu, u.x >> 16, u.y & 0xFFFFu, u.y >> 16};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = e4m3x2_to_float2(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// Rotates the queries: TPT threads a row, each for kHeadsPerThread heads.
+template <int TPT, bool BF16, bool PAIRS>
+__device__ void rotate_queries(const AppendArgs& a) {
+  const int sub = threadIdx.x % TPT;
+  const int chunks = (a.Hq + kHeadsPerThread - 1) / kHeadsPerThread;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) - a.units) * (kThreads / TPT) + threadIdx.x / TPT;
+  if (row >= static_cast<int64_t>(a.c.B) * a.n * chunks) return;
+  const int h0 = static_cast<int>(row % chunks) * kHeadsPerThread;
+  const int64_t token = row / chunks;
+  const int b = static_cast<int>(token / a.n), j = static_cast<int>(token % a.n);
+  const Span sp = span_of(a.c, b, a.n);
+  const int64_t pos = static_cast<int64_t>(sp.first) + j;
+  bool there = j < sp.n_new && pos >= 0;
+  const Lane l = lane_of<TPT>(sub, a.rot, PAIRS);
+  if (there && a.rot > 0 && pos >= a.max_pos) {
+    if (sub == 0) atomicOr(a.status, kErrCacheIndex);
+    there = false;
+  }
+  Angles g;
+  if (there && l.turns) load_angles<PAIRS>(a.cos, a.sin, pos * (a.rot / 2), l, g);
+  const int D = TPT * 16;
+  float x[kHeadsPerThread][8], y[kHeadsPerThread][8];
+  const int64_t in = b * a.q.sb + j * a.q.sn;
+#pragma unroll
+  for (int i = 0; i < kHeadsPerThread; ++i)
+    if (there && h0 + i < a.Hq) {
+      load8<BF16>(a.q.data, in + (h0 + i) * a.q.sh + l.off0, x[i]);
+      load8<BF16>(a.q.data, in + (h0 + i) * a.q.sh + l.off1, y[i]);
+    }
+#pragma unroll
+  for (int i = 0; i < kHeadsPerThread; ++i) {
+    if (h0 + i >= a.Hq) break;
+    const int64_t to = (token * a.Hq + h0 + i) * D;
+    if (!there) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = y[i][e] = 0.0f;
+    } else if (l.turns) {
+      rotate<PAIRS>(x[i], y[i], g);
+    }
+    store8<BF16>(a.q_out, to + l.off0, x[i]);
+    store8<BF16>(a.q_out, to + l.off1, y[i]);
+  }
+}
+
+// TPT threads a token (D = 16 TPT), PASSES * 256 / TPT >= block tokens.
+template <int TPT, int PASSES, bool BF16, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  if (static_cast<int64_t>(blockIdx.x) >= a.units) {
+    rotate_queries<TPT, BF16, PAIRS>(a);
+    return;
+  }
+  constexpr int D = 16 * TPT;
+  constexpr int kTokens = kThreads / TPT;  // tokens of one pass
+  __shared__ uint32_t s_max[kThreads / 32];
+  __shared__ float s_sum[kThreads / 32][D];
+
+  uint32_t u = blockIdx.x;
+  const bool is_v = u & 1;
+  u >>= 1;
+  const int h = static_cast<int>(u % a.c.Hkv);
+  u /= a.c.Hkv;
+  const int i = static_cast<int>(u % a.blocks_per_seq), b = static_cast<int>(u / a.blocks_per_seq);
+
+  const Span sp = span_of(a.c, b, a.n);
+  const int p0 = max(sp.first, 0);
+  if (sp.len <= p0) return;  // no new token
+  const int64_t blk64 = static_cast<int64_t>(p0) / a.c.block + i;
+  const int64_t start64 = blk64 * a.c.block;
+  if (start64 >= sp.len) return;
+  const int64_t end64 = min(start64 + a.c.block, static_cast<int64_t>(sp.len));
+  int page = -1;
+  if (blk64 < a.c.max_blocks) page = __ldg(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
+  if (page < 0 || page >= a.c.n_pages || (a.rot > 0 && end64 > a.max_pos)) {
+    if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
+    return;
+  }
+  const int start = static_cast<int>(start64), end = static_cast<int>(end64);
+  const int n_old = max(p0 - start, 0), held = end - start;
+
+  float* const scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hkv + h;
+  const float s_old = n_old > 0 ? *scale_at : 0.0f;
+  uint8_t* const codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * D;
+  const KvRows& src = is_v ? a.v : a.k;
+  const int64_t in = b * src.sb + h * src.sh;
+  const int sub = threadIdx.x % TPT, tok = threadIdx.x / TPT;
+  const Lane l = lane_of<TPT>(sub, is_v ? 0 : a.rot, PAIRS);
+
+  float x[PASSES][8], y[PASSES][8];
+#pragma unroll
+  for (int t = 0; t < PASSES; ++t) {
+    const int slot = t * kTokens + tok;
+    if (slot >= n_old && slot < held) {
+      const int64_t row = in + (static_cast<int64_t>(start) + slot - sp.first) * src.sn;
+      load8<BF16>(src.data, row + l.off0, x[t]);
+      load8<BF16>(src.data, row + l.off1, y[t]);
+    }
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int t = 0; t < PASSES; ++t) {
+    const int slot = t * kTokens + tok;
+    if (slot >= n_old && slot < held) {
+      if (l.turns) {
+        Angles g;
+        load_angles<PAIRS>(a.cos, a.sin, (static_cast<int64_t>(start) + slot) * (a.rot / 2), l, g);
+        rotate<PAIRS>(x[t], y[t], g);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[t][e]), fabsf(y[t][e])));
+    }
+  }
+  // Non-negative floats order as their bits.
+  const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+  if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = wm;
+  __syncthreads();
+  uint32_t bm = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) bm = max(bm, s_max[w]);
+  const float s_new = pow2_scale(__uint_as_float(bm));
+  const float s = n_old > 0 ? fmaxf(s_old, s_new) : s_new;
+  const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.0f;
+  const float ratio = n_old > 0 ? __fdiv_rn(s_old, s) : 1.0f;
+  const bool want_kb = a.kb != nullptr && !is_v;
+  if (threadIdx.x == 0) *scale_at = s;
+
+  float acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < PASSES; ++t) {
+    const int slot = t * kTokens + tok;
+    if (slot >= held) continue;
+    uint2* const at0 = reinterpret_cast<uint2*>(codes + slot * D + l.off0);
+    uint2* const at1 = reinterpret_cast<uint2*>(codes + slot * D + l.off1);
+    uint2 c0, c1;
+    if (slot >= n_old) {
+      c0 = encode8(x[t], s, inv, pow2);
+      c1 = encode8(y[t], s, inv, pow2);
+      *at0 = c0;
+      *at1 = c1;
+    } else {
+      if (ratio == 1.0f && !want_kb) continue;
+      c0 = *at0;
+      c1 = *at1;
+      if (ratio != 1.0f) {
+        float f[8];
+        decode8(c0, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= ratio;
+        c0 = encode8(f, 1.0f, 1.0f, true);
+        decode8(c1, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= ratio;
+        c1 = encode8(f, 1.0f, 1.0f, true);
+        *at0 = c0;
+        *at1 = c1;
+      }
+    }
+    if (want_kb) {
+      float f[8];
+      decode8(c0, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      decode8(c1, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[8 + e] += f[e];
+    }
+  }
+  if (!want_kb) return;
+#pragma unroll
+  for (int d = TPT; d < 32; d *= 2)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], d);
+  if (threadIdx.x % 32 < TPT) {
+    float* const row = s_sum[threadIdx.x / 32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      row[l.off0 + e] = acc[e];
+      row[l.off1 + e] = acc[8 + e];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w][threadIdx.x];
+    const float mean = __fdiv_rn(__fmul_rn(total, s), static_cast<float>(held));
+    const int64_t at = ((static_cast<int64_t>(b) * a.c.Hkv + h) * a.c.max_blocks + blk64) * D + threadIdx.x;
+    a.kb[at] = __half_as_ushort(__float2half_rn(mean));
+  }
+}
+
+template <int TPT, int PASSES>
+cudaError_t launch_form(const AppendArgs& a, bool bf16, bool pairs, unsigned grid, cudaStream_t stream) {
+  if (bf16) {
+    if (pairs) kv_append_kernel<TPT, PASSES, true, true><<<grid, kThreads, 0, stream>>>(a);
+    else kv_append_kernel<TPT, PASSES, true, false><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    if (pairs) kv_append_kernel<TPT, PASSES, false, true><<<grid, kThreads, 0, stream>>>(a);
+    else kv_append_kernel<TPT, PASSES, false, false><<<grid, kThreads, 0, stream>>>(a);
+  }
+  plan_add("kv_append_kernel");
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t kv_append_grid(const KvAppendProblem& p, int64_t* units, int32_t* blocks_per_seq) {
+  // n tokens that begin anywhere in a block reach at most this many blocks.
+  const int64_t per_seq = (static_cast<int64_t>(p.n) + p.cache.block - 2) / p.cache.block + 1;
+  *blocks_per_seq = static_cast<int32_t>(per_seq);
+  *units = per_seq * p.cache.B * p.cache.Hkv * 2;
+  if (!p.q.data) return *units;
+  const int64_t rows =
+      static_cast<int64_t>(p.cache.B) * p.n * ((p.Hq + kHeadsPerThread - 1) / kHeadsPerThread);
+  const int per_cta = kThreads / (p.cache.D / 16);
+  return *units + (rows + per_cta - 1) / per_cta;
+}
+
+cudaError_t launch_kv_append(const KvAppendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+  AppendArgs a{};
+  a.c = p.cache;
+  a.k = p.k;
+  a.v = p.v;
+  a.q = p.q;
+  a.cos = p.cos;
+  a.sin = p.sin;
+  a.q_out = p.q_out;
+  a.kb = p.kb;
+  a.status = dev.status_word;
+  a.n = p.n;
+  a.Hq = p.Hq;
+  a.rot = p.rot;
+  a.max_pos = p.max_pos;
+  const unsigned grid = static_cast<unsigned>(kv_append_grid(p, &a.units, &a.blocks_per_seq));
+  if (p.cache.D == 128) {
+    if (p.cache.block <= 32) return launch_form<8, 1>(a, p.bf16, p.interleaved, grid, stream);
+    if (p.cache.block <= 64) return launch_form<8, 2>(a, p.bf16, p.interleaved, grid, stream);
+    return launch_form<8, 4>(a, p.bf16, p.interleaved, grid, stream);
+  }
+  if (p.cache.block <= 64) return launch_form<4, 1>(a, p.bf16, p.interleaved, grid, stream);
+  return launch_form<4, 2>(a, p.bf16, p.interleaved, grid, stream);
+}
+
+}  // namespace qsa

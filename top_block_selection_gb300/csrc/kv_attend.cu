@@ -1,0 +1,131 @@
+// kv_attend.cu - launcher of the cache attention, and the kernel that joins
+// the partial results of items that were split over several CTAs.
+#include "kv_attend_kernel.cuh"
+
+#include <algorithm>
+
+namespace qsa {
+namespace {
+
+constexpr int kCombineThreads = 128;
+
+// One CTA per (CTA that began a split item, row): the item's parts are that
+// CTA's second slot and the first slots of the CTAs after it, added in order.
+__global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float s_f[kKvMaxCtas];
+  __shared__ float s_red[kCombineThreads / 32], s_sum[kCombineThreads / 32];
+  pdl_wait();
+  const int c0 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, rows = a.qt * a.R, D = a.c.D;
+  const int e = a.jobs[4 * c0];
+  if (e < 0) return;
+  const int h = a.jobs[4 * c0 + 1], parts = a.jobs[4 * c0 + 2] - c0 + 1;
+  const int b = e / a.n_qt, j = (e - b * a.n_qt) * a.qt + r / a.R;
+  if (j >= a.n) return;
+  float m = -INFINITY, l = 0.0f;
+  for (int i = tid; i < parts; i += kCombineThreads) {
+    const float* const p = part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r);
+    m = fmaxf(m, p[D]);
+  }
+  m = warp_max(m);
+  if (tid % 32 == 0) s_red[tid / 32] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  for (int i = tid; i < parts; i += kCombineThreads) {
+    const float* const p = part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r);
+    // A part without a maximum saw nothing (sum 0) or only NaN scores (sum NaN).
+    const float f = p[D] == -INFINITY ? 1.0f : exp2_approx(p[D] - m);
+    s_f[i] = f;
+    l += p[D + 1] * f;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+  if (tid % 32 == 0) s_sum[tid / 32] = l;
+  __syncthreads();
+  l = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  const int64_t at = (static_cast<int64_t>(b) * a.n + j) * a.Hq + h * a.R + r % a.R;
+  if (tid < D) {
+    float v = part_row(a, 2 * c0 + 1, rows, r)[tid] * s_f[0];
+#pragma unroll 8
+    for (int i = 1; i < parts; ++i) v += part_row(a, 2 * (c0 + i), rows, r)[tid] * s_f[i];
+    v = l == 0.0f ? 0.0f : v / l;
+    if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + tid] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(a.out)[at * D + tid] = __float2half_rn(v);
+  }
+  if (a.lse && tid == 0)
+    a.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * 0.6931471805599453f + logf(l));
+}
+
+// Rows of the instantiation for `rows` of them.
+int rows_form(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+bool encode_cache_map(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.Hkv) * c.block,
+                              static_cast<cuuint64_t>(c.n_pages)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_stride)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.D), static_cast<cuuint32_t>(c.block), 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kKvMaxGroup || (D != 64 && D != 128))
+    return 0;
+  return sizeof(float) * 2 * kKvMaxCtas * kKvMaxGroup * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
+}
+
+cudaError_t init_kv_attend_kernels(const DeviceInfo&) {
+  const CUtensorMap none{};
+  const AttendArgs a{};
+  for (int rt = 4; rt <= 32; rt *= 2) {
+    cudaError_t e = attend_rows_d64(rt, none, none, a, 0, true, nullptr);
+    if (e == cudaSuccess) e = attend_rows_d128(rt, none, none, a, 0, true, nullptr);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+  AttendArgs a{};
+  a.c = p.cache;
+  a.q = p.q;
+  a.out = p.out;
+  a.lse = p.lse;
+  a.ids = p.ids;
+  a.status = dev.status_word;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.n = p.n;
+  a.Hq = p.Hq;
+  a.R = p.Hq / p.cache.Hkv;
+  a.n_lists = p.n_lists;
+  a.k = p.k;
+  a.spt = kKvTile / p.cache.block;
+  a.bf16 = p.bf16;
+  // Chosen blocks are each query's own; over the whole cache, consecutive
+  // queries of a sequence share a tile as far as the rows go.
+  a.qt = p.ids ? 1 : std::min(p.n, kKvMaxGroup / a.R);
+  a.n_qt = (p.n + a.qt - 1) / a.qt;
+  a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
+  const int rt = rows_form(a.qt * a.R);
+  const int grid = std::min(dev.sm_count, kKvMaxCtas);
+  a.jobs = static_cast<int32_t*>(p.workspace);
+  a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
+
+  CUtensorMap tk, tv;
+  if (!encode_cache_map(&tk, p.cache.k, p.cache) || !encode_cache_map(&tv, p.cache.v, p.cache))
+    return cudaErrorInvalidValue;
+  cudaError_t e = p.cache.D == 64 ? attend_rows_d64(rt, tk, tv, a, grid, false, stream)
+                                  : attend_rows_d128(rt, tk, tv, a, grid, false, stream);
+  if (e != cudaSuccess) return e;
+  plan_add("kv_attend_kernel");
+  e = launch_pdl(kv_combine_kernel, dim3(grid, a.qt * a.R), dim3(kCombineThreads), 0, stream, a);
+  if (e == cudaSuccess) plan_add("kv_combine_kernel");
+  return e;
+}
+
+}  // namespace qsa

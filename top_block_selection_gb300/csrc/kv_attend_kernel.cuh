@@ -1,0 +1,920 @@
+// kv_attend_kernel.cuh - attention over the paged 8-bit cache, whole or over
+// chosen blocks. One instantiation per head size and row count.
+//
+// For the R query heads of one KV head (and, over the whole cache, a few
+// consecutive queries), rows r and cached tokens t:
+//     x[r,t] = scale * q_r . (sk_b code_k[t]),  t visible to r;  m_r = max_t x
+//     out_r  = sum_t 2^(x - m) (sv_b code_v[t]) / sum_t 2^(x - m)   (x in log2 units)
+// with sk_b, sv_b the scales of the token's block.
+//
+// The codes go to the tensor cores as they are. Both products are
+// tcgen05.mma kind::f8f6f4 with the cache as the M = 128 operand (128 tokens
+// for the scores, the D dimensions for the output, read MN-major), loaded by
+// TMA and never touched by a thread. The other operand is made e4m3 without
+// losing its bits: a value y is y1 + y2 + y3, y1 = e4m3(y), y2 = e4m3(y - y1),
+// y3 = e4m3(y - y1 - y2). Each term takes 4 significant bits and its sign one
+// more, so three hold the 11 bits of an fp16 query exactly (as far as they lie
+// above 2^-19 of the row's maximum) and a probability to 2^-12. The
+// three terms are three groups of N columns, added in fp32 after the product.
+// With few rows a tile's product is bound by reading the M operand from
+// shared memory, so the extra columns cost little.
+//
+// What bounds it: decoding reads every code once from HBM (about 23 bytes a
+// cycle and SM); over chosen blocks of many queries the codes come from L2.
+// Each CTA (one per SM) runs a ring of 128-token stages filled by one
+// producer warp, two or three warpgroups that take the tiles in turn, each with its
+// own running maximum, sum and output (so that loads, products and the
+// softmax of different tiles overlap without a hand-over between warps), and
+// one warp that prepares the next query rows. All tiles of a call are dealt
+// to the CTAs in equal contiguous shares, whatever the lengths; an (query,
+// head) item that ends up in several CTAs leaves partial results in the
+// workspace, which kv_combine_kernel joins.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_internal.h"
+#include "qsa_device.cuh"
+
+namespace qsa {
+
+constexpr int kKvTile = 128;       // tokens of a tile
+constexpr int kKvMaxSlots = 8;     // blocks of a tile (block >= 16)
+constexpr int kKvMaxCtas = 192;    // bound of the grid, sizes the workspace
+constexpr int kKvNoToken = 0x3FFFFFFF;
+
+struct AttendArgs {
+  KvCacheArgs c;
+  KvRows q;
+  void* out;
+  float* lse;
+  const int32_t* ids;
+  float* parts;      // [2 * grid][rows][D + 2]: outputs, then maxima, then sums
+  int32_t* jobs;     // [grid][4]: entry, head, last CTA of a split item, or -1
+  uint32_t* status;
+  float scale_log2;
+  int32_t n, Hq, R;
+  int32_t qt, n_qt;  // queries of a tile, query tiles of a sequence
+  int32_t n_lists, k;
+  int32_t spt;       // blocks of a tile
+  int32_t fixed;     // tiles of every item over chosen blocks, else 0
+  bool bf16;
+};
+
+// Row r of partial `slot`: D outputs, then all rows' maxima and sums.
+__device__ __forceinline__ float* part_row(const AttendArgs& a, int slot, int rows, int r) {
+  return a.parts + (static_cast<int64_t>(slot) * rows + r) * (a.c.D + 2);
+}
+
+// What the query tile `e` sees: its rows' queries j0 .. j0 + nq - 1 (those that
+// exist), the position of the first and the last, and its tiles.
+struct Entry {
+  int32_t b, j0, nq, first_pos, last_pos, tiles;
+};
+__device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
+  Entry t;
+  t.b = e / a.n_qt;
+  t.j0 = (e - t.b * a.n_qt) * a.qt;
+  const Span s = span_of(a.c, t.b, a.n);
+  t.nq = min(t.j0 + a.qt, s.n_new) - t.j0;
+  t.last_pos = t.nq > 0 ? s.first + t.j0 + t.nq - 1 : -1;
+  t.first_pos = s.first + t.j0;  // may be negative: those rows see nothing
+  if (a.fixed > 0) {
+    t.tiles = a.fixed;
+  } else {
+    const int keys = min(t.last_pos + 1, a.c.max_blocks * a.c.block);
+    t.tiles = keys > 0 ? (keys - 1) / kKvTile + 1 : 1;
+  }
+  return t;
+}
+
+// A CTA's walk over its share of the tiles: the part [t, t + n) of item (e, h).
+struct Walk {
+  int32_t e, h, t;
+  int64_t left;
+};
+
+// ------------------------------------------------------------ tcgen05 pieces
+// D[tmem] (+)= A[smem] * B[smem]^T on e4m3 codes, issued by one thread.
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor: fp32 D (bits 4-5 = 1), e4m3 A and B (formats 0), A
+// MN-major when asked (bit 15), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, bool a_mn_major) {
+  return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+// Shared-memory descriptor of rows of ROW bytes (128 or 64) swizzled over
+// their own width, 8-row groups 8 * ROW bytes apart. K-major, the group stride
+// steps over rows; MN-major (rows run along K), it steps over 8 K. The leading
+// offset only matters for an MN-major tile wider than a row: rows of 64 bytes
+// then repeat at the next group (the output lanes 64-127 they give are not read).
+template <int ROW>
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
+  constexpr uint64_t swizzle = ROW == 128 ? 2 : 4;
+  constexpr uint64_t group = (8 * ROW) >> 4;
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (group << 16) | (group << 32) | (1ull << 46) |
+         (swizzle << 61);
+}
+
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzled(uint32_t off) {
+  return ROW == 128 ? off ^ ((off >> 3) & 0x70u) : off ^ ((off >> 3) & 0x30u);
+}
+
+// Each thread reads NC consecutive columns of its TMEM lane.
+template <int NC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[NC]);
+template <>
+__device__ __forceinline__ void tmem_ld_cols<4>(uint32_t taddr, float (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_ld_cols<8>(uint32_t taddr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_ld_cols<16>(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_ld_cols<32>(uint32_t taddr, float (&r)[32]) {
+  uint32_t u[32];
+  tmem_ld_32cols(taddr, u);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
+
+// ------------------------------------------------------------- small pieces
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// bar_sync that also tells every thread whether any of them passed true.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {  // NaN counts as nothing
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void store_u8(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+// Waits for a phase of `bar`, but at most kWaitTimeoutNs; the first wait of a
+// CTA that runs out sets its stop flag (and the device's status word), and
+// from then on every wait of the CTA returns at once. Loop counts never hang
+// on what a failed wait would have guarded, so all warps still reach the end.
+__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile uint32_t* stop,
+                                             uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*stop) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      *stop = 1;
+      atomicOr(status, kErrKvWaitTimeout);
+      return false;
+    }
+  }
+}
+
+// ------------------------------------------------------------ configuration
+template <int D_, int RT_>
+struct AttendCfg {
+  static constexpr int D = D_;
+  static constexpr int RT = RT_;                            // rows
+  static constexpr int N = (3 * RT + 15) / 16 * 16;         // columns: three terms of each row
+  static constexpr int W = RT >= 32 ? 2 : 3;                // warpgroups
+  static constexpr int kThreads = W * 128 + 64;
+  static constexpr int kStageBytes = 2 * kKvTile * D;       // K then V
+  // A stage serves one warpgroup only: a parity wait may not run two phases
+  // ahead, and only a stage's own last user knows that its phase has passed.
+  static constexpr int kStages = (RT >= 32 ? 4 : 6) * (128 / D);
+  static_assert(kStages % W == 0, "a stage serves one warpgroup");
+  static constexpr int kQBytes = N * D;                     // one of two buffers
+  static constexpr int kPBytes = N * kKvTile;               // one of W
+  static constexpr int kMergeBytes = (W - 1) * RT * D * 4;  // lies over the P buffers
+  static_assert(kMergeBytes <= W * kPBytes, "merge buffer");
+  static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
+  static_assert(2 * N * W <= 512, "TMEM");
+};
+
+struct StageMeta {
+  int32_t base[kKvMaxSlots];  // position of the slot's first token, kKvNoToken if none
+  float ks[kKvMaxSlots];      // key scale
+  float vs[kKvMaxSlots];      // 256 * value scale / the tile's largest
+  float vfac;                 // that largest / 256
+  int32_t any;                // some slot holds tokens
+};
+
+template <int RT>
+struct ItemInfo {
+  int32_t row_pos[RT];  // last position the row sees; -1: nothing
+  float row_mul[RT];    // query scale * softmax scale * log2(e)
+  int32_t tiles;        // of this CTA's part; 0 ends the walk
+  int32_t lo_pos, hi_pos;  // smallest and largest row_pos of rows that see anything
+  int32_t rows, b, j0, h;
+  int32_t slot;         // partial result to write, -1: the whole item
+};
+
+template <class C>
+struct AttendShared {
+  ItemInfo<C::RT> item[2];
+  StageMeta meta[C::kStages];
+  alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
+  float ml[2][C::W][C::RT];      // the warpgroups' maxima and sums
+  int32_t poison[128];           // first position whose value code is NaN, per dimension
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_bar[C::W], o_bar[C::W];
+  uint64_t scan[C::kThreads / 32 + 1];
+  Walk start;
+  uint32_t tmem;
+  uint32_t stop;
+};
+
+// ------------------------------------------------------------------ producer
+template <class C>
+__device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                               AttendShared<C>& s, uint8_t* ring, Walk w) {
+  const int lane = threadIdx.x % 32;
+  const int spt = a.spt, per_batch = 32 / spt;
+  uint32_t g = 0;  // tiles issued by this CTA
+  bool ok = true;
+  Entry en{};
+  int en_of = -1;
+  while (w.left > 0 && ok) {
+    if (en_of != w.e) {
+      en = entry_of(a, w.e);
+      en_of = w.e;
+    }
+    const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
+    const int cap = a.c.max_blocks * a.c.block;
+    bool bad = en.last_pos >= cap;  // longer than its page table
+    const int keys = min(en.last_pos + 1, cap);
+    const int32_t* list = nullptr;
+    if (a.ids)
+      list = a.ids + ((static_cast<int64_t>(en.b) * a.n_lists + (a.n_lists > 1 ? w.h : 0)) * a.n + en.j0) * a.k;
+    const int32_t* table = a.c.page_table + static_cast<int64_t>(en.b) * a.c.max_blocks;
+    for (int t0 = 0; t0 < part && ok; t0 += per_batch) {
+      // One block of the next 32 / spt tiles per lane.
+      const int slot = (w.t + t0) * spt + lane;
+      const bool in_part = t0 + lane / spt < part;
+      int blk = in_part ? slot : -1;
+      if (list) blk = in_part && slot < a.k ? __ldg(list + slot) : -1;
+      if (list && blk >= a.c.max_blocks) {
+        bad = true;
+        blk = -1;
+      }
+      if (blk >= 0 && static_cast<int64_t>(blk) * a.c.block >= keys) blk = -1;
+      int page = blk >= 0 ? __ldg(table + blk) : -1;
+      if (blk >= 0 && (page < 0 || page >= a.c.n_pages)) {
+        bad = true;
+        blk = page = -1;
+      }
+      float ks = 0.0f, vs = 0.0f;
+      if (page >= 0) {
+        ks = __ldg(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+        vs = __ldg(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+      }
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, page >= 0);
+      const int tiles = min(per_batch, part - t0);
+      for (int i = 0; i < tiles; ++i, ++g) {
+        const int st = g % C::kStages;
+        if (g >= C::kStages)
+          ok = wait_or_stop(&s.empty[st], ((g / C::kStages) & 1) ^ 1, &s.stop, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const bool any = ((valid >> (i * spt)) & ((1u << spt) - 1)) != 0;
+        const bool mine = lane / spt == i;
+        if (any) {
+          if (lane == 0) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
+          __syncwarp();
+          if (mine) {
+            // A slot without a block reads past the last page: zeros.
+            uint8_t* const k_at = ring + st * C::kStageBytes + (lane % spt) * a.c.block * C::D;
+            const int y = w.h * a.c.block, z = page >= 0 ? page : a.c.n_pages;
+            tma_load_3d(k_at, tm_k, 0, y, z, &s.full[st]);
+            tma_load_3d(k_at + kKvTile * C::D, tm_v, 0, y, z, &s.full[st]);
+          }
+        } else if (lane == 0) {
+          mbar_arrive(&s.full[st]);
+        }
+        float vmax = mine ? vs : 0.0f;
+        for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
+        StageMeta& m = s.meta[st];
+        if (mine) {
+          m.base[lane % spt] = page >= 0 ? blk * a.c.block : kKvNoToken;
+          m.ks[lane % spt] = ks;
+          m.vs[lane % spt] = vmax > 0.0f ? 256.0f * __fdiv_rn(vs, vmax) : 0.0f;
+          if (lane % spt == 0) {
+            m.vfac = vmax * (1.0f / 256.0f);
+            m.any = any;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[st]);
+      }
+    }
+    if (bad && (a.ids || lane == 0)) atomicOr(a.status, kErrCacheIndex);
+    w.left -= part;
+    w.t += part;
+    if (w.t >= en.tiles) {
+      w.t = 0;
+      if (++w.h == a.c.Hkv) {
+        w.h = 0;
+        ++w.e;
+      }
+    }
+  }
+  if (!ok) {  // let the copies in flight land before the CTA gives its memory back
+    const uint32_t n = min(g, static_cast<uint32_t>(C::kStages));
+    for (uint32_t i = g - n; i < g; ++i)
+      mbar_wait_bounded(&s.full[i % C::kStages], (i / C::kStages) & 1, 100000000ull);
+  }
+}
+
+// --------------------------------------------------------- the query's terms
+template <class C>
+__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, Walk w, int64_t lo,
+                               int64_t total, int grid) {
+  constexpr int kPer = C::D / 32;  // elements of a lane
+  const int lane = threadIdx.x % 32;
+  int64_t at = lo;  // tiles before this item
+  uint32_t it = 0;
+  bool ok = true;
+  Entry en{};
+  int en_of = -1;
+  while (ok) {
+    const int buf = it & 1;
+    if (it >= 2) ok = wait_or_stop(&s.q_empty[buf], ((it >> 1) & 1) ^ 1, &s.stop, a.status);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) break;
+    ItemInfo<C::RT>& info = s.item[buf];
+    if (w.left <= 0) {
+      if (lane == 0) {
+        info.tiles = 0;
+        mbar_arrive(&s.q_full[buf]);
+      }
+      break;
+    }
+    if (en_of != w.e) {
+      en = entry_of(a, w.e);
+      en_of = w.e;
+    }
+    const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
+    const int rows = a.qt * a.R;
+    uint8_t* const dst = q_smem + buf * C::kQBytes;
+    for (int r0 = 0; r0 < C::RT; r0 += 4) {
+      float x[4][kPer];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i, j = r / a.R;
+        const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[i][e] = 0.0f;
+        if (there) {
+          const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
+                                      static_cast<int64_t>(en.j0 + j) * a.q.sn +
+                                      static_cast<int64_t>(w.h * a.R + r % a.R) * a.q.sh + lane * kPer;
+          uint32_t u[kPer / 2];
+          if (kPer == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            u[0] = v.x;
+            u[kPer / 2 - 1] = v.y;
+          } else {
+            u[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          }
+#pragma unroll
+          for (int e = 0; e < kPer / 2; ++e) {
+            if (a.bf16) {
+              x[i][2 * e] = __uint_as_float(u[e] << 16);
+              x[i][2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+            } else {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+              x[i][2 * e] = f.x;
+              x[i][2 * e + 1] = f.y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i, j = r / a.R;
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) m = fmaxf(m, fabsf(x[i][e]));
+        const float t = pow2_scale(
+            __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(t));
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          x[i][e] *= inv;
+          if (isinf(x[i][e])) x[i][e] = __int_as_float(0x7FC00000);
+        }
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          uint32_t code[kPer / 2];
+#pragma unroll
+          for (int e = 0; e < kPer / 2; ++e) {
+            code[e] = e4m3x2(x[i][2 * e], x[i][2 * e + 1]);
+            const float2 back = e4m3x2_to_float2(code[e]);
+            x[i][2 * e] -= back.x;
+            x[i][2 * e + 1] -= back.y;
+          }
+          uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
+          if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
+          else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
+        }
+        if (lane == 0) {
+          const bool there = j < en.nq && en.first_pos + j >= 0;
+          info.row_pos[r] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
+          info.row_mul[r] = t * a.scale_log2;
+        }
+      }
+    }
+    if (lane == 0) {
+      info.tiles = part;
+      info.lo_pos = en.last_pos < 0 ? -1 : max(en.first_pos, 0);
+      info.hi_pos = en.last_pos;
+      info.rows = rows;
+      info.b = en.b;
+      info.j0 = en.j0;
+      info.h = w.h;
+      const bool begins = w.t == 0, ends = w.t + part == en.tiles;
+      info.slot = begins && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
+      if (begins && !ends) {
+        const int64_t last = at + en.tiles - 1;  // the item's last tile, and the CTA that has it
+        int32_t* const job = a.jobs + 4 * blockIdx.x;
+        job[0] = w.e;
+        job[1] = w.h;
+        job[2] = static_cast<int32_t>(((last + 1) * grid - 1) / total);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full[buf]);
+    ++it;
+    at += w.t + part;
+    w.left -= part;
+    w.t += part;
+    if (w.t >= en.tiles) {
+      w.t = 0;
+      if (++w.h == a.c.Hkv) {
+        w.h = 0;
+        ++w.e;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------- the warpgroups
+// A value row whose token no row of the tile sees is zeroed, so that 0 * code
+// stays 0 whatever stands there. One that some rows see has its NaN codes
+// zeroed and remembered: the rows that see them get NaN at the end.
+template <int D>
+__device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos, bool unseen, int32_t* poison) {
+  uint4* const row = reinterpret_cast<uint4*>(v_row_base + t * D);
+  for (int i = 0; i < D / 16; ++i) {
+    if (unseen) {
+      row[i] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 u = row[i];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t hit = 0;
+    for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    if (!hit) continue;
+    uint8_t* const bytes = reinterpret_cast<uint8_t*>(row + i);
+    const uint32_t chunk = swizzled<D>(t * D + i * 16) - t * D;  // the swizzle is its own inverse
+    for (int k = 0; k < 16; ++k)
+      if ((bytes[k] & 0x7F) == 0x7F) {
+        bytes[k] = 0;
+        atomicMin(&poison[chunk + k], pos);
+      }
+  }
+}
+
+template <class C>
+__device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
+                               uint8_t* p_smem) {
+  constexpr int RT = C::RT, N = C::N, W = C::W, D = C::D;
+  constexpr int kAll = W * 128;
+  const int wg = threadIdx.x / 128, t = threadIdx.x % 128, warp = t / 32, lane = t % 32;
+  const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t tm_s = s.tmem + wg * 2 * N, tm_o = tm_s + N;
+  uint8_t* const p_buf = p_smem + wg * C::kPBytes;
+  const uint32_t p_addr = smem_u32(p_buf);
+  const int my_slot = t / a.c.block, my_off = t % a.c.block;
+  uint32_t g0 = 0;      // tiles of the CTA before this item
+  uint32_t phase = 0;   // of this warpgroup's two product barriers
+  bool bad = false;
+  const float kNegInf = -INFINITY;
+
+  for (uint32_t it = 0;; ++it) {
+    const int buf = it & 1;
+    if (!wait_or_stop(&s.q_full[buf], (it >> 1) & 1, &s.stop, a.status)) bad = true;
+    if (threadIdx.x < 128) s.poison[threadIdx.x] = kKvNoToken;
+    if (bar_any(8, kAll, bad)) break;
+    const ItemInfo<RT>& info = s.item[buf];
+    const int tiles = info.tiles;
+    if (tiles == 0) break;
+    const int lo_pos = info.lo_pos, hi_pos = info.hi_pos;
+
+    float o[RT], l[RT], m[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      o[r] = 0.0f;
+      l[r] = 0.0f;
+      m[r] = kNegInf;
+    }
+
+    for (int i = (W - g0 % W + wg) % W; i < tiles; i += W) {
+      const uint32_t g = g0 + i;
+      const int st = g % C::kStages;
+      if (!wait_or_stop(&s.full[st], (g / C::kStages) & 1, &s.stop, a.status)) bad = true;
+      const StageMeta& meta = s.meta[st];
+      const int any = bad ? 0 : meta.any;
+      uint8_t* const k_tile = ring + st * C::kStageBytes;
+      if (!bar_any(1 + wg, 128, any != 0)) {  // no block in this tile (or a wait ran out)
+        if (t == 0) mbar_arrive(&s.empty[st]);
+        continue;
+      }
+      if (t == 0) {
+        tc_fence_after_sync();
+        const uint32_t ka = smem_u32(k_tile), qa = smem_u32(q_smem + buf * C::kQBytes);
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks)
+          mma_f8_ss(tm_s, smem_desc_rows<D>(ka + ks * 32), smem_desc_rows<D>(qa + ks * 32), idesc_f8(N, false),
+                    ks > 0);
+        mma_commit(&s.s_bar[wg]);
+      }
+      const int pos = meta.base[my_slot] + my_off;
+      const float k_mul = meta.ks[my_slot], v_mul = meta.vs[my_slot], v_fac = meta.vfac;
+      if (pos > lo_pos) {
+        const bool unseen = pos > hi_pos;
+        clean_value_row<D>(k_tile + kKvTile * D, t, pos, unseen, s.poison);
+      }
+      if (!wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
+      __syncwarp();
+      tc_fence_after_sync();
+      float x[RT];
+      {
+        float x1[RT], x2[RT];
+        tmem_ld_cols<RT>(tm_s + lane_addr, x);
+        tmem_ld_cols<RT>(tm_s + lane_addr + RT, x1);
+        tmem_ld_cols<RT>(tm_s + lane_addr + 2 * RT, x2);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < RT; ++r) x[r] = (x[r] + (x1[r] + x2[r])) * k_mul * info.row_mul[r];
+      }
+      if (pos > lo_pos) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (pos > info.row_pos[r]) x[r] = kNegInf;
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float v = warp_max(x[r]);
+        if (lane == r) top = v;
+      }
+      if (lane < RT) s.red[wg][lane][warp] = top;
+      bar_sync(1 + wg, 128);
+      bool grown = false;
+      float alpha[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float4 v = *reinterpret_cast<const float4*>(s.red[wg][r]);
+        const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+        const float mn = fmaxf(m[r], mx);
+        grown |= mn > m[r];
+        alpha[r] = m[r];
+        m[r] = mn;
+      }
+      if (grown) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          alpha[r] = m[r] == kNegInf ? 1.0f : exp2_approx(alpha[r] - m[r]);
+          l[r] *= alpha[r];
+          o[r] *= alpha[r];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; r += 2) {
+        float y[2];
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const float base = m[r + i2] == kNegInf ? 0.0f : m[r + i2];
+          const float p = exp2_approx(x[r + i2] - base);
+          l[r + i2] += p;
+          y[i2] = p * v_mul;
+        }
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          const uint32_t code = e4m3x2(y[0], y[1]);
+          const int row = term * RT + r;
+          store_u8(p_addr + row * 128 + (((t >> 4) ^ (row & 7)) << 4) + (t & 15), code);
+          store_u8(p_addr + (row + 1) * 128 + (((t >> 4) ^ ((row + 1) & 7)) << 4) + (t & 15), code >> 8);
+          if (term < 2) {
+            const float2 back = e4m3x2_to_float2(code);
+            y[0] -= back.x;
+            y[1] -= back.y;
+          }
+        }
+      }
+      tc_fence_before_sync();
+      fence_proxy_async_smem();
+      bar_sync(1 + wg, 128);
+      if (t == 0) {
+        tc_fence_after_sync();
+        const uint32_t va = smem_u32(k_tile + kKvTile * D);
+#pragma unroll
+        for (int ks = 0; ks < kKvTile / 32; ++ks)
+          mma_f8_ss(tm_o, smem_desc_rows<D>(va + ks * 32 * D), smem_desc_rows<128>(p_addr + ks * 32),
+                    idesc_f8(N, true), ks > 0);
+        mma_commit(&s.o_bar[wg]);
+        mma_commit(&s.empty[st]);
+      }
+      if (!wait_or_stop(&s.o_bar[wg], phase, &s.stop, a.status)) bad = true;
+      phase ^= 1;
+      __syncwarp();
+      tc_fence_after_sync();
+      {
+        float x1[RT], x2[RT];
+        tmem_ld_cols<RT>(tm_o + lane_addr, x);
+        tmem_ld_cols<RT>(tm_o + lane_addr + RT, x1);
+        tmem_ld_cols<RT>(tm_o + lane_addr + 2 * RT, x2);
+        tmem_ld_wait();
+        tc_fence_before_sync();
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r] += (x[r] + (x1[r] + x2[r])) * v_fac;
+      }
+    }
+    g0 += tiles;
+
+    // Join the warpgroups: sums over the tokens, then the outputs, in order.
+    float mine = 0.0f;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
+      if (lane == r) mine = l[r];
+    }
+    if (lane < RT) s.red[wg][lane][warp] = mine;
+    bar_sync(1 + wg, 128);
+    if (t < RT) {
+      const float4 v = *reinterpret_cast<const float4*>(s.red[wg][t]);
+      s.ml[1][wg][t] = (v.x + v.y) + (v.z + v.w);
+    }
+    if (t == 0) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s.ml[0][wg][r] = m[r];
+    }
+    bar_sync(8, kAll);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float mx = s.ml[0][0][r];
+#pragma unroll
+      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][r]);
+      o[r] *= m[r] == kNegInf ? 0.0f : exp2_approx(m[r] - mx);
+      m[r] = mx;
+    }
+    float* const merge = reinterpret_cast<float*>(p_smem);
+    if (wg > 0 && t < D) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) merge[((wg - 1) * RT + r) * D + t] = o[r];
+    }
+    bar_sync(8, kAll);
+    if (wg == 0 && t < D) {
+#pragma unroll
+      for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r] += merge[(w * RT + r) * D + t];
+    }
+    if (wg == 0) {
+      const int rows = info.rows, first_poison = t < D ? s.poison[t] : kKvNoToken;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (r >= rows) break;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float mw = s.ml[0][w][r];
+          sum += mw == kNegInf && !(s.ml[1][w][r] != s.ml[1][w][r])
+                     ? 0.0f
+                     : s.ml[1][w][r] * (mw == kNegInf ? 1.0f : exp2_approx(mw - m[r]));
+        }
+        const int row_pos = info.row_pos[r];
+        float v = o[r];
+        if (row_pos >= first_poison) v = __int_as_float(0x7FC00000);
+        if (info.slot >= 0) {
+          float* const part = part_row(a, info.slot, rows, r);
+          if (t < D) part[t] = v;
+          if (t == 0) {
+            part[D] = row_pos < 0 ? kNegInf : m[r];
+            part[D + 1] = row_pos < 0 ? 0.0f : sum;
+          }
+        } else {
+          const int j = info.j0 + r / a.R;
+          if (j >= a.n) break;
+          const bool none = row_pos < 0 || sum == 0.0f;
+          const int64_t at = (static_cast<int64_t>(info.b) * a.n + j) * a.Hq + info.h * a.R + r % a.R;
+          if (t < D) {
+            v = none ? 0.0f : __fdividef(v, sum);
+            if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
+            else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
+          }
+          if (a.lse && t == 0)
+            a.lse[at] = none ? kNegInf : (m[r] == kNegInf ? sum : m[r] * 0.6931471805599453f + logf(sum));
+        }
+      }
+    }
+    bar_sync(8, kAll);
+    if (threadIdx.x == 0) mbar_arrive(&s.q_empty[buf]);
+  }
+}
+
+// -------------------------------------------------------------- the kernel
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    kv_attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ AttendArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* const ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* const q_smem = ring + C::kStages * C::kStageBytes;
+  uint8_t* const p_smem = q_smem + 2 * C::kQBytes;
+  AttendShared<C>& s = *reinterpret_cast<AttendShared<C>*>(p_smem + C::W * C::kPBytes);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&s.full[i], 2);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_empty[i], 1);
+    }
+    for (int i = 0; i < C::W; ++i) {
+      mbar_init(&s.s_bar[i], 1);
+      mbar_init(&s.o_bar[i], 1);
+    }
+    s.stop = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    a.jobs[4 * blockIdx.x] = -1;
+  }
+  if (warp == 0) {
+    tmem_alloc(&s.tmem, C::kTmemCols);
+    tmem_relinquish();
+  }
+
+  // This CTA's share of all tiles: [total c / grid, total (c + 1) / grid).
+  const int entries = a.c.B * a.n_qt;
+  const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
+  const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
+  uint64_t sum = 0;
+  if (a.fixed > 0) {
+    sum = static_cast<uint64_t>(e1 - e0) * a.fixed;
+  } else {
+    for (int64_t e = e0; e < e1; ++e) sum += entry_of(a, static_cast<int>(e)).tiles;
+  }
+  uint64_t before = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+    if (lane >= d) before += v;
+  }
+  if (lane == 31) s.scan[warp] = before;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  uint64_t all = 0;
+  before -= sum;
+#pragma unroll 1
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w < warp) before += s.scan[w];
+    all += s.scan[w];
+  }
+  const int64_t total = static_cast<int64_t>(all) * a.c.Hkv;
+  const int grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  const int cta = blockIdx.x;
+  const int64_t lo = cta < grid ? total * cta / grid : 0, hi = cta < grid ? total * (cta + 1) / grid : 0;
+  if (hi > lo) {
+    uint64_t at = before * a.c.Hkv;
+    if (static_cast<int64_t>(at) <= lo && lo < static_cast<int64_t>((before + sum) * a.c.Hkv)) {
+      int64_t e = e0;
+      int tiles = a.fixed;
+      if (a.fixed > 0) {
+        const int64_t skip = (lo - static_cast<int64_t>(at)) / (static_cast<int64_t>(a.fixed) * a.c.Hkv);
+        e += skip;
+        at += static_cast<uint64_t>(skip) * a.fixed * a.c.Hkv;
+      } else {
+        for (;; ++e) {
+          tiles = entry_of(a, static_cast<int>(e)).tiles;
+          const uint64_t next = at + static_cast<uint64_t>(tiles) * a.c.Hkv;
+          if (lo < static_cast<int64_t>(next)) break;
+          at = next;
+        }
+      }
+      const int64_t off = lo - static_cast<int64_t>(at);
+      s.start.e = static_cast<int32_t>(e);
+      s.start.h = static_cast<int32_t>(off / tiles);
+      s.start.t = static_cast<int32_t>(off % tiles);
+      s.start.left = hi - lo;
+    }
+    __syncthreads();
+    if (warp < C::W * 4) {
+      attend_consume<C>(a, s, ring, q_smem, p_smem);
+    } else if (warp == C::W * 4) {
+      attend_produce<C>(a, &tm_k, &tm_v, s, ring, s.start);
+    } else {
+      attend_queries<C>(a, s, q_smem, s.start, lo - s.start.t, total, grid);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(s.tmem, C::kTmemCols);
+}
+
+// Launch with the given tensor maps; grid CTAs.
+template <int D, int RT>
+cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid, bool init,
+                        cudaStream_t stream) {
+  using C = AttendCfg<D, RT>;
+  constexpr int smem = 1024 + C::kStages * C::kStageBytes + 2 * C::kQBytes + C::W * C::kPBytes +
+                       static_cast<int>(sizeof(AttendShared<C>));
+  static_assert(smem <= 227 * 1024, "shared memory");
+  if (init) return cudaFuncSetAttribute(kv_attend_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  kv_attend_kernel<C><<<grid, C::kThreads, smem, stream>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+
+// All row counts of one head size (kv_attend_d64.cu, kv_attend_d128.cu).
+template <int D>
+cudaError_t attend_rows(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
+                        bool init, cudaStream_t stream) {
+  switch (rt) {
+    case 4: return attend_form<D, 4>(tk, tv, a, grid, init, stream);
+    case 8: return attend_form<D, 8>(tk, tv, a, grid, init, stream);
+    case 16: return attend_form<D, 16>(tk, tv, a, grid, init, stream);
+    default: return attend_form<D, 32>(tk, tv, a, grid, init, stream);
+  }
+}
+cudaError_t attend_rows_d64(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
+                            bool init, cudaStream_t stream);
+cudaError_t attend_rows_d128(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
+                             bool init, cudaStream_t stream);
+
+}  // namespace qsa

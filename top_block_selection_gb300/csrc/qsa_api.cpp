@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cuda_runtime.h>
 
+#include "kv_internal.h"
 #include "qsa_internal.h"
 
 namespace qsa {
@@ -500,6 +501,132 @@ qsa_status qsa_split_reduce_static(const float* partial_max, const float* partia
   return from_cuda(qsa::launch_split_reduce(p, *dev, s));
 }
 
+// ------------------------------------------------- the paged 8-bit cache
+// Sizes of the cache and the batch; nothing is dereferenced but *c.
+static qsa_status check_cache_sizes(const qsa_kv_cache* c, int32_t n) {
+  if (!c) return QSA_ERR_INVALID_ARG;
+  if (c->B < 0 || n < 0 || c->n_pages < 0 || c->max_blocks < 0 || c->Hkv < 1 || c->block < 1 || c->D < 1)
+    return QSA_ERR_INVALID_ARG;
+  if ((c->D != 64 && c->D != 128) ||
+      (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) || c->Hkv > 65535)
+    return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (static_cast<int64_t>(c->max_blocks) * c->block > (1 << 30) ||
+      static_cast<int64_t>(c->B) * n > 0x7FFFFFFFLL)
+    return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (c->page_stride < static_cast<int64_t>(c->Hkv) * c->block * c->D) return QSA_ERR_INVALID_ARG;
+  if (c->page_stride >= (1LL << 40)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (c->page_stride % 16 != 0) return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+
+static qsa_status check_cache_pointers(const qsa_kv_cache* c) {
+  if (!c->lens || (c->max_blocks > 0 && !c->page_table)) return QSA_ERR_INVALID_ARG;
+  if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->page_table, 4) || !aligned(c->lens, 4) || !aligned(c->n_new, 4))
+    return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+
+// Rows of 16-bit floats read by 16-byte loads.
+static qsa_status check_rows(const qsa_rows* r) {
+  if (!r || !r->data) return QSA_ERR_INVALID_ARG;
+  if (r->stride_b < 0 || r->stride_n < 0 || r->stride_h < 0) return QSA_ERR_INVALID_ARG;
+  if (!aligned(r->data, 16) || r->stride_b % 8 != 0 || r->stride_n % 8 != 0 || r->stride_h % 8 != 0)
+    return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+
+static qsa::KvCacheArgs cache_args(const qsa_kv_cache* c) {
+  return qsa::KvCacheArgs{c->k,     c->v,       c->k_scale,    c->v_scale, c->page_table, c->lens,
+                          c->n_new, c->page_stride, c->n_pages, c->max_blocks, c->B, c->Hkv,
+                          c->block, c->D};
+}
+
+static qsa::KvRows row_args(const qsa_rows* r) {
+  return r ? qsa::KvRows{r->data, r->stride_b, r->stride_n, r->stride_h} : qsa::KvRows{nullptr, 0, 0, 0};
+}
+
+qsa_status qsa_kv_append(const qsa_kv_cache* cache, const qsa_rows* k, const qsa_rows* v, const qsa_rows* q,
+                         int32_t n, int32_t Hq, qsa_dtype dtype, const float* cos, const float* sin,
+                         int32_t rot, int32_t max_pos, int32_t interleaved, void* q_out, uint16_t* kb,
+                         qsa_stream_t stream) {
+  qsa_status st = check_cache_sizes(cache, n);
+  if (st != QSA_OK) return st;
+  if (rot < 0 || max_pos < 0 || (q && Hq < 1)) return QSA_ERR_INVALID_ARG;
+  if (dtype != QSA_F16 && dtype != QSA_BF16) return QSA_ERR_INVALID_ARG;
+  if (rot % 16 != 0 || rot > cache->D) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  qsa::KvAppendProblem p{};
+  p.cache = cache_args(cache);
+  p.q = row_args(q);
+  p.n = n;
+  p.Hq = q ? Hq : 0;
+  if (cache->B == 0 || n == 0) return QSA_OK;
+  int64_t units = 0;
+  int32_t per_seq = 0;
+  if (qsa::kv_append_grid(p, &units, &per_seq) > 0x7FFFFFFFLL) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if ((st = check_rows(k)) != QSA_OK || (st = check_rows(v)) != QSA_OK) return st;
+  if (q && ((st = check_rows(q)) != QSA_OK)) return st;
+  if ((q != nullptr) != (q_out != nullptr)) return QSA_ERR_INVALID_ARG;
+  if (rot > 0 && (!cos || !sin)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(kb, 2) || !aligned(cos, 16) || !aligned(sin, 16)) return QSA_ERR_MISALIGNED;
+  p.k = row_args(k);
+  p.v = row_args(v);
+  p.rot = rot;
+  p.max_pos = max_pos;
+  p.bf16 = dtype == QSA_BF16;
+  p.interleaved = interleaved != 0;
+  p.cos = cos;
+  p.sin = sin;
+  p.q_out = q_out;
+  p.kb = kb;
+  const DeviceInfo* dev = nullptr;
+  if ((st = device_or_error(&dev)) != QSA_OK) return st;
+  return from_cuda(qsa::launch_kv_append(p, *dev, as_cuda(stream)));
+}
+
+size_t qsa_kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  return qsa::kv_attend_workspace_bytes(B, n, Hq, Hkv, D);
+}
+
+qsa_status qsa_kv_attend(const qsa_kv_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                         float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, qsa_stream_t stream) {
+  qsa_status st = check_cache_sizes(cache, n);
+  if (st != QSA_OK) return st;
+  if (Hq < 1 || (dtype != QSA_F16 && dtype != QSA_BF16)) return QSA_ERR_INVALID_ARG;
+  if (Hq % cache->Hkv != 0) return QSA_ERR_INVALID_ARG;
+  if (ids && (k < 1 || (n_lists != 1 && n_lists != cache->Hkv))) return QSA_ERR_INVALID_ARG;
+  if (Hq / cache->Hkv > qsa::kKvMaxGroup || (ids && k > (1 << 20))) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (cache->B == 0 || n == 0) return QSA_OK;
+  if (!(scale - scale == 0.0f)) return QSA_ERR_INVALID_ARG;
+  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
+  if ((st = check_rows(q)) != QSA_OK) return st;
+  if (!out || !workspace ||
+      workspace_bytes < qsa::kv_attend_workspace_bytes(cache->B, n, Hq, cache->Hkv, cache->D))
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ids, 4) || !aligned(workspace, 16))
+    return QSA_ERR_MISALIGNED;
+  qsa::KvAttendProblem p{};
+  p.cache = cache_args(cache);
+  p.q = row_args(q);
+  p.n = n;
+  p.Hq = Hq;
+  p.bf16 = dtype == QSA_BF16;
+  p.scale = scale;
+  p.ids = ids;
+  p.n_lists = ids ? n_lists : 1;
+  p.k = ids ? k : 0;
+  p.out = out;
+  p.lse = lse;
+  p.workspace = workspace;
+  const DeviceInfo* dev = nullptr;
+  if ((st = device_or_error(&dev)) != QSA_OK) return st;
+  return from_cuda(qsa::launch_kv_attend(p, *dev, as_cuda(stream)));
+}
+
 qsa_status qsa_selftest_bounded_wait(uint64_t timeout_ns, qsa_stream_t stream) {
   if (timeout_ns == 0 || timeout_ns > 1000000000ull) return QSA_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
@@ -523,6 +650,7 @@ qsa_status qsa_device_status(int clear, uint32_t* bits, qsa_stream_t stream) {
         (e = cudaDeviceSynchronize()) != cudaSuccess)
       return cuda_fail(e);
   }
+  if (v == qsa::kKvIndexBit) return QSA_ERR_INVALID_ARG;
   return v == 0 ? QSA_OK : QSA_ERR_TIMEOUT;
 }
 

@@ -14,6 +14,8 @@ enum : uint32_t {
   kErrScoreMmaTimeout = 1u << 1,   // tcgen05.commit never arrived
   kErrFusedWaitTimeout = 1u << 2,  // a cross-CTA dependency never completed
   kErrSplitLoadTimeout = 1u << 3,  // a split-reduce bulk copy never arrived
+  kErrKvWaitTimeout = 1u << 4,     // a wait of the cache attention ran out
+  kErrCacheIndex = 1u << 5,        // a page, block or position outside the cache (not a timeout)
   kErrSelftestTimeout = 1u << 31,  // the bounded-wait self-test ran out (expected)
 };
 
