@@ -124,14 +124,14 @@ def seen_tokens(cache, b, j, n, ids=None):
     return [(int(cache["table"][b, i]), o, i * block + o) for i in blocks for o in range(block) if i * block + o <= p]
 
 
-def attend_row(cache, q, b, j, n, h, scale, ids=None):
+def attend_row(cache, q, b, j, n, h, scale, ids=None, terms=3):
     """(out [D], lse, bound [D]) in float64 of one query row on KV head h.
 
     `bound` is the first-order error of the GPU path before the rounding of
-    its result, from its number formats: a probability in three e4m3 terms is
-    off by at most 2^-14 of itself or 2^-18 of the largest value scale among
-    the tokens over the row's maximum; a score (fp32 sums of exact products,
-    three terms of a query exact above 2^-18 of the row's largest element)
+    its result, from its number formats: a probability in e4m3 terms is off by
+    at most 2^-12 (three terms) or 2^-9 (two) of itself, or 2^-17 of the largest
+    value scale among the tokens over the row's maximum; a score (fp32 sums of
+    exact products, a query's terms exact above 2^-18 of the row's largest)
     by (D + 8) 2^-23 sum|q k| + 2^-18 max|q| sum|k|; exp2 and the scaling of
     its argument by 2^-21 (1 + |x|)."""
     seen = seen_tokens(cache, b, j, n, ids)
@@ -151,13 +151,13 @@ def attend_row(cache, q, b, j, n, h, scale, ids=None):
     out = p @ vv / total
     dx = abs(scale) * ((D + 8) * 2.0 ** -23 * (np.abs(kk) @ np.abs(q))
                        + 2.0 ** -18 * np.abs(q).max() * np.abs(kk).sum(1)) + 2.0 ** -21 * (1 + np.abs(x - m) + np.abs(x))
-    rel = 2.0 ** -14 + 2 * dx
+    rel = (2.0 ** -12 if terms == 3 else 2.0 ** -9) + 2 * dx
     bound = ((p * rel)[:, None] * np.abs(vv)).sum(0) / total + (p * 2 * dx).sum() / total * np.abs(out) \
-        + 2.0 ** -18 * vs.max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
+        + 2.0 ** -17 * vs.max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
     return out, m + np.log(total), bound
 
 
-def attend(cache, q, scale, ids=None):
+def attend(cache, q, scale, ids=None, terms=3):
     """q [B, n, Hq, D] -> (out, lse, bound); ids [B, lists, n, k] or None."""
     B, n, Hq, D = q.shape
     Hkv = cache["k"].shape[1]
@@ -168,5 +168,6 @@ def attend(cache, q, scale, ids=None):
             for hq in range(Hq):
                 h = hq // R
                 row = None if ids is None else ids[b, h if ids.shape[1] > 1 else 0, j]
-                out[b, j, hq], lse[b, j, hq], bound[b, j, hq] = attend_row(cache, q[b, j, hq], b, j, n, h, scale, row)
+                out[b, j, hq], lse[b, j, hq], bound[b, j, hq] = attend_row(cache, q[b, j, hq], b, j, n, h, scale, row,
+                                                                               terms)
     return out, lse, bound

@@ -193,7 +193,7 @@ def check_attend(tbs, c, n, Hq, dtype, ids=None, scale=None, seed=0, amp=1.0, ro
         rows(q)
     scale = D ** -0.5 if scale is None else scale
     with np.errstate(invalid="ignore"):
-        want, wlse, bound = ko.attend(c, q, scale, ids)
+        want, wlse, bound = ko.attend(c, q, scale, ids, terms=3 if dtype == "f16" else 2)
     args, nn = on_gpu(c)
     lse = torch.full(q.shape[:3], 7.0, dtype=torch.float32, device="cuda")
     out = tbs.qsa_kv_attend(dev(q, dtype), *args, ids=None if ids is None else dev(ids), scale=scale, n_new=nn, lse=lse)

@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
   m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
   for (int i = tid; i < parts; i += kCombineThreads) {
     const float* const p = part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r);
-    // A part without a maximum saw nothing (sum 0) or only NaN scores (sum NaN).
-    const float f = p[D] == -INFINITY ? 1.0f : exp2_approx(p[D] - m);
+    const float f = exp2_approx(p[D] - m);
     s_f[i] = f;
     l += p[D + 1] * f;
   }
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     else static_cast<__half*>(a.out)[at * D + tid] = __float2half_rn(v);
   }
   if (a.lse && tid == 0)
-    a.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * 0.6931471805599453f + logf(l));
+    a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 // Rows of the instantiation for `rows` of them.
@@ -82,11 +81,11 @@ size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, 
 cudaError_t init_kv_attend_kernels(const DeviceInfo&) {
   const CUtensorMap none{};
   const AttendArgs a{};
-  for (int rt = 4; rt <= 32; rt *= 2) {
-    cudaError_t e = attend_rows_d64(rt, none, none, a, 0, true, nullptr);
-    if (e == cudaSuccess) e = attend_rows_d128(rt, none, none, a, 0, true, nullptr);
-    if (e != cudaSuccess) return e;
-  }
+  for (const AttendLaunch form : {attend_d64_t2, attend_d64_t3, attend_d128_t2, attend_d128_t3})
+    for (int rt = 4; rt <= 32; rt *= 2) {
+      const cudaError_t e = form(rt, none, none, a, 0, true, nullptr);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 
@@ -119,8 +118,9 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   CUtensorMap tk, tv;
   if (!encode_cache_map(&tk, p.cache.k, p.cache) || !encode_cache_map(&tv, p.cache.v, p.cache))
     return cudaErrorInvalidValue;
-  cudaError_t e = p.cache.D == 64 ? attend_rows_d64(rt, tk, tv, a, grid, false, stream)
-                                  : attend_rows_d128(rt, tk, tv, a, grid, false, stream);
+  const AttendLaunch form = p.cache.D == 64 ? (p.bf16 ? attend_d64_t2 : attend_d64_t3)
+                                            : (p.bf16 ? attend_d128_t2 : attend_d128_t3);
+  cudaError_t e = form(rt, tk, tv, a, grid, false, stream);
   if (e != cudaSuccess) return e;
   plan_add("kv_attend_kernel");
   e = launch_pdl(kv_combine_kernel, dim3(grid, a.qt * a.R), dim3(kCombineThreads), 0, stream, a);

@@ -1,0 +1,10 @@
+// kv_attend_d64_t3.cu - the cache attention for heads of 64 dimensions in
+// 3 terms (fp16 calls).
+#include "kv_attend_kernel.cuh"
+
+namespace qsa {
+cudaError_t attend_d64_t3(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
+                         bool init, cudaStream_t stream) {
+  return attend_rows<64, 3>(rt, tk, tv, a, grid, init, stream);
+}
+}  // namespace qsa

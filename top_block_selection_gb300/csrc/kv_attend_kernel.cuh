@@ -11,13 +11,27 @@
 // tcgen05.mma kind::f8f6f4 with the cache as the M = 128 operand (128 tokens
 // for the scores, the D dimensions for the output, read MN-major), loaded by
 // TMA and never touched by a thread. The other operand is made e4m3 without
-// losing its bits: a value y is y1 + y2 + y3, y1 = e4m3(y), y2 = e4m3(y - y1),
-// y3 = e4m3(y - y1 - y2). Each term takes 4 significant bits and its sign one
-// more, so three hold the 11 bits of an fp16 query exactly (as far as they lie
-// above 2^-19 of the row's maximum) and a probability to 2^-12. The
-// three terms are three groups of N columns, added in fp32 after the product.
+// losing its bits, as a sum of T terms of 4 significant bits, T = 3 for fp16
+// and 2 for bf16 calls:
+//   queries        y1 = e4m3(y), y2 = e4m3(y - y1), y3 = ...: exact for every
+//                  fp16 (T = 3) or bf16 (T = 2) element above 2^-18 of its
+//                  row's largest, the rest to 2^-19 of that;
+//   probabilities  T = 3: cut, cut and rounded, to 2^-12 of each; T = 2:
+//                  rounded twice, to 2^-9. Both are a fraction of the
+//                  rounding of the result (2^-11 and 2^-8 at most), and what
+//                  lies below e4m3's range is off by 2^-17 of the row's
+//                  largest at most.
+// The terms are groups of columns of one product, added in fp32 after it.
 // With few rows a tile's product is bound by reading the M operand from
 // shared memory, so the extra columns cost little.
+//
+// The softmax reference m_r is not each tile's maximum but one that lags: a
+// tile keeps it unless a score exceeds it by more than 2^1.75 (codes then
+// still fit: 128 * 2^1.75 < 448). Most tiles thus need one vote of the
+// warpgroup instead of a maximum over its tokens for each row, and the output
+// stays in TMEM, accumulated by the product itself, until a reference moves
+// or the item ends. The value scales ride on the probabilities, relative to
+// the largest so far, in the same way.
 //
 // What bounds it: decoding reads every code once from HBM (about 23 bytes a
 // cycle and SM); over chosen blocks of many queries the codes come from L2.
@@ -108,9 +122,10 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
 }
 
 // Instruction descriptor: fp32 D (bits 4-5 = 1), e4m3 A and B (formats 0), A
-// MN-major when asked (bit 15), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t idesc_f8(int N, bool a_mn_major) {
-  return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// and B MN-major when asked (bits 15, 16), N >> 3 at bits 17-22, M >> 4 at
+// bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, bool mn_major) {
+  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 
 // Shared-memory descriptor of rows of ROW bytes (128 or 64) swizzled over
@@ -124,6 +139,15 @@ __device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
   constexpr uint64_t group = (8 * ROW) >> 4;
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (group << 16) | (group << 32) | (1ull << 46) |
          (swizzle << 61);
+}
+
+// The probabilities: MN-major without swizzle, 16 columns of a token in 16
+// bytes, 8 tokens in 128, then the next 8 tokens (leading offset), the next 16
+// columns behind all 128 tokens (stride offset). A thread writes its token's
+// terms by 16-byte stores, 32 threads of a warp 512 consecutive bytes.
+__device__ __forceinline__ uint64_t smem_desc_tokens(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(16 * kKvTile >> 4) << 32) | (1ull << 46);
 }
 
 template <int ROW>
@@ -201,8 +225,33 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ void store_u8(uint32_t saddr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+
+// Two fp32 operations in one instruction.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
 // Waits for a phase of `bar`, but at most kWaitTimeoutNs; the first wait of a
@@ -227,11 +276,12 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
 }
 
 // ------------------------------------------------------------ configuration
-template <int D_, int RT_>
+template <int D_, int RT_, int T_>
 struct AttendCfg {
   static constexpr int D = D_;
   static constexpr int RT = RT_;                            // rows
-  static constexpr int N = (3 * RT + 15) / 16 * 16;         // columns: three terms of each row
+  static constexpr int T = T_;                              // e4m3 terms of a value
+  static constexpr int N = (T * RT + 15) / 16 * 16;         // columns: the terms of each row
   static constexpr int W = RT >= 32 ? 2 : 3;                // warpgroups
   static constexpr int kThreads = W * 128 + 64;
   static constexpr int kStageBytes = 2 * kKvTile * D;       // K then V
@@ -242,7 +292,7 @@ struct AttendCfg {
   static constexpr int kQBytes = N * D;                     // one of two buffers
   static constexpr int kPBytes = N * kKvTile;               // one of W
   static constexpr int kMergeBytes = (W - 1) * RT * D * 4;  // lies over the P buffers
-  static_assert(kMergeBytes <= W * kPBytes, "merge buffer");
+  static constexpr int kPRegion = W * kPBytes > kMergeBytes ? W * kPBytes : kMergeBytes;
   static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
   static_assert(2 * N * W <= 512, "TMEM");
 };
@@ -250,15 +300,14 @@ struct AttendCfg {
 struct StageMeta {
   int32_t base[kKvMaxSlots];  // position of the slot's first token, kKvNoToken if none
   float ks[kKvMaxSlots];      // key scale
-  float vs[kKvMaxSlots];      // 256 * value scale / the tile's largest
-  float vfac;                 // that largest / 256
-  int32_t any;                // some slot holds tokens
+  float vs[kKvMaxSlots];      // value scale (0: no block)
+  float vmax;                 // the largest of them
 };
 
 template <int RT>
 struct ItemInfo {
-  int32_t row_pos[RT];  // last position the row sees; -1: nothing
-  float row_mul[RT];    // query scale * softmax scale * log2(e)
+  alignas(16) int32_t row_pos[RT];  // last position the row sees; -1: nothing
+  alignas(16) float row_mul[RT];    // query scale * softmax scale * log2(e)
   int32_t tiles;        // of this CTA's part; 0 ends the walk
   int32_t lo_pos, hi_pos;  // smallest and largest row_pos of rows that see anything
   int32_t rows, b, j0, h;
@@ -325,7 +374,6 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         ks = __ldg(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
         vs = __ldg(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
       }
-      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, page >= 0);
       const int tiles = min(per_batch, part - t0);
       for (int i = 0; i < tiles; ++i, ++g) {
         const int st = g % C::kStages;
@@ -333,20 +381,15 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
           ok = wait_or_stop(&s.empty[st], ((g / C::kStages) & 1) ^ 1, &s.stop, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const bool any = ((valid >> (i * spt)) & ((1u << spt) - 1)) != 0;
         const bool mine = lane / spt == i;
-        if (any) {
-          if (lane == 0) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
-          __syncwarp();
-          if (mine) {
-            // A slot without a block reads past the last page: zeros.
-            uint8_t* const k_at = ring + st * C::kStageBytes + (lane % spt) * a.c.block * C::D;
-            const int y = w.h * a.c.block, z = page >= 0 ? page : a.c.n_pages;
-            tma_load_3d(k_at, tm_k, 0, y, z, &s.full[st]);
-            tma_load_3d(k_at + kKvTile * C::D, tm_v, 0, y, z, &s.full[st]);
-          }
-        } else if (lane == 0) {
-          mbar_arrive(&s.full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
+        __syncwarp();
+        if (mine) {
+          // A slot without a block reads past the last page: zeros.
+          uint8_t* const k_at = ring + st * C::kStageBytes + (lane % spt) * a.c.block * C::D;
+          const int y = w.h * a.c.block, z = page >= 0 ? page : a.c.n_pages;
+          tma_load_3d(k_at, tm_k, 0, y, z, &s.full[st]);
+          tma_load_3d(k_at + kKvTile * C::D, tm_v, 0, y, z, &s.full[st]);
         }
         float vmax = mine ? vs : 0.0f;
         for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
@@ -354,11 +397,8 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         if (mine) {
           m.base[lane % spt] = page >= 0 ? blk * a.c.block : kKvNoToken;
           m.ks[lane % spt] = ks;
-          m.vs[lane % spt] = vmax > 0.0f ? 256.0f * __fdiv_rn(vs, vmax) : 0.0f;
-          if (lane % spt == 0) {
-            m.vfac = vmax * (1.0f / 256.0f);
-            m.any = any;
-          }
+          m.vs[lane % spt] = vs;
+          if (lane % spt == 0) m.vmax = vmax;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[st]);
@@ -461,7 +501,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           if (isinf(x[i][e])) x[i][e] = __int_as_float(0x7FC00000);
         }
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
+        for (int term = 0; term < C::T; ++term) {
           uint32_t code[kPer / 2];
 #pragma unroll
           for (int e = 0; e < kPer / 2; ++e) {
@@ -543,6 +583,32 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
+// The columns of RT rows at `taddr`, their T terms added, a few rows at a time
+// (the terms of all would not fit in registers beside the softmax state).
+template <class C>
+__device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
+  constexpr int kPart = C::RT <= 8 ? C::RT : C::RT / 2;
+#pragma unroll
+  for (int r0 = 0; r0 < C::RT; r0 += kPart) {
+    float t0[kPart], t1[kPart], t2[kPart];
+    tmem_ld_cols<kPart>(taddr + r0, t0);
+    tmem_ld_cols<kPart>(taddr + C::RT + r0, t1);
+    if (C::T == 3) tmem_ld_cols<kPart>(taddr + 2 * C::RT + r0, t2);
+    tmem_ld_wait();
+#pragma unroll
+    for (int r = 0; r < kPart; r += 2) {
+      F2 sum = f2(t1[r], t1[r + 1]);
+      if (C::T == 3) sum = sum + f2(t2[r], t2[r + 1]);
+      sum = sum + f2(t0[r], t0[r + 1]);
+      f2_get(sum, x[r0 + r], x[r0 + r + 1]);
+    }
+  }
+}
+
+constexpr float kUnset = -3e38f;   // a reference that no score has set yet
+constexpr float kLag = 1.75f;      // how far (log2) a score may exceed its reference
+constexpr float kProbScale = 128;  // of the codes of a probability 1
+
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
                                uint8_t* p_smem) {
@@ -556,7 +622,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const int my_slot = t / a.c.block, my_off = t % a.c.block;
   uint32_t g0 = 0;      // tiles of the CTA before this item
   uint32_t phase = 0;   // of this warpgroup's two product barriers
-  bool bad = false;
+  bool bad = false;     // a wait ran out: what follows is not used
   const float kNegInf = -INFINITY;
 
   for (uint32_t it = 0;; ++it) {
@@ -574,20 +640,34 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     for (int r = 0; r < RT; ++r) {
       o[r] = 0.0f;
       l[r] = 0.0f;
-      m[r] = kNegInf;
+      m[r] = kUnset;
     }
+    float vref = 0.0f, inv_vref = 0.0f;  // largest value scale so far, kProbScale / it
+    bool pending = false;                // a product runs that was not waited for
+    bool held = false;                   // TMEM holds output not yet in o[]
+    // Waits for the product in flight (the phase of its tile's barriers) and
+    // moves what TMEM holds to o[].
+    auto flush = [&](uint32_t its_phase) {
+      if (pending) {
+        if (!wait_or_stop(&s.o_bar[wg], its_phase, &s.stop, a.status)) bad = true;
+        pending = false;
+      }
+      if (!held) return;
+      held = false;
+      __syncwarp();
+      tc_fence_after_sync();
+      float x[RT];
+      tmem_rows<C>(tm_o + lane_addr, x);
+      const float f = vref * (1.0f / kProbScale);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) o[r] += x[r] * f;
+    };
 
     for (int i = (W - g0 % W + wg) % W; i < tiles; i += W) {
       const uint32_t g = g0 + i;
       const int st = g % C::kStages;
       if (!wait_or_stop(&s.full[st], (g / C::kStages) & 1, &s.stop, a.status)) bad = true;
-      const StageMeta& meta = s.meta[st];
-      const int any = bad ? 0 : meta.any;
       uint8_t* const k_tile = ring + st * C::kStageBytes;
-      if (!bar_any(1 + wg, 128, any != 0)) {  // no block in this tile (or a wait ran out)
-        if (t == 0) mbar_arrive(&s.empty[st]);
-        continue;
-      }
       if (t == 0) {
         tc_fence_after_sync();
         const uint32_t ka = smem_u32(k_tile), qa = smem_u32(q_smem + buf * C::kQBytes);
@@ -597,79 +677,93 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
                     ks > 0);
         mma_commit(&s.s_bar[wg]);
       }
+      const StageMeta& meta = s.meta[st];
       const int pos = meta.base[my_slot] + my_off;
-      const float k_mul = meta.ks[my_slot], v_mul = meta.vs[my_slot], v_fac = meta.vfac;
-      if (pos > lo_pos) {
-        const bool unseen = pos > hi_pos;
-        clean_value_row<D>(k_tile + kKvTile * D, t, pos, unseen, s.poison);
-      }
+      const float k_mul = meta.ks[my_slot], v_scale = meta.vs[my_slot], v_max = meta.vmax;
+      const bool masks = pos > lo_pos;
+      if (masks) clean_value_row<D>(k_tile + kKvTile * D, t, pos, pos > hi_pos, s.poison);
       if (!wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
+      phase ^= 1;
       __syncwarp();
       tc_fence_after_sync();
-      float x[RT];
-      {
-        float x1[RT], x2[RT];
-        tmem_ld_cols<RT>(tm_s + lane_addr, x);
-        tmem_ld_cols<RT>(tm_s + lane_addr + RT, x1);
-        tmem_ld_cols<RT>(tm_s + lane_addr + 2 * RT, x2);
-        tmem_ld_wait();
+      float e[RT];
+      // e = x - m, or x itself.
+      auto scores = [&](bool relative) {
+        tmem_rows<C>(tm_s + lane_addr, e);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) x[r] = (x[r] + (x1[r] + x2[r])) * k_mul * info.row_mul[r];
-      }
-      if (pos > lo_pos) {
+        for (int r = 0; r < RT; r += 2) {
+          const F2 f = f2(info.row_mul[r], info.row_mul[r + 1]) * f2(k_mul, k_mul);
+          const F2 base = relative ? f2(-m[r], -m[r + 1]) : f2(0.0f, 0.0f);
+          f2_get(fma2(f2(e[r], e[r + 1]), f, base), e[r], e[r + 1]);
+        }
+        if (masks) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          if (pos > info.row_pos[r]) x[r] = kNegInf;
-      }
-      float top = 0.0f;
+          for (int r = 0; r < RT; ++r)
+            if (pos > info.row_pos[r]) e[r] = kNegInf;
+        }
+      };
+      scores(true);
+      float top = kNegInf;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float v = warp_max(x[r]);
-        if (lane == r) top = v;
-      }
-      if (lane < RT) s.red[wg][lane][warp] = top;
-      bar_sync(1 + wg, 128);
-      bool grown = false;
-      float alpha[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float4 v = *reinterpret_cast<const float4*>(s.red[wg][r]);
-        const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-        const float mn = fmaxf(m[r], mx);
-        grown |= mn > m[r];
-        alpha[r] = m[r];
-        m[r] = mn;
-      }
-      if (grown) {
+      for (int r = 0; r < RT; ++r) top = fmaxf(top, e[r]);
+      if (bar_any(1 + wg, 128, top > kLag || v_max > vref)) {
+        // Move the references to the largest scores so far.
+        scores(false);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          alpha[r] = m[r] == kNegInf ? 1.0f : exp2_approx(alpha[r] - m[r]);
-          l[r] *= alpha[r];
-          o[r] *= alpha[r];
+          const float v = warp_max(e[r]);
+          if (lane == r) top = v;
+        }
+        if (lane < RT) s.red[wg][lane][warp] = top;
+        flush(phase);  // of the tile before: two flips ago
+        bar_sync(1 + wg, 128);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(s.red[wg][r]);
+          const float mn = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+          const float alpha = exp2_approx(m[r] - mn);
+          m[r] = mn;
+          l[r] *= alpha;
+          o[r] *= alpha;
+          e[r] -= mn;
+        }
+        if (v_max > vref) {
+          vref = v_max;
+          inv_vref = __fdiv_rn(kProbScale, vref);
         }
       }
+      const float v_mul = v_scale * inv_vref;
+      uint32_t codes[N / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
-        float y[2];
+        float p0 = exp2_approx(e[r]), p1 = exp2_approx(e[r + 1]);
+        F2 p = f2(p0, p1);
+        f2_get(f2(l[r], l[r + 1]) + p, l[r], l[r + 1]);
+        F2 y = p * f2(v_mul, v_mul);
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float base = m[r + i2] == kNegInf ? 0.0f : m[r + i2];
-          const float p = exp2_approx(x[r + i2] - base);
-          l[r + i2] += p;
-          y[i2] = p * v_mul;
-        }
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          const uint32_t code = e4m3x2(y[0], y[1]);
-          const int row = term * RT + r;
-          store_u8(p_addr + row * 128 + (((t >> 4) ^ (row & 7)) << 4) + (t & 15), code);
-          store_u8(p_addr + (row + 1) * 128 + (((t >> 4) ^ ((row + 1) & 7)) << 4) + (t & 15), code >> 8);
-          if (term < 2) {
-            const float2 back = e4m3x2_to_float2(code);
-            y[0] -= back.x;
-            y[1] -= back.y;
+        for (int term = 0; term < C::T; ++term) {
+          f2_get(y, p0, p1);
+          uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+          if (term < C::T - 1) {  // 4 significant bits: cut (T = 3) or rounded half up (T = 2)
+            b0 = (b0 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
+            b1 = (b1 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
+            y = fma2(f2(__uint_as_float(b0), __uint_as_float(b1)), f2(-1.0f, -1.0f), y);
           }
+          const uint32_t pair = e4m3x2(__uint_as_float(b0), __uint_as_float(b1));
+          const int col = term * RT + r;
+          if (col % 4 == 0) codes[col / 4] = pair;
+          else codes[col / 4] |= pair << 16;
         }
+      }
+      // The product before this one has to be done with the probabilities' buffer.
+      if (pending && !wait_or_stop(&s.o_bar[wg], phase, &s.stop, a.status)) bad = true;
+#pragma unroll
+      for (int c = 0; c < C::T * RT; c += 16) {
+        uint8_t* const to = p_buf + c * kKvTile + t * 16;
+        if (C::T * RT - c >= 16)
+          *reinterpret_cast<uint4*>(to) = make_uint4(codes[c / 4], codes[c / 4 + 1], codes[c / 4 + 2], codes[c / 4 + 3]);
+        else
+          for (int k = 0; k < (C::T * RT - c) / 4; ++k) reinterpret_cast<uint32_t*>(to)[k] = codes[c / 4 + k];
       }
       tc_fence_before_sync();
       fence_proxy_async_smem();
@@ -679,26 +773,14 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         const uint32_t va = smem_u32(k_tile + kKvTile * D);
 #pragma unroll
         for (int ks = 0; ks < kKvTile / 32; ++ks)
-          mma_f8_ss(tm_o, smem_desc_rows<D>(va + ks * 32 * D), smem_desc_rows<128>(p_addr + ks * 32),
-                    idesc_f8(N, true), ks > 0);
+          mma_f8_ss(tm_o, smem_desc_rows<D>(va + ks * 32 * D), smem_desc_tokens(p_addr + ks * 512),
+                    idesc_f8(N, true), held || ks > 0);
         mma_commit(&s.o_bar[wg]);
         mma_commit(&s.empty[st]);
       }
-      if (!wait_or_stop(&s.o_bar[wg], phase, &s.stop, a.status)) bad = true;
-      phase ^= 1;
-      __syncwarp();
-      tc_fence_after_sync();
-      {
-        float x1[RT], x2[RT];
-        tmem_ld_cols<RT>(tm_o + lane_addr, x);
-        tmem_ld_cols<RT>(tm_o + lane_addr + RT, x1);
-        tmem_ld_cols<RT>(tm_o + lane_addr + 2 * RT, x2);
-        tmem_ld_wait();
-        tc_fence_before_sync();
-#pragma unroll
-        for (int r = 0; r < RT; ++r) o[r] += (x[r] + (x1[r] + x2[r])) * v_fac;
-      }
+      pending = held = true;
     }
+    flush(phase ^ 1);
     g0 += tiles;
 
     // Join the warpgroups: sums over the tokens, then the outputs, in order.
@@ -709,6 +791,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       for (int d = 16; d > 0; d /= 2) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
       if (lane == r) mine = l[r];
     }
+    bar_sync(1 + wg, 128);
     if (lane < RT) s.red[wg][lane][warp] = mine;
     bar_sync(1 + wg, 128);
     if (t < RT) {
@@ -725,7 +808,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       float mx = s.ml[0][0][r];
 #pragma unroll
       for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][r]);
-      o[r] *= m[r] == kNegInf ? 0.0f : exp2_approx(m[r] - mx);
+      o[r] *= exp2_approx(m[r] - mx);
       m[r] = mx;
     }
     float* const merge = reinterpret_cast<float*>(p_smem);
@@ -748,10 +831,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float mw = s.ml[0][w][r];
-          sum += mw == kNegInf && !(s.ml[1][w][r] != s.ml[1][w][r])
-                     ? 0.0f
-                     : s.ml[1][w][r] * (mw == kNegInf ? 1.0f : exp2_approx(mw - m[r]));
+          sum += s.ml[1][w][r] * exp2_approx(s.ml[0][w][r] - m[r]);
         }
         const int row_pos = info.row_pos[r];
         float v = o[r];
@@ -760,7 +840,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           float* const part = part_row(a, info.slot, rows, r);
           if (t < D) part[t] = v;
           if (t == 0) {
-            part[D] = row_pos < 0 ? kNegInf : m[r];
+            part[D] = row_pos < 0 ? kUnset : m[r];
             part[D + 1] = row_pos < 0 ? 0.0f : sum;
           }
         } else {
@@ -774,7 +854,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
             else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
           }
           if (a.lse && t == 0)
-            a.lse[at] = none ? kNegInf : (m[r] == kNegInf ? sum : m[r] * 0.6931471805599453f + logf(sum));
+            a.lse[at] = none ? kNegInf : m[r] * 0.6931471805599453f + logf(sum);
         }
       }
     }
@@ -792,7 +872,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint8_t* const ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* const q_smem = ring + C::kStages * C::kStageBytes;
   uint8_t* const p_smem = q_smem + 2 * C::kQBytes;
-  AttendShared<C>& s = *reinterpret_cast<AttendShared<C>*>(p_smem + C::W * C::kPBytes);
+  AttendShared<C>& s = *reinterpret_cast<AttendShared<C>*>(p_smem + C::kPRegion);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   pdl_launch_dependents();
@@ -889,11 +969,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 }
 
 // Launch with the given tensor maps; grid CTAs.
-template <int D, int RT>
+template <int D, int RT, int T>
 cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid, bool init,
                         cudaStream_t stream) {
-  using C = AttendCfg<D, RT>;
-  constexpr int smem = 1024 + C::kStages * C::kStageBytes + 2 * C::kQBytes + C::W * C::kPBytes +
+  using C = AttendCfg<D, RT, T>;
+  constexpr int smem = 1024 + C::kStages * C::kStageBytes + 2 * C::kQBytes + C::kPRegion +
                        static_cast<int>(sizeof(AttendShared<C>));
   static_assert(smem <= 227 * 1024, "shared memory");
   if (init) return cudaFuncSetAttribute(kv_attend_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -901,20 +981,22 @@ cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const Atte
   return cudaGetLastError();
 }
 
-// All row counts of one head size (kv_attend_d64.cu, kv_attend_d128.cu).
-template <int D>
+// All row counts of one head size and term count (kv_attend_d*_t*.cu).
+template <int D, int T>
 cudaError_t attend_rows(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
                         bool init, cudaStream_t stream) {
   switch (rt) {
-    case 4: return attend_form<D, 4>(tk, tv, a, grid, init, stream);
-    case 8: return attend_form<D, 8>(tk, tv, a, grid, init, stream);
-    case 16: return attend_form<D, 16>(tk, tv, a, grid, init, stream);
-    default: return attend_form<D, 32>(tk, tv, a, grid, init, stream);
+    case 4: return attend_form<D, 4, T>(tk, tv, a, grid, init, stream);
+    case 8: return attend_form<D, 8, T>(tk, tv, a, grid, init, stream);
+    case 16: return attend_form<D, 16, T>(tk, tv, a, grid, init, stream);
+    default: return attend_form<D, 32, T>(tk, tv, a, grid, init, stream);
   }
 }
-cudaError_t attend_rows_d64(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
-                            bool init, cudaStream_t stream);
-cudaError_t attend_rows_d128(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
-                             bool init, cudaStream_t stream);
+using AttendLaunch = cudaError_t (*)(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a,
+                                     int grid, bool init, cudaStream_t stream);
+cudaError_t attend_d64_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
+cudaError_t attend_d64_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
+cudaError_t attend_d128_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
+cudaError_t attend_d128_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
 
 }  // namespace qsa
