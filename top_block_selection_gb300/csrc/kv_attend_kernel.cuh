@@ -19,29 +19,30 @@
 //   probabilities  T = 3: cut, cut and rounded, to 2^-12 of each; T = 2:
 //                  rounded twice, to 2^-9. Both are a fraction of the
 //                  rounding of the result (2^-11 and 2^-8 at most), and what
-//                  lies below e4m3's range is off by 2^-17 of the row's
+//                  lies below e4m3's range is off by 2^-16 of the row's
 //                  largest at most.
 // The terms are groups of columns of one product, added in fp32 after it.
 // With few rows a tile's product is bound by reading the M operand from
 // shared memory, so the extra columns cost little.
 //
-// The softmax reference m_r is not each tile's maximum but one that lags: a
-// tile keeps it unless a score exceeds it by more than 2^1.75 (codes then
-// still fit: 128 * 2^1.75 < 448). Most tiles thus need one vote of the
+// The softmax reference m_r is not each tile's maximum but one that lags: it
+// is set to twice (one in log2) the largest score, and a tile keeps it as long
+// as its codes still fit below 448. Most tiles thus need one vote of the
 // warpgroup instead of a maximum over its tokens for each row, and the output
 // stays in TMEM, accumulated by the product itself, until a reference moves
 // or the item ends. The value scales ride on the probabilities, relative to
-// the largest so far, in the same way.
+// the largest at the last move.
 //
 // What bounds it: decoding reads every code once from HBM (about 23 bytes a
 // cycle and SM); over chosen blocks of many queries the codes come from L2.
-// Each CTA (one per SM) runs a ring of 128-token stages filled by one
-// producer warp, two or three warpgroups that take the tiles in turn, each with its
-// own running maximum, sum and output (so that loads, products and the
-// softmax of different tiles overlap without a hand-over between warps), and
-// one warp that prepares the next query rows. All tiles of a call are dealt
-// to the CTAs in equal contiguous shares, whatever the lengths; an (query,
-// head) item that ends up in several CTAs leaves partial results in the
+// Each CTA (one per SM) runs a ring of 128-token stages, two or three
+// warpgroups that take the tiles in turn, each with its own running reference,
+// sum and output (so that loads, products and the softmax of different tiles
+// overlap without a hand-over between them) and its own producer warp (one
+// warp for all took 1,200 to 1,450 cycles a tile: as long as everything else),
+// and one warp that prepares the next query rows. All tiles of a call are
+// dealt to the CTAs in equal contiguous shares, whatever the lengths; a (query
+// tile, head) item that ends up in several CTAs leaves partial results in the
 // workspace, which kv_combine_kernel joins.
 #pragma once
 
@@ -215,6 +216,27 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
       : "memory");
   return r != 0;
 }
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// A value that all lanes hold, known to the compiler as such: descriptors and
+// addresses of single-thread instructions then stay in uniform registers.
+template <class V>
+__device__ __forceinline__ V uniform(V x) {
+  return __shfl_sync(0xFFFFFFFFu, x, 0);
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float warp_max(float x) {  // NaN counts as nothing
   float r;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -283,7 +305,7 @@ struct AttendCfg {
   static constexpr int T = T_;                              // e4m3 terms of a value
   static constexpr int N = (T * RT + 15) / 16 * 16;         // columns: the terms of each row
   static constexpr int W = RT >= 32 ? 2 : 3;                // warpgroups
-  static constexpr int kThreads = W * 128 + 64;
+  static constexpr int kThreads = W * 128 + W * 32 + 32;    // they, a producer warp for each, the query warp
   static constexpr int kStageBytes = 2 * kKvTile * D;       // K then V
   // A stage serves one warpgroup only: a parity wait may not run two phases
   // ahead, and only a stage's own last user knows that its phase has passed.
@@ -291,8 +313,9 @@ struct AttendCfg {
   static_assert(kStages % W == 0, "a stage serves one warpgroup");
   static constexpr int kQBytes = N * D;                     // one of two buffers
   static constexpr int kPBytes = N * kKvTile;               // one of W
-  static constexpr int kMergeBytes = (W - 1) * RT * D * 4;  // lies over the P buffers
-  static constexpr int kPRegion = W * kPBytes > kMergeBytes ? W * kPBytes : kMergeBytes;
+  static constexpr int kJoinRows = RT <= 8 ? RT : RT / 2;   // rows joined at a time, over the P buffers
+  static constexpr int kJoinBytes = W * kJoinRows * D * 4;
+  static constexpr int kPRegion = W * kPBytes > kJoinBytes ? W * kPBytes : kJoinBytes;
   static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
   static_assert(2 * N * W <= 512, "TMEM");
 };
@@ -301,17 +324,17 @@ struct StageMeta {
   int32_t base[kKvMaxSlots];  // position of the slot's first token, kKvNoToken if none
   float ks[kKvMaxSlots];      // key scale
   float vs[kKvMaxSlots];      // value scale (0: no block)
-  float vmax;                 // the largest of them
 };
 
 template <int RT>
 struct ItemInfo {
   alignas(16) int32_t row_pos[RT];  // last position the row sees; -1: nothing
   alignas(16) float row_mul[RT];    // query scale * softmax scale * log2(e)
-  int32_t tiles;        // of this CTA's part; 0 ends the walk
-  int32_t lo_pos, hi_pos;  // smallest and largest row_pos of rows that see anything
-  int32_t rows, b, j0, h;
-  int32_t slot;         // partial result to write, -1: the whole item
+  int64_t row_at[RT];               // index of the row in out (rows of D) and lse; -1: none
+  int32_t tiles;                    // of this CTA's part; 0 ends the walk
+  int32_t lo_pos, hi_pos;           // smallest and largest row_pos of rows that see anything
+  int32_t rows;
+  int32_t slot;                     // partial result to write, -1: the whole item
 };
 
 template <class C>
@@ -319,7 +342,8 @@ struct AttendShared {
   ItemInfo<C::RT> item[2];
   StageMeta meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
-  float ml[2][C::W][C::RT];      // the warpgroups' maxima and sums
+  alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
+  float mx[C::RT], sum[C::RT];   // joined
   int32_t poison[128];           // first position whose value code is NaN, per dimension
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
@@ -330,13 +354,32 @@ struct AttendShared {
   uint32_t stop;
 };
 
+// Advances the walk past `part` tiles of an item of `tiles`.
+__device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads) {
+  w.left -= part;
+  w.t += part;
+  if (w.t >= tiles) {
+    w.t = 0;
+    if (++w.h == heads) {
+      w.h = 0;
+      ++w.e;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ producer
+// The tiles of warpgroup p: block lists, pages and scales for up to 32 blocks
+// at a time, one per lane, then two TMA loads a block.
 template <class C>
 __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                               AttendShared<C>& s, uint8_t* ring, Walk w) {
+                               AttendShared<C>& s, uint8_t* ring, Walk w, int p) {
+  constexpr int W = C::W;
   const int lane = threadIdx.x % 32;
   const int spt = a.spt, per_batch = 32 / spt;
-  uint32_t g = 0;  // tiles issued by this CTA
+  const int my_k = lane / spt, my_slot = lane % spt;
+  uint32_t g0 = 0;         // tiles of the CTA before this item
+  uint32_t last = 0;       // tiles of this warp so far
+  uint32_t last_g[C::kStages / W];
   bool ok = true;
   Entry en{};
   int en_of = -1;
@@ -346,6 +389,8 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
       en_of = w.e;
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
+    const int first = (W - g0 % W + p) % W;  // this warpgroup's tiles: first, first + W, ...
+    const int own = part > first ? (part - first + W - 1) / W : 0;
     const int cap = a.c.max_blocks * a.c.block;
     bool bad = en.last_pos >= cap;  // longer than its page table
     const int keys = min(en.last_pos + 1, cap);
@@ -353,10 +398,9 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
     if (a.ids)
       list = a.ids + ((static_cast<int64_t>(en.b) * a.n_lists + (a.n_lists > 1 ? w.h : 0)) * a.n + en.j0) * a.k;
     const int32_t* table = a.c.page_table + static_cast<int64_t>(en.b) * a.c.max_blocks;
-    for (int t0 = 0; t0 < part && ok; t0 += per_batch) {
-      // One block of the next 32 / spt tiles per lane.
-      const int slot = (w.t + t0) * spt + lane;
-      const bool in_part = t0 + lane / spt < part;
+    for (int k0 = 0; k0 < own && ok; k0 += per_batch) {
+      const int slot = (w.t + first + (k0 + my_k) * W) * spt + my_slot;
+      const bool in_part = k0 + my_k < own;
       int blk = in_part ? slot : -1;
       if (list) blk = in_part && slot < a.k ? __ldg(list + slot) : -1;
       if (list && blk >= a.c.max_blocks) {
@@ -374,66 +418,150 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         ks = __ldg(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
         vs = __ldg(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
       }
-      const int tiles = min(per_batch, part - t0);
-      for (int i = 0; i < tiles; ++i, ++g) {
-        const int st = g % C::kStages;
+      const int z = page >= 0 ? page : a.c.n_pages;  // no block: reads past the last page give zeros
+      const int base = page >= 0 ? blk * a.c.block : kKvNoToken;
+      const int tiles = min(per_batch, own - k0);
+      const int y = uniform(w.h * a.c.block), slab = a.c.block * C::D;
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t g = uniform(g0 + first + (k0 + i) * W);
+        const uint32_t st = g % C::kStages;
         if (g >= C::kStages)
           ok = wait_or_stop(&s.empty[st], ((g / C::kStages) & 1) ^ 1, &s.stop, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const bool mine = lane / spt == i;
-        if (lane == 0) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
-        __syncwarp();
-        if (mine) {
-          // A slot without a block reads past the last page: zeros.
-          uint8_t* const k_at = ring + st * C::kStageBytes + (lane % spt) * a.c.block * C::D;
-          const int y = w.h * a.c.block, z = page >= 0 ? page : a.c.n_pages;
-          tma_load_3d(k_at, tm_k, 0, y, z, &s.full[st]);
-          tma_load_3d(k_at + kKvTile * C::D, tm_v, 0, y, z, &s.full[st]);
+        uint8_t* const k_at = ring + st * C::kStageBytes;
+        if (elect_one()) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
+        for (int j = 0; j < spt; ++j) {
+          const int zj = __shfl_sync(0xFFFFFFFFu, z, i * spt + j);
+          if (elect_one()) {
+            tma_load_3d(k_at + j * slab, tm_k, 0, y, zj, &s.full[st]);
+            tma_load_3d(k_at + kKvTile * C::D + j * slab, tm_v, 0, y, zj, &s.full[st]);
+          }
+          __syncwarp();
         }
-        float vmax = mine ? vs : 0.0f;
-        for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
-        StageMeta& m = s.meta[st];
-        if (mine) {
-          m.base[lane % spt] = page >= 0 ? blk * a.c.block : kKvNoToken;
-          m.ks[lane % spt] = ks;
-          m.vs[lane % spt] = vs;
-          if (lane % spt == 0) m.vmax = vmax;
+        if (my_k == i) {
+          s.meta[st].base[my_slot] = base;
+          s.meta[st].ks[my_slot] = ks;
+          s.meta[st].vs[my_slot] = vs;
         }
+        last_g[last % (C::kStages / W)] = g;
+        ++last;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[st]);
       }
     }
     if (bad && (a.ids || lane == 0)) atomicOr(a.status, kErrCacheIndex);
-    w.left -= part;
-    w.t += part;
-    if (w.t >= en.tiles) {
-      w.t = 0;
-      if (++w.h == a.c.Hkv) {
-        w.h = 0;
-        ++w.e;
-      }
-    }
+    g0 += part;
+    step(w, part, en.tiles, a.c.Hkv);
   }
   if (!ok) {  // let the copies in flight land before the CTA gives its memory back
-    const uint32_t n = min(g, static_cast<uint32_t>(C::kStages));
-    for (uint32_t i = g - n; i < g; ++i)
-      mbar_wait_bounded(&s.full[i % C::kStages], (i / C::kStages) & 1, 100000000ull);
+    const uint32_t n = min(last, static_cast<uint32_t>(C::kStages / W));
+    for (uint32_t i = last - n; i < last; ++i) {
+      const uint32_t g = last_g[i % (C::kStages / W)];
+      mbar_wait_bounded(&s.full[g % C::kStages], (g / C::kStages) & 1, 100000000ull);
+    }
   }
 }
 
 // --------------------------------------------------------- the query's terms
+// Row r of the query tile `en` for KV head h, by one warp: scaled by a power
+// of two to the range of e4m3 and split in terms. Rows that are not there are
+// zero. `dst` holds rows of D bytes, term after term.
 template <class C>
-__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, Walk w, int64_t lo,
-                               int64_t total, int grid) {
+__device__ __forceinline__ void query_row(const AttendArgs& a, ItemInfo<C::RT>& info, uint8_t* dst, const Entry& en,
+                                          int h, int r) {
   constexpr int kPer = C::D / 32;  // elements of a lane
+  const int lane = threadIdx.x % 32, rows = a.qt * a.R;
+  const int j = r / a.R, head = h * a.R + (r - j * a.R);
+  const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
+  float x[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
+  if (there) {
+    const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
+                                static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
+                                lane * kPer;
+    uint32_t u[kPer / 2];
+    if (kPer == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+      u[0] = v.x;
+      u[kPer / 2 - 1] = v.y;
+    } else {
+      u[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    }
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) {
+      if (a.bf16) {
+        x[2 * e] = __uint_as_float(u[e] << 16);
+        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+      }
+    }
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) m = fmaxf(m, fabsf(x[e]));
+  const float t = pow2_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(t));
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    x[e] *= inv;
+    if (isinf(x[e])) x[e] = __int_as_float(0x7FC00000);
+  }
+#pragma unroll
+  for (int term = 0; term < C::T; ++term) {
+    uint32_t code[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) {
+      code[e] = e4m3x2(x[2 * e], x[2 * e + 1]);
+      const float2 back = e4m3x2_to_float2(code[e]);
+      x[2 * e] -= back.x;
+      x[2 * e + 1] -= back.y;
+    }
+    uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
+    if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
+    else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
+  }
+  if (lane == 0) {
+    info.row_pos[r] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
+    info.row_mul[r] = t * a.scale_log2;
+    info.row_at[r] = r < rows && en.j0 + j < a.n ? (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + head : -1;
+  }
+}
+
+// The rest of an item's description, and the note for kv_combine_kernel where
+// this CTA begins an item that others end (one thread). `at`: the place of the
+// item's first tile among all tiles.
+template <class C>
+__device__ __forceinline__ void describe_item(const AttendArgs& a, ItemInfo<C::RT>& info, const Entry& en, const Walk& w,
+                                              int part, int64_t at, int64_t total, int grid) {
+  info.tiles = part;
+  info.lo_pos = en.last_pos < 0 ? -1 : max(en.first_pos, 0);
+  info.hi_pos = en.last_pos;
+  info.rows = a.qt * a.R;
+  const bool begins = w.t == 0, ends = w.t + part == en.tiles;
+  info.slot = begins && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
+  if (begins && !ends) {
+    int32_t* const job = a.jobs + 4 * blockIdx.x;
+    job[0] = w.e;
+    job[1] = w.h;
+    job[2] = static_cast<int32_t>(((at + en.tiles) * grid - 1) / total);  // the CTA that has its last tile
+  }
+}
+
+// The query warp: every item of the CTA's walk but the first (which the
+// warpgroups prepare themselves), one ahead of its use.
+template <class C>
+__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, Walk w, int64_t at,
+                               int64_t total, int grid) {
   const int lane = threadIdx.x % 32;
-  int64_t at = lo;  // tiles before this item
-  uint32_t it = 0;
   bool ok = true;
   Entry en{};
   int en_of = -1;
-  while (ok) {
+  for (uint32_t it = 0;; ++it) {
     const int buf = it & 1;
     if (it >= 2) ok = wait_or_stop(&s.q_empty[buf], ((it >> 1) & 1) ^ 1, &s.stop, a.status);
     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -451,108 +579,16 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       en_of = w.e;
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
-    const int rows = a.qt * a.R;
-    uint8_t* const dst = q_smem + buf * C::kQBytes;
-    for (int r0 = 0; r0 < C::RT; r0 += 4) {
-      float x[4][kPer];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i, j = r / a.R;
-        const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) x[i][e] = 0.0f;
-        if (there) {
-          const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
-                                      static_cast<int64_t>(en.j0 + j) * a.q.sn +
-                                      static_cast<int64_t>(w.h * a.R + r % a.R) * a.q.sh + lane * kPer;
-          uint32_t u[kPer / 2];
-          if (kPer == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-            u[0] = v.x;
-            u[kPer / 2 - 1] = v.y;
-          } else {
-            u[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-          }
-#pragma unroll
-          for (int e = 0; e < kPer / 2; ++e) {
-            if (a.bf16) {
-              x[i][2 * e] = __uint_as_float(u[e] << 16);
-              x[i][2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-            } else {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
-              x[i][2 * e] = f.x;
-              x[i][2 * e + 1] = f.y;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i, j = r / a.R;
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) m = fmaxf(m, fabsf(x[i][e]));
-        const float t = pow2_scale(
-            __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
-        const float inv = __uint_as_float((254u << 23) - __float_as_uint(t));
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          x[i][e] *= inv;
-          if (isinf(x[i][e])) x[i][e] = __int_as_float(0x7FC00000);
-        }
-#pragma unroll
-        for (int term = 0; term < C::T; ++term) {
-          uint32_t code[kPer / 2];
-#pragma unroll
-          for (int e = 0; e < kPer / 2; ++e) {
-            code[e] = e4m3x2(x[i][2 * e], x[i][2 * e + 1]);
-            const float2 back = e4m3x2_to_float2(code[e]);
-            x[i][2 * e] -= back.x;
-            x[i][2 * e + 1] -= back.y;
-          }
-          uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
-          if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
-          else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
-        }
-        if (lane == 0) {
-          const bool there = j < en.nq && en.first_pos + j >= 0;
-          info.row_pos[r] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
-          info.row_mul[r] = t * a.scale_log2;
-        }
-      }
+    if (it > 0) {
+#pragma unroll 4
+      for (int r = 0; r < C::RT; ++r) query_row<C>(a, info, q_smem + buf * C::kQBytes, en, w.h, r);
+      if (lane == 0) describe_item<C>(a, info, en, w, part, at, total, grid);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.q_full[buf]);
     }
-    if (lane == 0) {
-      info.tiles = part;
-      info.lo_pos = en.last_pos < 0 ? -1 : max(en.first_pos, 0);
-      info.hi_pos = en.last_pos;
-      info.rows = rows;
-      info.b = en.b;
-      info.j0 = en.j0;
-      info.h = w.h;
-      const bool begins = w.t == 0, ends = w.t + part == en.tiles;
-      info.slot = begins && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
-      if (begins && !ends) {
-        const int64_t last = at + en.tiles - 1;  // the item's last tile, and the CTA that has it
-        int32_t* const job = a.jobs + 4 * blockIdx.x;
-        job[0] = w.e;
-        job[1] = w.h;
-        job[2] = static_cast<int32_t>(((last + 1) * grid - 1) / total);
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.q_full[buf]);
-    ++it;
     at += w.t + part;
-    w.left -= part;
-    w.t += part;
-    if (w.t >= en.tiles) {
-      w.t = 0;
-      if (++w.h == a.c.Hkv) {
-        w.h = 0;
-        ++w.e;
-      }
-    }
+    step(w, part, en.tiles, a.c.Hkv);
   }
 }
 
@@ -605,33 +641,57 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
   }
 }
 
-constexpr float kUnset = -3e38f;   // a reference that no score has set yet
-constexpr float kLag = 1.75f;      // how far (log2) a score may exceed its reference
-constexpr float kProbScale = 128;  // of the codes of a probability 1
+constexpr float kUnset = -3e38f;     // a reference that no score has set yet
+constexpr float kMargin = 1.0f;      // a reference is set so far (log2) above the largest score
+constexpr float kProbScale = 128.0f; // code of a probability 1 at the largest value scale
+constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
-                               uint8_t* p_smem) {
+                               uint8_t* p_smem, const Walk& walk, int64_t at0, int64_t total, int grid) {
   constexpr int RT = C::RT, N = C::N, W = C::W, D = C::D;
   constexpr int kAll = W * 128;
-  const int wg = threadIdx.x / 128, t = threadIdx.x % 128, warp = t / 32, lane = t % 32;
+  const int wg = uniform(static_cast<int>(threadIdx.x / 128)), warp = uniform(static_cast<int>(threadIdx.x / 32 % 4));
+  const int t = threadIdx.x % 128, lane = t % 32;
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t tm_s = s.tmem + wg * 2 * N, tm_o = tm_s + N;
+  const uint32_t tm_s = uniform(s.tmem) + wg * 2 * N, tm_o = tm_s + N;
   uint8_t* const p_buf = p_smem + wg * C::kPBytes;
-  const uint32_t p_addr = smem_u32(p_buf);
+  const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem), p_addr = smem_u32(p_buf);
   const int my_slot = t / a.c.block, my_off = t % a.c.block;
   uint32_t g0 = 0;      // tiles of the CTA before this item
   uint32_t phase = 0;   // of this warpgroup's two product barriers
   bool bad = false;     // a wait ran out: what follows is not used
   const float kNegInf = -INFINITY;
 
+  // Scores of a tile, issued by one thread of the warpgroup's last warp.
+  auto issue_scores = [&](uint32_t st, int buf) {
+    tc_fence_after_sync();
+    const uint64_t ka = smem_desc_rows<D>(ring_addr + st * C::kStageBytes);
+    const uint64_t qa = smem_desc_rows<D>(q_addr + buf * C::kQBytes);
+    if (elect_one()) {
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(tm_s, ka + ks * 2, qa + ks * 2, idesc_f8(N, false), ks > 0);
+      mma_commit(&s.s_bar[wg]);
+    }
+    __syncwarp();
+  };
+
+  {
+    const Entry en = entry_of(a, walk.e);
+    for (int r = threadIdx.x / 32; r < RT; r += W * 4) query_row<C>(a, s.item[0], q_smem, en, walk.h, r);
+    if (threadIdx.x == 0)
+      describe_item<C>(a, s.item[0], en, walk,
+                       static_cast<int>(min(static_cast<int64_t>(en.tiles - walk.t), walk.left)), at0, total, grid);
+    fence_proxy_async_smem();
+  }
+
   for (uint32_t it = 0;; ++it) {
     const int buf = it & 1;
-    if (!wait_or_stop(&s.q_full[buf], (it >> 1) & 1, &s.stop, a.status)) bad = true;
+    if (it > 0 && !wait_or_stop(&s.q_full[buf], ((it - 1) >> 1) & 1, &s.stop, a.status)) bad = true;
     if (threadIdx.x < 128) s.poison[threadIdx.x] = kKvNoToken;
     if (bar_any(8, kAll, bad)) break;
     const ItemInfo<RT>& info = s.item[buf];
-    const int tiles = info.tiles;
+    const int tiles = uniform(info.tiles);
     if (tiles == 0) break;
     const int lo_pos = info.lo_pos, hi_pos = info.hi_pos;
 
@@ -645,6 +705,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     float vref = 0.0f, inv_vref = 0.0f;  // largest value scale so far, kProbScale / it
     bool pending = false;                // a product runs that was not waited for
     bool held = false;                   // TMEM holds output not yet in o[]
+    bool issued = false;                 // this tile's scores are under way
     // Waits for the product in flight (the phase of its tile's barriers) and
     // moves what TMEM holds to o[].
     auto flush = [&](uint32_t its_phase) {
@@ -665,23 +726,16 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 
     for (int i = (W - g0 % W + wg) % W; i < tiles; i += W) {
       const uint32_t g = g0 + i;
-      const int st = g % C::kStages;
+      const uint32_t st = g % C::kStages;
       if (!wait_or_stop(&s.full[st], (g / C::kStages) & 1, &s.stop, a.status)) bad = true;
-      uint8_t* const k_tile = ring + st * C::kStageBytes;
-      if (t == 0) {
-        tc_fence_after_sync();
-        const uint32_t ka = smem_u32(k_tile), qa = smem_u32(q_smem + buf * C::kQBytes);
-#pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks)
-          mma_f8_ss(tm_s, smem_desc_rows<D>(ka + ks * 32), smem_desc_rows<D>(qa + ks * 32), idesc_f8(N, false),
-                    ks > 0);
-        mma_commit(&s.s_bar[wg]);
-      }
+      __syncwarp();
+      if (!issued && warp == 3) issue_scores(st, buf);
       const StageMeta& meta = s.meta[st];
       const int pos = meta.base[my_slot] + my_off;
-      const float k_mul = meta.ks[my_slot], v_scale = meta.vs[my_slot], v_max = meta.vmax;
+      const float k_mul = meta.ks[my_slot], v_scale = meta.vs[my_slot];
       const bool masks = pos > lo_pos;
-      if (masks) clean_value_row<D>(k_tile + kKvTile * D, t, pos, pos > hi_pos, s.poison);
+      if (masks)
+        clean_value_row<D>(ring + st * C::kStageBytes + kKvTile * D, t, pos, pos > hi_pos, s.poison);
       if (!wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
       phase ^= 1;
       __syncwarp();
@@ -703,11 +757,13 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         }
       };
       scores(true);
+      tc_fence_before_sync();
       float top = kNegInf;
 #pragma unroll
       for (int r = 0; r < RT; ++r) top = fmaxf(top, e[r]);
-      if (bar_any(1 + wg, 128, top > kLag || v_max > vref)) {
-        // Move the references to the largest scores so far.
+      float v_mul = v_scale * inv_vref;
+      if (bar_any(1 + wg, 128, top + log2_approx(v_mul) > kMaxCode || (vref == 0.0f && v_scale > 0.0f))) {
+        // Move the references above the largest scores and value scales so far.
         scores(false);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -716,23 +772,31 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         }
         if (lane < RT) s.red[wg][lane][warp] = top;
         flush(phase);  // of the tile before: two flips ago
+        tc_fence_before_sync();
         bar_sync(1 + wg, 128);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const float4 v = *reinterpret_cast<const float4*>(s.red[wg][r]);
-          const float mn = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+          const float mn = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) + kMargin);
           const float alpha = exp2_approx(m[r] - mn);
           m[r] = mn;
           l[r] *= alpha;
           o[r] *= alpha;
           e[r] -= mn;
         }
-        if (v_max > vref) {
-          vref = v_max;
-          inv_vref = __fdiv_rn(kProbScale, vref);
-        }
+#pragma unroll
+        for (int k = 0; k < kKvMaxSlots; ++k)
+          if (k < a.spt) vref = fmaxf(vref, meta.vs[k]);
+        inv_vref = vref > 0.0f ? __fdiv_rn(kProbScale, vref) : 0.0f;
+        v_mul = v_scale * inv_vref;
       }
-      const float v_mul = v_scale * inv_vref;
+      // The scores have been read: the next tile's may overwrite them.
+      issued = false;
+      if (warp == 3 && i + W < tiles) {
+        const uint32_t g2 = g + W, st2 = g2 % C::kStages;
+        issued = __all_sync(0xFFFFFFFFu, mbar_try_wait(&s.full[st2], (g2 / C::kStages) & 1));
+        if (issued) issue_scores(st2, buf);
+      }
       uint32_t codes[N / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
@@ -768,93 +832,103 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       tc_fence_before_sync();
       fence_proxy_async_smem();
       bar_sync(1 + wg, 128);
-      if (t == 0) {
+      if (warp == 0) {
         tc_fence_after_sync();
-        const uint32_t va = smem_u32(k_tile + kKvTile * D);
+        const uint64_t va = smem_desc_rows<D>(ring_addr + st * C::kStageBytes + kKvTile * D);
+        const uint64_t pa = smem_desc_tokens(p_addr);
+        const uint32_t add = uniform(static_cast<uint32_t>(held));
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < kKvTile / 32; ++ks)
-          mma_f8_ss(tm_o, smem_desc_rows<D>(va + ks * 32 * D), smem_desc_tokens(p_addr + ks * 512),
-                    idesc_f8(N, true), held || ks > 0);
-        mma_commit(&s.o_bar[wg]);
-        mma_commit(&s.empty[st]);
+          for (int ks = 0; ks < kKvTile / 32; ++ks)
+            mma_f8_ss(tm_o, va + ks * (32 * D / 16), pa + ks * (512 / 16), idesc_f8(N, true), ks > 0 ? 1u : add);
+          mma_commit(&s.o_bar[wg]);
+          mma_commit(&s.empty[st]);
+        }
+        __syncwarp();
       }
       pending = held = true;
     }
     flush(phase ^ 1);
     g0 += tiles;
 
-    // Join the warpgroups: sums over the tokens, then the outputs, in order.
-    float mine = 0.0f;
+    // Join the warpgroups. The sums over the tokens first: in each step half
+    // of a lane's rows go to its partner, until a lane has one row.
+    {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+      for (int d = 16; d > 0; d /= 2) {
+        const bool up = lane & d;
 #pragma unroll
-      for (int d = 16; d > 0; d /= 2) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
-      if (lane == r) mine = l[r];
+        for (int r = 0; r < RT; ++r) {
+          if (r < RT * d / 32) {
+            const int o2 = r + RT * d / 32;
+            const float give = up ? l[r] : l[o2];
+            l[r] = (up ? l[o2] : l[r]) + __shfl_xor_sync(0xFFFFFFFFu, give, d);
+          }
+        }
+        if (RT * d < 32) l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], d);
+      }
+      if (lane % (32 / RT) == 0) s.red[wg][lane / (32 / RT)][warp] = l[0];
+      if (t == 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s.ml[0][wg][r] = m[r];
+      }
     }
-    bar_sync(1 + wg, 128);
-    if (lane < RT) s.red[wg][lane][warp] = mine;
-    bar_sync(1 + wg, 128);
+    bar_sync(8, kAll);
+    // Then the common reference, and each warpgroup's weight against it.
     if (t < RT) {
-      const float4 v = *reinterpret_cast<const float4*>(s.red[wg][t]);
-      s.ml[1][wg][t] = (v.x + v.y) + (v.z + v.w);
-    }
-    if (t == 0) {
+      float mx = s.ml[0][0][t];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) s.ml[0][wg][r] = m[r];
-    }
-    bar_sync(8, kAll);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float mx = s.ml[0][0][r];
-#pragma unroll
-      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][r]);
-      o[r] *= exp2_approx(m[r] - mx);
-      m[r] = mx;
-    }
-    float* const merge = reinterpret_cast<float*>(p_smem);
-    if (wg > 0 && t < D) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) merge[((wg - 1) * RT + r) * D + t] = o[r];
-    }
-    bar_sync(8, kAll);
-    if (wg == 0 && t < D) {
-#pragma unroll
-      for (int w = 0; w < W - 1; ++w)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) o[r] += merge[(w * RT + r) * D + t];
-    }
-    if (wg == 0) {
-      const int rows = info.rows, first_poison = t < D ? s.poison[t] : kKvNoToken;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (r >= rows) break;
+      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][t]);
+      s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
+      if (wg == 0) {
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          sum += s.ml[1][w][r] * exp2_approx(s.ml[0][w][r] - m[r]);
+          const float4 v = *reinterpret_cast<const float4*>(s.red[w][t]);
+          sum += ((v.x + v.y) + (v.z + v.w)) * exp2_approx(s.ml[0][w][t] - mx);
         }
+        s.mx[t] = mx;
+        s.sum[t] = sum;
+      }
+    }
+    bar_sync(1 + wg, 128);
+    float* const join = reinterpret_cast<float*>(p_smem);
+    const int rows = info.rows, first_poison = t < D ? s.poison[t] : kKvNoToken, part = info.slot;
+#pragma unroll
+    for (int r0 = 0; r0 < RT; r0 += C::kJoinRows) {
+      if (r0 > 0) bar_sync(8, kAll);
+      if (t < D) {
+#pragma unroll
+        for (int r = 0; r < C::kJoinRows; ++r)
+          join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r];
+      }
+      bar_sync(8, kAll);
+#pragma unroll 1
+      for (int r = r0 + wg; r < min(r0 + C::kJoinRows, rows); r += W) {
+        const float sum = s.sum[r], mx = s.mx[r];
         const int row_pos = info.row_pos[r];
-        float v = o[r];
-        if (row_pos >= first_poison) v = __int_as_float(0x7FC00000);
-        if (info.slot >= 0) {
-          float* const part = part_row(a, info.slot, rows, r);
-          if (t < D) part[t] = v;
+        const int64_t at = info.row_at[r];
+        float v = 0.0f;
+        if (t < D) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) v += join[(w * C::kJoinRows + r - r0) * D + t];
+          if (row_pos >= first_poison) v = __int_as_float(0x7FC00000);
+        }
+        if (part >= 0) {
+          float* const to = part_row(a, part, rows, r);
+          if (t < D) to[t] = v;
           if (t == 0) {
-            part[D] = row_pos < 0 ? kUnset : m[r];
-            part[D + 1] = row_pos < 0 ? 0.0f : sum;
+            to[D] = row_pos < 0 ? kUnset : mx;
+            to[D + 1] = row_pos < 0 ? 0.0f : sum;
           }
-        } else {
-          const int j = info.j0 + r / a.R;
-          if (j >= a.n) break;
+        } else if (at >= 0) {
           const bool none = row_pos < 0 || sum == 0.0f;
-          const int64_t at = (static_cast<int64_t>(info.b) * a.n + j) * a.Hq + info.h * a.R + r % a.R;
           if (t < D) {
             v = none ? 0.0f : __fdividef(v, sum);
             if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
             else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
           }
-          if (a.lse && t == 0)
-            a.lse[at] = none ? kNegInf : m[r] * 0.6931471805599453f + logf(sum);
+          if (a.lse && t == 0) a.lse[at] = none ? kNegInf : mx * 0.6931471805599453f + logf(sum);
         }
       }
     }
@@ -956,9 +1030,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     __syncthreads();
     if (warp < C::W * 4) {
-      attend_consume<C>(a, s, ring, q_smem, p_smem);
-    } else if (warp == C::W * 4) {
-      attend_produce<C>(a, &tm_k, &tm_v, s, ring, s.start);
+      attend_consume<C>(a, s, ring, q_smem, p_smem, s.start, lo - s.start.t, total, grid);
+    } else if (warp < C::W * 5) {
+      attend_produce<C>(a, &tm_k, &tm_v, s, ring, s.start, warp - C::W * 4);
     } else {
       attend_queries<C>(a, s, q_smem, s.start, lo - s.start.t, total, grid);
     }
