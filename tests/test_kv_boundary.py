@@ -11,6 +11,16 @@ OK, INVALID, GEOM, ARCH, MISALIGNED, CUDA, TIMEOUT = range(7)
 A = 1 << 20  # a fake, aligned address; never dereferenced
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_void_p) for x in ("k", "v", "k_scale", "v_scale", "page_table", "lens", "n_new")] \
+        + [("page_stride", ctypes.c_int64)] \
+        + [(x, ctypes.c_int32) for x in ("n_pages", "max_blocks", "B", "Hkv", "block", "D")]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(x, ctypes.c_int64) for x in ("stride_b", "stride_n", "stride_h")]
+
+
 @pytest.fixture(scope="module")
 def lib():
     _build.build()
@@ -23,13 +33,13 @@ def cache(**kw):
     f.update(kw)
     if "page_stride" not in kw:
         f["page_stride"] = f["Hkv"] * f["block"] * f["D"]
-    return tbs._KvCache(*[f[n] for n, _ in tbs._KvCache._fields_])
+    return Cache(*[f[n] for n, _ in Cache._fields_])
 
 
 def rows(**kw):
     f = dict(data=A, stride_b=1024, stride_n=1024, stride_h=128)
     f.update(kw)
-    return tbs._Rows(*[f[n] for n, _ in tbs._Rows._fields_])
+    return Rows(*[f[n] for n, _ in Rows._fields_])
 
 
 def append(lib, c=None, k=None, v=None, q=None, n=1, Hq=8, dtype=0, cos=A, sin=A, rot=128, max_pos=100, q_out=None, kb=None):

@@ -432,6 +432,55 @@ def test_indexes_outside_are_reported(tbs):
     assert torch.equal(args[0], before)
 
 
+def test_binding_refuses_wrong_tensors(tbs):
+    c = kc.make_cache([100, 30], 2, 32, 64, seed=17)
+    args, _ = on_gpu(c)
+    q = torch.zeros((2, 3, 4, 64), dtype=torch.float16, device="cuda")
+    kv = torch.zeros((2, 3, 2, 64), dtype=torch.float16, device="cuda")
+    cos = torch.ones((100, 32), device="cuda")
+
+    def bad(i, t):
+        a = list(args)
+        a[i] = t
+        return a
+    wrong = [bad(0, args[0].half()), bad(1, args[1][:, :1]), bad(1, args[1][:-1]), bad(0, args[0].transpose(2, 3)),
+             bad(2, args[2].double()), bad(3, args[3][:-1]), bad(4, args[4].long()), bad(4, args[4][:1]),
+             bad(4, args[4].t().contiguous().t()), bad(5, args[5].long()), bad(5, args[5].cpu()), bad(2, args[2].cpu())]
+    for a in wrong:
+        with pytest.raises(ValueError):
+            tbs.qsa_kv_attend(q, *a)
+        with pytest.raises(ValueError):
+            tbs.qsa_kv_append(kv, kv, *a)
+    ids = torch.zeros((2, 1, 3, 4), dtype=torch.int32, device="cuda")
+    for kw in (dict(ids=ids.long()), dict(ids=ids[:1]), dict(ids=ids[:, :, :2]), dict(ids=ids[..., :0]), dict(ids=ids[0]),
+               dict(ids=ids.expand(2, 2, 3, 4)), dict(ids=torch.zeros((2, 4, 3, 4), dtype=torch.int32, device="cuda")),
+               dict(out=q.bfloat16()), dict(out=q[:1]), dict(out=q.cpu()), dict(lse=q[..., 0]),
+               dict(lse=torch.zeros((2, 3, 2), device="cuda")), dict(n_new=args[5][:1]), dict(n_new=args[5].cpu()),
+               dict(workspace=torch.zeros(8, device="cuda"))):
+        with pytest.raises(ValueError):
+            tbs.qsa_kv_attend(q, *args, **kw)
+    for x in (q.float(), q[:1], q[..., :32], q[0], q.cpu(), q.transpose(2, 3).contiguous().transpose(2, 3)):
+        with pytest.raises(ValueError):
+            tbs.qsa_kv_attend(x, *args)
+    for a, kw in (((kv, kv[:, :2]), {}), ((kv, kv.bfloat16()), {}), ((kv[:, :, :1], kv), {}), ((kv, kv), dict(q_out=q)),
+                  ((kv, kv), dict(q=q.bfloat16())), ((kv, kv), dict(q=q, q_out=q[:1])),
+                  ((kv, kv), dict(cos=cos, sin=cos[:50])), ((kv, kv), dict(cos=cos.half(), sin=cos.half())),
+                  ((kv, kv), dict(kb=torch.zeros((2, 2, 1, 64), dtype=torch.float16, device="cuda")))):
+        with pytest.raises(ValueError):
+            tbs.qsa_kv_append(*a, *args, **kw)
+    with pytest.raises(TypeError):
+        tbs.qsa_kv_append(kv, kv, *args, cos=cos)
+    with pytest.raises(tbs.QsaError):
+        tbs.qsa_kv_attend(q, *args, scale=float("inf"))
+    with pytest.raises(tbs.QsaError):
+        tbs.qsa_kv_attend(q, *args, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(tbs.QsaError):   # rows that are not 16-byte aligned
+        tbs.qsa_kv_attend(torch.zeros(2 * 3 * 4 * 64 + 4, dtype=torch.float16, device="cuda")[4:].view(2, 3, 4, 64), *args)
+    with pytest.raises(tbs.QsaError):
+        tbs.qsa_kv_append(kv, kv, *args, cos=cos[:, :20].contiguous(), sin=cos[:, :20].contiguous())
+    assert tbs.qsa_kv_attend(q[:, :0], *args).shape == (2, 0, 4, 64)
+
+
 def test_arm_names_the_kernels(tbs):
     c = kc.make_cache([200], 1, 64, 128, seed=17)
     args, _ = on_gpu(c)

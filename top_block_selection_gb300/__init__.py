@@ -10,6 +10,8 @@ If libqsa.so is missing or cannot load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 __all__ = [
@@ -39,18 +41,6 @@ EXPORTED_SYMBOLS = (
 STATUS_NAMES = {0: "QSA_OK", 1: "QSA_ERR_INVALID_ARG", 2: "QSA_ERR_UNSUPPORTED_GEOMETRY",
                 3: "QSA_ERR_UNSUPPORTED_ARCH", 4: "QSA_ERR_MISALIGNED", 5: "QSA_ERR_CUDA",
                 6: "QSA_ERR_TIMEOUT"}
-
-
-class _KvCache(ctypes.Structure):
-    """qsa_kv_cache of include/qsa.h."""
-    _fields_ = [(x, ctypes.c_void_p) for x in ("k", "v", "k_scale", "v_scale", "page_table", "lens", "n_new")] \
-        + [("page_stride", ctypes.c_int64)] \
-        + [(x, ctypes.c_int32) for x in ("n_pages", "max_blocks", "B", "Hkv", "block", "D")]
-
-
-class _Rows(ctypes.Structure):
-    """qsa_rows of include/qsa.h."""
-    _fields_ = [("data", ctypes.c_void_p)] + [(x, ctypes.c_int64) for x in ("stride_b", "stride_n", "stride_h")]
 
 
 class QsaError(RuntimeError):
@@ -103,11 +93,10 @@ def load_library():
         "qsa_split_reduce": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp, ctypes.c_size_t,
                                             vp]),
         "qsa_split_reduce_static": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp]),
-        "qsa_kv_append": (ctypes.c_int, [ctypes.POINTER(_KvCache)] + [ctypes.POINTER(_Rows)] * 3
-                          + [i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
+        "qsa_kv_append": (ctypes.c_int, [vp] * 4 + [i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
         "qsa_kv_attend_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
-        "qsa_kv_attend": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rows), i32, i32, i32,
-                                         ctypes.c_float, vp, i32, i32, vp, vp, vp, ctypes.c_size_t, vp]),
+        "qsa_kv_attend": (ctypes.c_int, [vp, vp, i32, i32, i32, ctypes.c_float, vp, i32, i32, vp, vp, vp,
+                                         ctypes.c_size_t, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -124,9 +113,15 @@ def _check(status: int, where: str):
         raise QsaError(status, where, detail)
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_of(t):
@@ -582,65 +577,26 @@ def qsa_split_reduce(partial_max, partial_sum, partial_out, out=None, workspace=
 
 
 # ------------------------------------------------- the paged 8-bit cache
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+# These calls run once per layer and token of a serving loop, so their tensors
+# are checked and marshalled by a compiled module (csrc/kv_binding.cpp).
+_KV = None
 
 
-def _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, lens, n_new):
-    """Checks the cache tensors and marshals them; returns the struct (the
-    tensors must outlive the call)."""
-    torch = _torch()
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.dim() != 4 or not t.is_cuda:
-            raise ValueError(f"{name} must be a 4-D CUDA float8_e4m3fn or uint8 tensor [n_pages, Hkv, block, D]")
-        if t.shape[0] > 0 and not t[0].is_contiguous():
-            raise ValueError(f"every page of {name} must be contiguous")
-    n_pages, Hkv, block, D = k_cache.shape
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or v_cache.stride(0) != k_cache.stride(0):
-        raise ValueError("k_cache and v_cache must have the same shape and page stride")
-    _need(k_scale, torch.float32, 2, "k_scale")
-    _need(v_scale, torch.float32, 2, "v_scale")
-    _need(page_table, torch.int32, 2, "page_table")
-    _need(lens, torch.int32, 1, "lens")
-    B = lens.shape[0]
-    if tuple(k_scale.shape) != (n_pages, Hkv) or tuple(v_scale.shape) != (n_pages, Hkv):
-        raise ValueError(f"k_scale and v_scale must be [{n_pages}, {Hkv}]")
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [{B}, max_blocks]")
-    if n_new is not None:
-        _need(n_new, torch.int32, 1, "n_new")
-        if n_new.shape[0] != B:
-            raise ValueError(f"n_new must be [{B}]")
-    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
-                 lens=lens, n_new=n_new)
-    stride = k_cache.stride(0) if n_pages > 1 else Hkv * block * D
-    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                    page_table.data_ptr(), lens.data_ptr(), n_new.data_ptr() if n_new is not None else None,
-                    stride, n_pages, page_table.shape[1], B, Hkv, block, D)
-
-
-def _rows(t, B, heads, D, name):
-    """Checks rows [B, n, heads, D] (any strides but the last) and marshals them."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.float16, torch.bfloat16) or t.dim() != 4 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 4-D CUDA float16 or bfloat16 tensor")
-    if t.shape[0] != B or t.shape[3] != D or (heads is not None and t.shape[2] != heads):
-        raise ValueError(f"{name} must be [{B}, n, {'Hq' if heads is None else heads}, {D}], is {tuple(t.shape)}")
-    # The stride of an axis of one element means nothing and may be anything.
-    stride = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-    if t.numel() and t.stride(3) != 1:
-        raise ValueError(f"{name} must be contiguous in its last axis")
-    return _Rows(t.data_ptr(), *stride)
-
-
-def _dtype_code(t):
-    return 1 if t.dtype == _torch().bfloat16 else 0
+def _kv_binding():
+    global _KV
+    lib = load_library()
+    _torch()
+    path = os.path.join(_HERE, "lib", "_qsa_kv.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_qsa_kv.so not found at {path}: build it with "
+                           "`python -m top_block_selection_gb300._build`")
+    loader = importlib.machinery.ExtensionFileLoader("_qsa_kv", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_qsa_kv", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
+                  for fn in (lib.qsa_kv_append, lib.qsa_kv_attend, lib.qsa_kv_attend_workspace_bytes)))
+    _KV = module
+    return module
 
 
 def qsa_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cos=None, sin=None,
@@ -652,53 +608,11 @@ def qsa_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
     q [B, n, Hq, D], if given, is rotated into q_out (allocated if not given).
     kb, an optional f16 [B, Hkv, max_blocks, D], receives the block keys of the
     blocks written to. Returns q_out (None without q)."""
-    torch = _torch()
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, lens, n_new)
-    dev = k_cache.device
-    rk = _rows(k, cache.B, cache.Hkv, cache.D, "k")
-    rv = _rows(v, cache.B, cache.Hkv, cache.D, "v")
-    n = k.shape[1]
-    if v.shape[1] != n or v.dtype != k.dtype:
-        raise ValueError("v must have k's shape and dtype")
-    rot = max_pos = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin must be given together")
-    if cos is not None:
-        _need(cos, torch.float32, 2, "cos")
-        _need(sin, torch.float32, 2, "sin")
-        if tuple(sin.shape) != tuple(cos.shape):
-            raise ValueError("sin must be shaped like cos")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    rq = None
-    Hq = 0
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out needs q")
-    else:
-        rq = _rows(q, cache.B, None, cache.D, "q")
-        Hq = q.shape[2]
-        if q.shape[1] != n or q.dtype != k.dtype:
-            raise ValueError("q must have k's row count and dtype")
-        if q_out is None:
-            q_out = torch.empty((cache.B, n, Hq, cache.D), dtype=q.dtype, device=dev)
-        _need(q_out, q.dtype, 4, "q_out")
-        if tuple(q_out.shape) != tuple(q.shape):
-            raise ValueError("q_out must be shaped like q")
-    if kb is not None:
-        _need(kb, torch.float16, 4, "kb")
-        if tuple(kb.shape) != (cache.B, cache.Hkv, cache.max_blocks, cache.D):
-            raise ValueError(f"kb must be [{cache.B}, {cache.Hkv}, {cache.max_blocks}, {cache.D}]")
-    _same_device(dev, k=k, v=v, q=q, q_out=q_out, kb=kb, cos=cos, sin=sin)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        _check(lib.qsa_kv_append(ctypes.byref(cache), ctypes.byref(rk), ctypes.byref(rv),
-                                 ctypes.byref(rq) if rq is not None else None, n, Hq, _dtype_code(k),
-                                 cos.data_ptr() if cos is not None else None,
-                                 sin.data_ptr() if sin is not None else None, rot, max_pos,
-                                 1 if interleaved else 0, q_out.data_ptr() if q_out is not None else None,
-                                 kb.data_ptr() if kb is not None else None, _stream_of(k_cache)),
-               "qsa_kv_append")
-    return q_out
+    r = (_KV or _kv_binding()).append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cos, sin, interleaved,
+                                      n_new, q, q_out, kb)
+    if r.__class__ is int:
+        _check(r, "qsa_kv_append")
+    return r
 
 
 def qsa_kv_attend_workspace_bytes(B: int, n: int, Hq: int, Hkv: int, D: int) -> int:
@@ -716,37 +630,8 @@ def qsa_kv_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids=N
     [B, n, Hq], receives the log of the softmax sums. workspace: a CUDA uint8
     tensor of qsa_kv_attend_workspace_bytes, allocated here when not given.
     Returns out [B, n, Hq, D] of q's dtype."""
-    torch = _torch()
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, lens, n_new)
-    dev = k_cache.device
-    rq = _rows(q, cache.B, None, cache.D, "q")
-    n, Hq = q.shape[1], q.shape[2]
-    lists = k = 0
-    if ids is not None:
-        _need(ids, torch.int32, 4, "ids")
-        lists, k = ids.shape[1], ids.shape[3]
-        if ids.shape[0] != cache.B or ids.shape[2] != n or lists not in (1, cache.Hkv) or k < 1:
-            raise ValueError(f"ids must be [{cache.B}, 1 or {cache.Hkv}, {n}, k]")
-    if out is None:
-        out = torch.empty((cache.B, n, Hq, cache.D), dtype=q.dtype, device=dev)
-    _need(out, q.dtype, 4, "out")
-    if tuple(out.shape) != tuple(q.shape):
-        raise ValueError("out must be shaped like q")
-    if lse is not None:
-        _need(lse, torch.float32, 3, "lse")
-        if tuple(lse.shape) != (cache.B, n, Hq):
-            raise ValueError(f"lse must be [{cache.B}, {n}, {Hq}]")
-    lib = load_library()
-    if workspace is None:
-        need = int(lib.qsa_kv_attend_workspace_bytes(cache.B, n, Hq, cache.Hkv, cache.D))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
-    _same_device(dev, q=q, ids=ids, out=out, lse=lse, workspace=workspace)
-    with torch.cuda.device(dev):
-        _check(lib.qsa_kv_attend(ctypes.byref(cache), ctypes.byref(rq), n, Hq, _dtype_code(q),
-                                 cache.D ** -0.5 if scale is None else float(scale),
-                                 ids.data_ptr() if ids is not None else None, lists, k, out.data_ptr(),
-                                 lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-                                 workspace.numel(), _stream_of(k_cache)), "qsa_kv_attend")
-    return out
+    r = (_KV or _kv_binding()).attend(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids, scale, n_new, out,
+                                      lse, workspace)
+    if r.__class__ is int:
+        _check(r, "qsa_kv_attend")
+    return r

@@ -2,16 +2,20 @@
 
 Each translation unit compiles in parallel; the objects link into
 ``top_block_selection_gb300/lib/libqsa.so`` with the CUDA runtime linked
-statically, so the library needs only the NVIDIA driver at run time.
+statically, so the library needs only the NVIDIA driver at run time. Beside it,
+``_qsa_kv.so`` is the CPython module through which PyTorch tensors reach the
+paged-cache calls (g++, PyTorch's headers).
 Run ``python -m top_block_selection_gb300._build`` or call ``build()``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIBPATH = os.path.join(LIBDIR, "libqsa.so")
+BINDINGPATH = os.path.join(LIBDIR, "_qsa_kv.so")
 
 SOURCES = ["qsa_runtime.cu", "score_tc.cu", "select.cu", "convert.cu", "fused.cu", "fused_h1.cu",
            "fused_h2.cu", "fused_h4.cu", "fused_h8.cu", "fused_h16.cu", "fused_h32.cu",
@@ -46,6 +51,16 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command(src: str) -> list:
+    """g++ command of the CPython module that marshals PyTorch tensors."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *(x for i in include for x in ("-isystem", i)), src, "-o",
+            BINDINGPATH, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
     """Compile (if stale) and return the path of libqsa.so."""
     nvcc = _nvcc()
@@ -59,13 +74,16 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         objs.append(op)
         if _stale(op, [sp, __file__] + hdrs):
             jobs.append([nvcc, *ARCH, *COMMON, *extra_flags, "-c", sp, "-o", op])
+    binding = os.path.join(CSRC, "kv_binding.cpp")
+    if _stale(BINDINGPATH, [binding, __file__, os.path.join(INCLUDE, "qsa.h")]):
+        jobs.append(_binding_command(binding))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for cmd, res in zip(jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs)):
                 if verbose and (res.stdout or res.stderr):
                     sys.stderr.write(res.stdout + res.stderr)
                 if res.returncode != 0:
-                    raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+                    raise RuntimeError("compilation failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     if jobs or _stale(LIBPATH, objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIBPATH, *objs, "-lrt", "-ldl", "-lpthread"]
         res = subprocess.run(cmd, capture_output=True, text=True)

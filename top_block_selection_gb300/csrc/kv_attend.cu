@@ -123,6 +123,8 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   cudaError_t e = form(rt, tk, tv, a, grid, false, stream);
   if (e != cudaSuccess) return e;
   plan_add("kv_attend_kernel");
+  // Items of one tile are never split.
+  if (a.fixed == 1 || (a.fixed == 0 && p.cache.max_blocks * p.cache.block <= kKvTile)) return cudaSuccess;
   e = launch_pdl(kv_combine_kernel, dim3(grid, a.qt * a.R), dim3(kCombineThreads), 0, stream, a);
   if (e == cudaSuccess) plan_add("kv_combine_kernel");
   return e;

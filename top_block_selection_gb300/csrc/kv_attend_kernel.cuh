@@ -65,8 +65,8 @@ struct AttendArgs {
   void* out;
   float* lse;
   const int32_t* ids;
-  float* parts;      // [2 * grid][rows][D + 2]: outputs, then maxima, then sums
-  int32_t* jobs;     // [grid][4]: entry, head, last CTA of a split item, or -1
+  float* parts;      // [2 * grid][rows][D + 2]: of each row its output, reference and sum
+  int32_t* jobs;     // [grid][4]: entry, head, last CTA of an item that this CTA begins and others end; or -1
   uint32_t* status;
   float scale_log2;
   int32_t n, Hq, R;
@@ -80,6 +80,13 @@ struct AttendArgs {
 // Row r of partial `slot`: D outputs, then all rows' maxima and sums.
 __device__ __forceinline__ float* part_row(const AttendArgs& a, int slot, int rows, int r) {
   return a.parts + (static_cast<int64_t>(slot) * rows + r) * (a.c.D + 2);
+}
+
+// a / b for a >= 0, b > 0, in 32 bits where they suffice.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((static_cast<uint64_t>(a) | static_cast<uint64_t>(b)) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // What the query tile `e` sees: its rows' queries j0 .. j0 + nq - 1 (those that
@@ -108,6 +115,10 @@ __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
 struct Walk {
   int32_t e, h, t;
   int64_t left;
+};
+struct Start {
+  Walk walk;
+  Entry entry;  // of walk.e
 };
 
 // ------------------------------------------------------------ tcgen05 pieces
@@ -349,7 +360,7 @@ struct AttendShared {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_bar[C::W], o_bar[C::W];
   uint64_t scan[C::kThreads / 32 + 1];
-  Walk start;
+  Start start;
   uint32_t tmem;
   uint32_t stop;
 };
@@ -372,7 +383,7 @@ __device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads) {
 // at a time, one per lane, then two TMA loads a block.
 template <class C>
 __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                               AttendShared<C>& s, uint8_t* ring, Walk w, int p) {
+                               AttendShared<C>& s, uint8_t* ring, int p) {
   constexpr int W = C::W;
   const int lane = threadIdx.x % 32;
   const int spt = a.spt, per_batch = 32 / spt;
@@ -381,8 +392,9 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
   uint32_t last = 0;       // tiles of this warp so far
   uint32_t last_g[C::kStages / W];
   bool ok = true;
-  Entry en{};
-  int en_of = -1;
+  Walk w = s.start.walk;
+  Entry en = s.start.entry;
+  int en_of = w.e;
   while (w.left > 0 && ok) {
     if (en_of != w.e) {
       en = entry_of(a, w.e);
@@ -548,19 +560,21 @@ __device__ __forceinline__ void describe_item(const AttendArgs& a, ItemInfo<C::R
     int32_t* const job = a.jobs + 4 * blockIdx.x;
     job[0] = w.e;
     job[1] = w.h;
-    job[2] = static_cast<int32_t>(((at + en.tiles) * grid - 1) / total);  // the CTA that has its last tile
+    // Tile g belongs to the last CTA c with total * c / grid <= g.
+    job[2] = static_cast<int32_t>(divide((at + en.tiles) * grid - 1, total));
   }
 }
 
 // The query warp: every item of the CTA's walk but the first (which the
 // warpgroups prepare themselves), one ahead of its use.
 template <class C>
-__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, Walk w, int64_t at,
-                               int64_t total, int grid) {
+__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, int64_t at, int64_t total,
+                               int grid) {
   const int lane = threadIdx.x % 32;
   bool ok = true;
-  Entry en{};
-  int en_of = -1;
+  Walk w = s.start.walk;
+  Entry en = s.start.entry;
+  int en_of = w.e;
   for (uint32_t it = 0;; ++it) {
     const int buf = it & 1;
     if (it >= 2) ok = wait_or_stop(&s.q_empty[buf], ((it >> 1) & 1) ^ 1, &s.stop, a.status);
@@ -619,6 +633,19 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
+// One finished row: thread t < D has dimension t.
+__device__ __forceinline__ void write_row(const AttendArgs& a, int64_t at, bool seen, float v, float mx, float sum,
+                                          int t, int D) {
+  if (at < 0) return;
+  const bool none = !seen || sum == 0.0f;
+  if (t < D) {
+    v = none ? 0.0f : __fdividef(v, sum);
+    if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
+  }
+  if (a.lse && t == 0) a.lse[at] = none ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
+}
+
 // The columns of RT rows at `taddr`, their T terms added, a few rows at a time
 // (the terms of all would not fit in registers beside the softmax state).
 template <class C>
@@ -648,7 +675,7 @@ constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
-                               uint8_t* p_smem, const Walk& walk, int64_t at0, int64_t total, int grid) {
+                               uint8_t* p_smem, int64_t at0, int64_t total, int grid) {
   constexpr int RT = C::RT, N = C::N, W = C::W, D = C::D;
   constexpr int kAll = W * 128;
   const int wg = uniform(static_cast<int>(threadIdx.x / 128)), warp = uniform(static_cast<int>(threadIdx.x / 32 % 4));
@@ -677,9 +704,10 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   };
 
   {
-    const Entry en = entry_of(a, walk.e);
+    const Walk walk = s.start.walk;
+    const Entry en = s.start.entry;
     for (int r = threadIdx.x / 32; r < RT; r += W * 4) query_row<C>(a, s.item[0], q_smem, en, walk.h, r);
-    if (threadIdx.x == 0)
+    if (threadIdx.x == W * 128 - 1)
       describe_item<C>(a, s.item[0], en, walk,
                        static_cast<int>(min(static_cast<int64_t>(en.tiles - walk.t), walk.left)), at0, total, grid);
     fence_proxy_async_smem();
@@ -907,7 +935,6 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       for (int r = r0 + wg; r < min(r0 + C::kJoinRows, rows); r += W) {
         const float sum = s.sum[r], mx = s.mx[r];
         const int row_pos = info.row_pos[r];
-        const int64_t at = info.row_at[r];
         float v = 0.0f;
         if (t < D) {
 #pragma unroll
@@ -921,14 +948,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
             to[D] = row_pos < 0 ? kUnset : mx;
             to[D + 1] = row_pos < 0 ? 0.0f : sum;
           }
-        } else if (at >= 0) {
-          const bool none = row_pos < 0 || sum == 0.0f;
-          if (t < D) {
-            v = none ? 0.0f : __fdividef(v, sum);
-            if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
-            else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
-          }
-          if (a.lse && t == 0) a.lse[at] = none ? kNegInf : mx * 0.6931471805599453f + logf(sum);
+        } else {
+          write_row(a, info.row_at[r], row_pos >= 0, v, mx, sum, t, D);
         }
       }
     }
@@ -951,6 +972,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   pdl_launch_dependents();
   if (tid == 0) {
+    a.jobs[4 * blockIdx.x] = -1;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&s.full[i], 2);
       mbar_init(&s.empty[i], 1);
@@ -967,7 +989,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     fence_mbarrier_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    a.jobs[4 * blockIdx.x] = -1;
   }
   if (warp == 0) {
     tmem_alloc(&s.tmem, C::kTmemCols);
@@ -979,10 +1000,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
   const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
   uint64_t sum = 0;
+  Entry mine{};
   if (a.fixed > 0) {
     sum = static_cast<uint64_t>(e1 - e0) * a.fixed;
   } else {
-    for (int64_t e = e0; e < e1; ++e) sum += entry_of(a, static_cast<int>(e)).tiles;
+    for (int64_t e = e0; e < e1; ++e) {
+      mine = entry_of(a, static_cast<int>(e));
+      sum += mine.tiles;
+    }
   }
   uint64_t before = sum;
 #pragma unroll
@@ -1004,37 +1029,39 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int64_t total = static_cast<int64_t>(all) * a.c.Hkv;
   const int grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
   const int cta = blockIdx.x;
-  const int64_t lo = cta < grid ? total * cta / grid : 0, hi = cta < grid ? total * (cta + 1) / grid : 0;
+  const int64_t lo = cta < grid ? divide(total * cta, grid) : 0, hi = cta < grid ? divide(total * (cta + 1), grid) : 0;
   if (hi > lo) {
-    uint64_t at = before * a.c.Hkv;
-    if (static_cast<int64_t>(at) <= lo && lo < static_cast<int64_t>((before + sum) * a.c.Hkv)) {
+    int64_t at = static_cast<int64_t>(before) * a.c.Hkv;
+    if (at <= lo && lo < at + static_cast<int64_t>(sum) * a.c.Hkv) {
+      // This thread's entries hold the CTA's first tile.
       int64_t e = e0;
-      int tiles = a.fixed;
       if (a.fixed > 0) {
-        const int64_t skip = (lo - static_cast<int64_t>(at)) / (static_cast<int64_t>(a.fixed) * a.c.Hkv);
+        const int64_t each = static_cast<int64_t>(a.fixed) * a.c.Hkv, skip = divide(lo - at, each);
         e += skip;
-        at += static_cast<uint64_t>(skip) * a.fixed * a.c.Hkv;
-      } else {
+        at += skip * each;
+        mine = entry_of(a, static_cast<int>(e));
+      } else if (per > 1) {
         for (;; ++e) {
-          tiles = entry_of(a, static_cast<int>(e)).tiles;
-          const uint64_t next = at + static_cast<uint64_t>(tiles) * a.c.Hkv;
-          if (lo < static_cast<int64_t>(next)) break;
-          at = next;
+          mine = entry_of(a, static_cast<int>(e));
+          if (lo < at + static_cast<int64_t>(mine.tiles) * a.c.Hkv) break;
+          at += static_cast<int64_t>(mine.tiles) * a.c.Hkv;
         }
       }
-      const int64_t off = lo - static_cast<int64_t>(at);
-      s.start.e = static_cast<int32_t>(e);
-      s.start.h = static_cast<int32_t>(off / tiles);
-      s.start.t = static_cast<int32_t>(off % tiles);
-      s.start.left = hi - lo;
+      const int64_t off = lo - at;
+      const int h = static_cast<int>(divide(off, mine.tiles));
+      s.start.walk.e = static_cast<int32_t>(e);
+      s.start.walk.h = h;
+      s.start.walk.t = static_cast<int32_t>(off - static_cast<int64_t>(h) * mine.tiles);
+      s.start.walk.left = hi - lo;
+      s.start.entry = mine;
     }
     __syncthreads();
     if (warp < C::W * 4) {
-      attend_consume<C>(a, s, ring, q_smem, p_smem, s.start, lo - s.start.t, total, grid);
+      attend_consume<C>(a, s, ring, q_smem, p_smem, lo - s.start.walk.t, total, grid);
     } else if (warp < C::W * 5) {
-      attend_produce<C>(a, &tm_k, &tm_v, s, ring, s.start, warp - C::W * 4);
+      attend_produce<C>(a, &tm_k, &tm_v, s, ring, warp - C::W * 4);
     } else {
-      attend_queries<C>(a, s, q_smem, s.start, lo - s.start.t, total, grid);
+      attend_queries<C>(a, s, q_smem, lo - s.start.walk.t, total, grid);
     }
   }
   tc_fence_before_sync();
