@@ -106,8 +106,9 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   a.spt = kKvTile / p.cache.block;
   a.bf16 = p.bf16;
   // Chosen blocks are each query's own; over the whole cache, consecutive
-  // queries of a sequence share a tile as far as the rows go.
-  a.qt = p.ids ? 1 : std::min(p.n, kKvMaxGroup / a.R);
+  // queries of a sequence share a tile, up to 16 rows: the form of 32 rows holds
+  // too much state for its threads and takes more than twice as long a tile.
+  a.qt = p.ids ? 1 : std::max(1, std::min(p.n, 16 / a.R));
   a.n_qt = (p.n + a.qt - 1) / a.qt;
   a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
   const int rt = rows_form(a.qt * a.R);

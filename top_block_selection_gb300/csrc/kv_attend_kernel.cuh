@@ -96,7 +96,7 @@ struct Entry {
 };
 __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
   Entry t;
-  t.b = e / a.n_qt;
+  t.b = a.n_qt > 1 ? e / a.n_qt : e;
   t.j0 = (e - t.b * a.n_qt) * a.qt;
   const Span s = span_of(a.c, t.b, a.n);
   t.nq = min(t.j0 + a.qt, s.n_new) - t.j0;
@@ -205,6 +205,19 @@ __device__ __forceinline__ void tmem_ld_cols<32>(uint32_t taddr, float (&r)[32])
 // ------------------------------------------------------------- small pieces
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Whether a phase has completed, without waiting for it at all (try_wait may
+// hold the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -354,12 +367,12 @@ struct AttendShared {
   StageMeta meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
   alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
-  float mx[C::RT], sum[C::RT];   // joined
+  float mx[C::RT], sum[C::RT], inv[C::RT];  // joined, 1 / sum
   int32_t poison[128];           // first position whose value code is NaN, per dimension
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_bar[C::W], o_bar[C::W];
-  uint64_t scan[C::kThreads / 32 + 1];
+  int64_t scan[C::kThreads / 32];
   Start start;
   uint32_t tmem;
   uint32_t stop;
@@ -383,7 +396,7 @@ __device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads) {
 // at a time, one per lane, then two TMA loads a block.
 template <class C>
 __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                               AttendShared<C>& s, uint8_t* ring, int p) {
+                               AttendShared<C>& s, uint8_t* ring, const Start& start, int p) {
   constexpr int W = C::W;
   const int lane = threadIdx.x % 32;
   const int spt = a.spt, per_batch = 32 / spt;
@@ -392,8 +405,8 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
   uint32_t last = 0;       // tiles of this warp so far
   uint32_t last_g[C::kStages / W];
   bool ok = true;
-  Walk w = s.start.walk;
-  Entry en = s.start.entry;
+  Walk w = start.walk;
+  Entry en = start.entry;
   int en_of = w.e;
   while (w.left > 0 && ok) {
     if (en_of != w.e) {
@@ -476,71 +489,82 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
 }
 
 // --------------------------------------------------------- the query's terms
-// Row r of the query tile `en` for KV head h, by one warp: scaled by a power
-// of two to the range of e4m3 and split in terms. Rows that are not there are
-// zero. `dst` holds rows of D bytes, term after term.
-template <class C>
-__device__ __forceinline__ void query_row(const AttendArgs& a, ItemInfo<C::RT>& info, uint8_t* dst, const Entry& en,
-                                          int h, int r) {
+// Rows r0, r0 + step, ... (K of them, below RT) of the query tile `en` for KV
+// head h, by one warp: all loaded, then each scaled by a power of two to the
+// range of e4m3 and split in terms. Rows that are not there are zero. `dst`
+// holds rows of D bytes, term after term.
+template <class C, int K>
+__device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>& info, uint8_t* dst, const Entry& en,
+                                           int h, int r0, int step) {
   constexpr int kPer = C::D / 32;  // elements of a lane
   const int lane = threadIdx.x % 32, rows = a.qt * a.R;
-  const int j = r / a.R, head = h * a.R + (r - j * a.R);
-  const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
-  float x[kPer];
+  uint32_t u[K][kPer / 2];
+  int row_pos[K];
+  int64_t row_at[K];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
-  if (there) {
-    const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
-                                static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
-                                lane * kPer;
-    uint32_t u[kPer / 2];
-    if (kPer == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-      u[0] = v.x;
-      u[kPer / 2 - 1] = v.y;
-    } else {
-      u[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-    }
+  for (int k = 0; k < K; ++k) {
+    const int r = r0 + k * step, j = a.qt > 1 ? r / a.R : 0, head = h * a.R + (r - j * a.R);
+    const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
+    row_pos[k] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
+    row_at[k] = r < rows && en.j0 + j < a.n ? (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + head : -1;
 #pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) {
-      if (a.bf16) {
-        x[2 * e] = __uint_as_float(u[e] << 16);
-        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    for (int e = 0; e < kPer / 2; ++e) u[k][e] = 0;
+    if (there) {
+      const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
+                                  static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
+                                  lane * kPer;
+      if (kPer == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        u[k][0] = v.x;
+        u[k][kPer / 2 - 1] = v.y;
       } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+        u[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
       }
     }
   }
-  float m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) m = fmaxf(m, fabsf(x[e]));
-  const float t = pow2_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
-  const float inv = __uint_as_float((254u << 23) - __float_as_uint(t));
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    x[e] *= inv;
-    if (isinf(x[e])) x[e] = __int_as_float(0x7FC00000);
-  }
-#pragma unroll
-  for (int term = 0; term < C::T; ++term) {
-    uint32_t code[kPer / 2];
+  for (int k = 0; k < K; ++k) {
+    const int r = r0 + k * step;
+    if (r >= C::RT) break;
+    float x[kPer], m = 0.0f;
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) {
-      code[e] = e4m3x2(x[2 * e], x[2 * e + 1]);
-      const float2 back = e4m3x2_to_float2(code[e]);
-      x[2 * e] -= back.x;
-      x[2 * e + 1] -= back.y;
+      if (a.bf16) {
+        x[2 * e] = __uint_as_float(u[k][e] << 16);
+        x[2 * e + 1] = __uint_as_float(u[k][e] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k][e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+      }
+      m = fmaxf(m, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
     }
-    uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
-    if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
-    else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
-  }
-  if (lane == 0) {
-    info.row_pos[r] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
-    info.row_mul[r] = t * a.scale_log2;
-    info.row_at[r] = r < rows && en.j0 + j < a.n ? (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + head : -1;
+    const float t = pow2_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(t));
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      x[e] *= inv;
+      if (isinf(x[e])) x[e] = __int_as_float(0x7FC00000);
+    }
+#pragma unroll
+    for (int term = 0; term < C::T; ++term) {
+      uint32_t code[kPer / 2];
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) {
+        code[e] = e4m3x2(x[2 * e], x[2 * e + 1]);
+        const float2 back = e4m3x2_to_float2(code[e]);
+        x[2 * e] -= back.x;
+        x[2 * e + 1] -= back.y;
+      }
+      uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
+      if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
+      else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
+    }
+    if (lane == 0) {
+      info.row_pos[r] = row_pos[k];
+      info.row_mul[r] = t * a.scale_log2;
+      info.row_at[r] = row_at[k];
+    }
   }
 }
 
@@ -568,12 +592,12 @@ __device__ __forceinline__ void describe_item(const AttendArgs& a, ItemInfo<C::R
 // The query warp: every item of the CTA's walk but the first (which the
 // warpgroups prepare themselves), one ahead of its use.
 template <class C>
-__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, int64_t at, int64_t total,
-                               int grid) {
+__device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t* q_smem, const Start& start,
+                               int64_t at, int64_t total, int grid) {
   const int lane = threadIdx.x % 32;
   bool ok = true;
-  Walk w = s.start.walk;
-  Entry en = s.start.entry;
+  Walk w = start.walk;
+  Entry en = start.entry;
   int en_of = w.e;
   for (uint32_t it = 0;; ++it) {
     const int buf = it & 1;
@@ -594,8 +618,8 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
     if (it > 0) {
-#pragma unroll 4
-      for (int r = 0; r < C::RT; ++r) query_row<C>(a, info, q_smem + buf * C::kQBytes, en, w.h, r);
+#pragma unroll 1
+      for (int r = 0; r < C::RT; r += 4) query_rows<C, 4>(a, info, q_smem + buf * C::kQBytes, en, w.h, r, 1);
       if (lane == 0) describe_item<C>(a, info, en, w, part, at, total, grid);
       fence_proxy_async_smem();
       __syncwarp();
@@ -633,19 +657,6 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
-// One finished row: thread t < D has dimension t.
-__device__ __forceinline__ void write_row(const AttendArgs& a, int64_t at, bool seen, float v, float mx, float sum,
-                                          int t, int D) {
-  if (at < 0) return;
-  const bool none = !seen || sum == 0.0f;
-  if (t < D) {
-    v = none ? 0.0f : __fdividef(v, sum);
-    if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
-  }
-  if (a.lse && t == 0) a.lse[at] = none ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
-}
-
 // The columns of RT rows at `taddr`, their T terms added, a few rows at a time
 // (the terms of all would not fit in registers beside the softmax state).
 template <class C>
@@ -675,7 +686,7 @@ constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
-                               uint8_t* p_smem, int64_t at0, int64_t total, int grid) {
+                               uint8_t* p_smem, const Start& start, int64_t at0, int64_t total, int grid) {
   constexpr int RT = C::RT, N = C::N, W = C::W, D = C::D;
   constexpr int kAll = W * 128;
   const int wg = uniform(static_cast<int>(threadIdx.x / 128)), warp = uniform(static_cast<int>(threadIdx.x / 32 % 4));
@@ -684,7 +695,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const uint32_t tm_s = uniform(s.tmem) + wg * 2 * N, tm_o = tm_s + N;
   uint8_t* const p_buf = p_smem + wg * C::kPBytes;
   const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem), p_addr = smem_u32(p_buf);
-  const int my_slot = t / a.c.block, my_off = t % a.c.block;
+  const int my_slot = t / a.c.block, my_off = t - my_slot * a.c.block;
   uint32_t g0 = 0;      // tiles of the CTA before this item
   uint32_t phase = 0;   // of this warpgroup's two product barriers
   bool bad = false;     // a wait ran out: what follows is not used
@@ -704,9 +715,10 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   };
 
   {
-    const Walk walk = s.start.walk;
-    const Entry en = s.start.entry;
-    for (int r = threadIdx.x / 32; r < RT; r += W * 4) query_row<C>(a, s.item[0], q_smem, en, walk.h, r);
+    const Walk& walk = start.walk;
+    const Entry& en = start.entry;
+    if (wg * 4 + warp < RT)
+      query_rows<C, (RT + W * 4 - 1) / (W * 4)>(a, s.item[0], q_smem, en, walk.h, wg * 4 + warp, W * 4);
     if (threadIdx.x == W * 128 - 1)
       describe_item<C>(a, s.item[0], en, walk,
                        static_cast<int>(min(static_cast<int64_t>(en.tiles - walk.t), walk.left)), at0, total, grid);
@@ -822,7 +834,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       issued = false;
       if (warp == 3 && i + W < tiles) {
         const uint32_t g2 = g + W, st2 = g2 % C::kStages;
-        issued = __all_sync(0xFFFFFFFFu, mbar_try_wait(&s.full[st2], (g2 / C::kStages) & 1));
+        issued = __all_sync(0xFFFFFFFFu, mbar_test(&s.full[st2], (g2 / C::kStages) & 1));
         if (issued) issue_scores(st2, buf);
       }
       uint32_t codes[N / 4];
@@ -917,6 +929,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         }
         s.mx[t] = mx;
         s.sum[t] = sum;
+        s.inv[t] = __fdividef(1.0f, sum);
       }
     }
     bar_sync(1 + wg, 128);
@@ -931,9 +944,10 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r];
       }
       bar_sync(8, kAll);
-#pragma unroll 1
-      for (int r = r0 + wg; r < min(r0 + C::kJoinRows, rows); r += W) {
-        const float sum = s.sum[r], mx = s.mx[r];
+#pragma unroll
+      for (int k = 0; k < (C::kJoinRows + W - 1) / W; ++k) {
+        const int r = r0 + wg + k * W;
+        if (r >= r0 + C::kJoinRows || r >= rows) break;
         const int row_pos = info.row_pos[r];
         float v = 0.0f;
         if (t < D) {
@@ -941,16 +955,25 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           for (int w = 0; w < W; ++w) v += join[(w * C::kJoinRows + r - r0) * D + t];
           if (row_pos >= first_poison) v = __int_as_float(0x7FC00000);
         }
+        const float sum = s.sum[r];
         if (part >= 0) {
           float* const to = part_row(a, part, rows, r);
           if (t < D) to[t] = v;
           if (t == 0) {
-            to[D] = row_pos < 0 ? kUnset : mx;
+            to[D] = row_pos < 0 ? kUnset : s.mx[r];
             to[D + 1] = row_pos < 0 ? 0.0f : sum;
           }
-        } else {
-          write_row(a, info.row_at[r], row_pos >= 0, v, mx, sum, t, D);
+          continue;
         }
+        const int64_t at = info.row_at[r];
+        if (at < 0) continue;
+        const bool none = row_pos < 0 || sum == 0.0f;
+        if (t < D) {
+          v = none ? 0.0f : v * s.inv[r];
+          if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
+          else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
+        }
+        if (a.lse && t == 0) a.lse[at] = none ? kNegInf : s.mx[r] * 0.6931471805599453f + logf(sum);
       }
     }
     bar_sync(8, kAll);
@@ -995,73 +1018,109 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tmem_relinquish();
   }
 
-  // This CTA's share of all tiles: [total c / grid, total (c + 1) / grid).
-  const int entries = a.c.B * a.n_qt;
-  const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
-  const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
-  uint64_t sum = 0;
-  Entry mine{};
+  // This CTA's share of all tiles, [total c / grid, total (c + 1) / grid), and
+  // the item that its first tile belongs to. Every item of a list has the same
+  // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
+  // to the CTA's threads.
+  const int entries = a.c.B * a.n_qt, heads = a.c.Hkv;
+  Start start{};
+  int64_t total, lo, hi;
+  int grid;
+  auto share = [&](int64_t tiles) {
+    total = tiles * heads;
+    grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int cta = blockIdx.x;
+    lo = hi = 0;
+    if (cta < grid) {
+      lo = divide(total * cta, grid);
+      hi = divide(total * (cta + 1), grid);
+    }
+    start.walk.left = hi - lo;
+  };
+  // The walk starts in the item of entry e, whose tiles begin at `at`.
+  auto begin = [&](int e, const Entry& en, int64_t at) {
+    const int64_t h = divide(lo - at, en.tiles);
+    start.walk.e = e;
+    start.walk.h = static_cast<int32_t>(h);
+    start.walk.t = static_cast<int32_t>(lo - at - h * en.tiles);
+    start.entry = en;
+  };
   if (a.fixed > 0) {
-    sum = static_cast<uint64_t>(e1 - e0) * a.fixed;
+    const int64_t each = static_cast<int64_t>(a.fixed) * heads;
+    share(static_cast<int64_t>(entries) * a.fixed);
+    const int64_t e = divide(lo, each);
+    begin(static_cast<int>(e), entry_of(a, static_cast<int>(e)), e * each);
+  } else if (entries <= 32) {
+    Entry mine{};
+    if (lane < entries) mine = entry_of(a, lane);
+    int64_t before = mine.tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += v;
+    }
+    share(__shfl_sync(0xFFFFFFFFu, before, 31));
+    before = (before - mine.tiles) * heads;
+    const int e = __popc(__ballot_sync(0xFFFFFFFFu, lane < entries && before <= lo)) - 1;
+    Entry en;
+    en.b = __shfl_sync(0xFFFFFFFFu, mine.b, e);
+    en.j0 = __shfl_sync(0xFFFFFFFFu, mine.j0, e);
+    en.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, e);
+    en.first_pos = __shfl_sync(0xFFFFFFFFu, mine.first_pos, e);
+    en.last_pos = __shfl_sync(0xFFFFFFFFu, mine.last_pos, e);
+    en.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, e);
+    begin(e, en, __shfl_sync(0xFFFFFFFFu, before, e));
   } else {
+    const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
+    const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
+    int64_t sum = 0;
+    Entry mine{};
     for (int64_t e = e0; e < e1; ++e) {
       mine = entry_of(a, static_cast<int>(e));
       sum += mine.tiles;
     }
-  }
-  uint64_t before = sum;
+    int64_t before = sum;
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
-    if (lane >= d) before += v;
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += v;
+    }
+    if (lane == 31) s.scan[warp] = before;
+    __syncthreads();
+    int64_t all = 0;
+    before -= sum;
+#pragma unroll 1
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) before += s.scan[w];
+      all += s.scan[w];
+    }
+    share(all);
+    int64_t at = before * heads;
+    if (at <= lo && lo < at + sum * heads) {
+      int64_t e = e0;
+      if (per > 1)
+        for (;; ++e) {
+          mine = entry_of(a, static_cast<int>(e));
+          if (lo < at + static_cast<int64_t>(mine.tiles) * heads) break;
+          at += static_cast<int64_t>(mine.tiles) * heads;
+        }
+      begin(static_cast<int>(e), mine, at);
+      s.start = start;
+    }
+    __syncthreads();
+    start = s.start;
+    start.walk.left = hi - lo;
   }
-  if (lane == 31) s.scan[warp] = before;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  uint64_t all = 0;
-  before -= sum;
-#pragma unroll 1
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) before += s.scan[w];
-    all += s.scan[w];
-  }
-  const int64_t total = static_cast<int64_t>(all) * a.c.Hkv;
-  const int grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  const int cta = blockIdx.x;
-  const int64_t lo = cta < grid ? divide(total * cta, grid) : 0, hi = cta < grid ? divide(total * (cta + 1), grid) : 0;
   if (hi > lo) {
-    int64_t at = static_cast<int64_t>(before) * a.c.Hkv;
-    if (at <= lo && lo < at + static_cast<int64_t>(sum) * a.c.Hkv) {
-      // This thread's entries hold the CTA's first tile.
-      int64_t e = e0;
-      if (a.fixed > 0) {
-        const int64_t each = static_cast<int64_t>(a.fixed) * a.c.Hkv, skip = divide(lo - at, each);
-        e += skip;
-        at += skip * each;
-        mine = entry_of(a, static_cast<int>(e));
-      } else if (per > 1) {
-        for (;; ++e) {
-          mine = entry_of(a, static_cast<int>(e));
-          if (lo < at + static_cast<int64_t>(mine.tiles) * a.c.Hkv) break;
-          at += static_cast<int64_t>(mine.tiles) * a.c.Hkv;
-        }
-      }
-      const int64_t off = lo - at;
-      const int h = static_cast<int>(divide(off, mine.tiles));
-      s.start.walk.e = static_cast<int32_t>(e);
-      s.start.walk.h = h;
-      s.start.walk.t = static_cast<int32_t>(off - static_cast<int64_t>(h) * mine.tiles);
-      s.start.walk.left = hi - lo;
-      s.start.entry = mine;
-    }
-    __syncthreads();
     if (warp < C::W * 4) {
-      attend_consume<C>(a, s, ring, q_smem, p_smem, lo - s.start.walk.t, total, grid);
+      attend_consume<C>(a, s, ring, q_smem, p_smem, start, lo - start.walk.t, total, grid);
     } else if (warp < C::W * 5) {
-      attend_produce<C>(a, &tm_k, &tm_v, s, ring, warp - C::W * 4);
+      attend_produce<C>(a, &tm_k, &tm_v, s, ring, start, warp - C::W * 4);
     } else {
-      attend_queries<C>(a, s, q_smem, lo - s.start.walk.t, total, grid);
+      attend_queries<C>(a, s, q_smem, start, lo - start.walk.t, total, grid);
     }
   }
   tc_fence_before_sync();
