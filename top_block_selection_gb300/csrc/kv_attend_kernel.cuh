@@ -371,7 +371,7 @@ struct AttendShared {
   int32_t poison[128];           // first position whose value code is NaN, per dimension
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_bar[C::W], o_bar[C::W];
+  uint64_t s_bar[C::W];
   int64_t scan[C::kThreads / 32];
   Start start;
   uint32_t tmem;
@@ -697,7 +697,9 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem), p_addr = smem_u32(p_buf);
   const int my_slot = t / a.c.block, my_off = t - my_slot * a.c.block;
   uint32_t g0 = 0;      // tiles of the CTA before this item
-  uint32_t phase = 0;   // of this warpgroup's two product barriers
+  uint32_t phase = 0;   // of this warpgroup's score barrier
+  uint32_t last_st = 0, last_turn = 0;  // stage of the last tile, and its phase
+  const bool leader = elect_one();
   bool bad = false;     // a wait ran out: what follows is not used
   const float kNegInf = -INFINITY;
 
@@ -706,7 +708,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     tc_fence_after_sync();
     const uint64_t ka = smem_desc_rows<D>(ring_addr + st * C::kStageBytes);
     const uint64_t qa = smem_desc_rows<D>(q_addr + buf * C::kQBytes);
-    if (elect_one()) {
+    if (leader) {
 #pragma unroll
       for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(tm_s, ka + ks * 2, qa + ks * 2, idesc_f8(N, false), ks > 0);
       mma_commit(&s.s_bar[wg]);
@@ -746,13 +748,13 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     bool pending = false;                // a product runs that was not waited for
     bool held = false;                   // TMEM holds output not yet in o[]
     bool issued = false;                 // this tile's scores are under way
-    // Waits for the product in flight (the phase of its tile's barriers) and
-    // moves what TMEM holds to o[].
-    auto flush = [&](uint32_t its_phase) {
-      if (pending) {
-        if (!wait_or_stop(&s.o_bar[wg], its_phase, &s.stop, a.status)) bad = true;
-        pending = false;
-      }
+    // Waits for the last tile's output: its stage is given back then.
+    auto settle = [&]() {
+      if (pending && !wait_or_stop(&s.empty[last_st], last_turn, &s.stop, a.status)) bad = true;
+      pending = false;
+    };
+    // Moves what TMEM holds to o[].
+    auto flush = [&]() {
       if (!held) return;
       held = false;
       __syncwarp();
@@ -767,16 +769,22 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     for (int i = (W - g0 % W + wg) % W; i < tiles; i += W) {
       const uint32_t g = g0 + i;
       const uint32_t st = g % C::kStages;
-      if (!wait_or_stop(&s.full[st], (g / C::kStages) & 1, &s.stop, a.status)) bad = true;
-      __syncwarp();
-      if (!issued && warp == 3) issue_scores(st, buf);
+      const uint32_t turn = (g / C::kStages) & 1;
+      if (!issued && warp == 3) {
+        if (!wait_or_stop(&s.full[st], turn, &s.stop, a.status)) bad = true;
+        __syncwarp();
+        issue_scores(st, buf);
+      }
+      // The load (for its description) and the scores, asked for together.
+      const bool there = mbar_test(&s.full[st], turn), scored = mbar_test(&s.s_bar[wg], phase);
+      if (!there && !wait_or_stop(&s.full[st], turn, &s.stop, a.status)) bad = true;
       const StageMeta& meta = s.meta[st];
       const int pos = meta.base[my_slot] + my_off;
       const float k_mul = meta.ks[my_slot], v_scale = meta.vs[my_slot];
       const bool masks = pos > lo_pos;
       if (masks)
         clean_value_row<D>(ring + st * C::kStageBytes + kKvTile * D, t, pos, pos > hi_pos, s.poison);
-      if (!wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
+      if (!scored && !wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
       phase ^= 1;
       __syncwarp();
       tc_fence_after_sync();
@@ -811,7 +819,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           if (lane == r) top = v;
         }
         if (lane < RT) s.red[wg][lane][warp] = top;
-        flush(phase);  // of the tile before: two flips ago
+        settle();
+        flush();
         tc_fence_before_sync();
         bar_sync(1 + wg, 128);
 #pragma unroll
@@ -837,6 +846,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         issued = __all_sync(0xFFFFFFFFu, mbar_test(&s.full[st2], (g2 / C::kStages) & 1));
         if (issued) issue_scores(st2, buf);
       }
+      if (pending && mbar_test(&s.empty[last_st], last_turn)) pending = false;  // asked early: by now it is done
       uint32_t codes[N / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
@@ -860,7 +870,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         }
       }
       // The product before this one has to be done with the probabilities' buffer.
-      if (pending && !wait_or_stop(&s.o_bar[wg], phase, &s.stop, a.status)) bad = true;
+      settle();
 #pragma unroll
       for (int c = 0; c < C::T * RT; c += 16) {
         uint8_t* const to = p_buf + c * kKvTile + t * 16;
@@ -877,18 +887,20 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         const uint64_t va = smem_desc_rows<D>(ring_addr + st * C::kStageBytes + kKvTile * D);
         const uint64_t pa = smem_desc_tokens(p_addr);
         const uint32_t add = uniform(static_cast<uint32_t>(held));
-        if (elect_one()) {
+        if (leader) {
 #pragma unroll
           for (int ks = 0; ks < kKvTile / 32; ++ks)
             mma_f8_ss(tm_o, va + ks * (32 * D / 16), pa + ks * (512 / 16), idesc_f8(N, true), ks > 0 ? 1u : add);
-          mma_commit(&s.o_bar[wg]);
           mma_commit(&s.empty[st]);
         }
         __syncwarp();
       }
       pending = held = true;
+      last_st = st;
+      last_turn = turn;
     }
-    flush(phase ^ 1);
+    settle();
+    flush();
     g0 += tiles;
 
     // Join the warpgroups. The sums over the tokens first: in each step half
@@ -1006,7 +1018,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < C::W; ++i) {
       mbar_init(&s.s_bar[i], 1);
-      mbar_init(&s.o_bar[i], 1);
     }
     s.stop = 0;
     fence_mbarrier_init();
