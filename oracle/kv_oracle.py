@@ -129,8 +129,8 @@ def attend_row(cache, q, b, j, n, h, scale, ids=None, terms=3):
 
     `bound` is the first-order error of the GPU path before the rounding of
     its result, from its number formats: a probability in e4m3 terms is off by
-    at most 2^-12 (three terms) or 2^-9 (two) of itself, or 2^-16 of the largest
-    value scale among the tokens over the row's maximum; a score (fp32 sums of
+    at most 2^-12 (three terms) or 2^-9 (two) of itself, or 2^-17 or 2^-14 of the
+    largest value scale among the tokens over the row's maximum; a score (fp32 sums of
     exact products, a query's terms exact above 2^-18 of the row's largest)
     by (D + 8) 2^-23 sum|q k| + 2^-18 max|q| sum|k|; exp2 and the scaling of
     its argument by 2^-21 (1 + |x|)."""
@@ -153,7 +153,7 @@ def attend_row(cache, q, b, j, n, h, scale, ids=None, terms=3):
                        + 2.0 ** -18 * np.abs(q).max() * np.abs(kk).sum(1)) + 2.0 ** -21 * (1 + np.abs(x - m) + np.abs(x))
     rel = (2.0 ** -12 if terms == 3 else 2.0 ** -9) + 2 * dx
     bound = ((p * rel)[:, None] * np.abs(vv)).sum(0) / total + (p * 2 * dx).sum() / total * np.abs(out) \
-        + 2.0 ** -16 * vs.max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
+        + (2.0 ** -17 if terms == 3 else 2.0 ** -14) * vs.max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
     return out, m + np.log(total), bound
 
 

@@ -17,16 +17,19 @@
 //                  fp16 (T = 3) or bf16 (T = 2) element above 2^-18 of its
 //                  row's largest, the rest to 2^-19 of that;
 //   probabilities  T = 3: cut, cut and rounded, to 2^-12 of each; T = 2:
-//                  rounded twice, to 2^-9. Both are a fraction of the
-//                  rounding of the result (2^-11 and 2^-8 at most), and what
-//                  lies below e4m3's range is off by 2^-16 of the row's
-//                  largest at most.
+//                  rounded twice, to 2^-9: a fraction of the rounding of the
+//                  result (2^-11 and 2^-8 at most). With T = 3 the second and
+//                  third term are scaled by 8 and 128 so that a small
+//                  probability does not end in e4m3's subnormals: it is off
+//                  by 2^-17 of the row's largest at most (T = 2: 2^-14). A sum
+//                  over 131,073 tokens of like weight is then as exact as one
+//                  over 1,000 (unscaled: 2.5 times the error of rounding alone).
 // The terms are groups of columns of one product, added in fp32 after it.
 // With few rows a tile's product is bound by reading the M operand from
 // shared memory, so the extra columns cost little.
 //
 // The softmax reference m_r is not each tile's maximum but one that lags: it
-// is set to twice (one in log2) the largest score, and a tile keeps it as long
+// is set above the largest score (by two in log2), and a tile keeps it as long
 // as its codes still fit below 448. Most tiles thus need one vote of the
 // warpgroup instead of a maximum over its tokens for each row, and the output
 // stays in TMEM, accumulated by the product itself, until a reference moves
@@ -657,9 +660,10 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
-// The columns of RT rows at `taddr`, their T terms added, a few rows at a time
-// (the terms of all would not fit in registers beside the softmax state).
-template <class C>
+// The columns of RT rows at `taddr`, their T terms added (kScaled: the later
+// two of three by 1/8 and 1/128), a few rows at a time (the terms of all would
+// not fit in registers beside the softmax state).
+template <class C, bool kScaled>
 __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
   constexpr int kPart = C::RT <= 8 ? C::RT : C::RT / 2;
 #pragma unroll
@@ -672,15 +676,20 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
 #pragma unroll
     for (int r = 0; r < kPart; r += 2) {
       F2 sum = f2(t1[r], t1[r + 1]);
-      if (C::T == 3) sum = sum + f2(t2[r], t2[r + 1]);
-      sum = sum + f2(t0[r], t0[r + 1]);
+      if (kScaled && C::T == 3) {
+        sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
+        sum = fma2(sum, f2(0.125f, 0.125f), f2(t0[r], t0[r + 1]));
+      } else {
+        if (C::T == 3) sum = sum + f2(t2[r], t2[r + 1]);
+        sum = sum + f2(t0[r], t0[r + 1]);
+      }
       f2_get(sum, x[r0 + r], x[r0 + r + 1]);
     }
   }
 }
 
 constexpr float kUnset = -3e38f;     // a reference that no score has set yet
-constexpr float kMargin = 1.0f;      // a reference is set so far (log2) above the largest score
+constexpr float kMargin = 2.0f;      // a reference is set so far (log2) above the largest score
 constexpr float kProbScale = 128.0f; // code of a probability 1 at the largest value scale
 constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 
@@ -760,7 +769,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       __syncwarp();
       tc_fence_after_sync();
       float x[RT];
-      tmem_rows<C>(tm_o + lane_addr, x);
+      tmem_rows<C, true>(tm_o + lane_addr, x);
       const float f = vref * (1.0f / kProbScale);
 #pragma unroll
       for (int r = 0; r < RT; ++r) o[r] += x[r] * f;
@@ -791,7 +800,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       float e[RT];
       // e = x - m, or x itself.
       auto scores = [&](bool relative) {
-        tmem_rows<C>(tm_s + lane_addr, e);
+        tmem_rows<C, false>(tm_s + lane_addr, e);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
           const F2 f = f2(info.row_mul[r], info.row_mul[r + 1]) * f2(k_mul, k_mul);
@@ -861,7 +870,21 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           if (term < C::T - 1) {  // 4 significant bits: cut (T = 3) or rounded half up (T = 2)
             b0 = (b0 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
             b1 = (b1 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
-            y = fma2(f2(__uint_as_float(b0), __uint_as_float(b1)), f2(-1.0f, -1.0f), y);
+            F2 cut = f2(__uint_as_float(b0), __uint_as_float(b1));
+            if (C::T == 3) {
+              // The first term to e4m3's smallest step too (24576 has steps of
+              // 2^-9), so that what it leaves is all that it leaves.
+              if (term == 0) {
+                cut = cut + f2(24576.0f, 24576.0f) + f2(-24576.0f, -24576.0f);
+                f2_get(cut, p0, p1);
+                b0 = __float_as_uint(p0);
+                b1 = __float_as_uint(p1);
+              }
+              const float up = term == 0 ? 8.0f : 16.0f;
+              y = fma2(cut, f2(-up, -up), y * f2(up, up));
+            } else {
+              y = fma2(cut, f2(-1.0f, -1.0f), y);
+            }
           }
           const uint32_t pair = e4m3x2(__uint_as_float(b0), __uint_as_float(b1));
           const int col = term * RT + r;
