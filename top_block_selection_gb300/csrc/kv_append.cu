@@ -28,8 +28,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHeadsPerThread = 4;  // query heads that share one load of the angles
+constexpr int kHeadsPerThread = 2;  // query heads of a thread (4: 3% to 18% slower, 8: 30%)
 
 struct AppendArgs {
   KvCacheArgs c;
@@ -43,9 +42,12 @@ struct AppendArgs {
   int32_t n, Hq, rot, max_pos, blocks_per_seq;
 };
 
+__device__ __forceinline__ uint4 load8(const void* base, int64_t off) {
+  return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+}
+
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, int64_t off, float (&x)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+__device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -101,40 +103,34 @@ __device__ __forceinline__ Lane lane_of(int sub, int rot, bool interleaved) {
   return l;
 }
 
-struct Angles {
-  float c[8], s[8];
-};
-
-template <bool PAIRS>
-__device__ __forceinline__ void load_angles(const float* cos, const float* sin, int64_t row, const Lane& l,
-                                            Angles& a) {
-  const int o[2] = {l.ang0, PAIRS ? l.ang1 : l.ang0 + 4};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cos + row + o[i]));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(sin + row + o[i]));
-    a.c[4 * i] = c.x, a.c[4 * i + 1] = c.y, a.c[4 * i + 2] = c.z, a.c[4 * i + 3] = c.w;
-    a.s[4 * i] = s.x, a.s[4 * i + 1] = s.y, a.s[4 * i + 2] = s.z, a.s[4 * i + 3] = s.w;
-  }
-}
-
 __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
   const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
   y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
   x = u;
 }
 
+// Rotates a thread's two runs by the angles of row `row` of the tables, four
+// pairs at a time.
 template <bool PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const Angles& a) {
-  if (PAIRS) {
+__device__ __forceinline__ void rotate(const float* cos, const float* sin, int64_t row, const Lane& l, float (&x)[8],
+                                       float (&y)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      turn(x[2 * i], x[2 * i + 1], a.c[i], a.s[i]);
-      turn(y[2 * i], y[2 * i + 1], a.c[4 + i], a.s[4 + i]);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t at = row + (i == 0 ? l.ang0 : (PAIRS ? l.ang1 : l.ang0 + 4));
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cos + at));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(sin + at));
+    if (PAIRS) {
+      float(&z)[8] = i == 0 ? x : y;
+      turn(z[0], z[1], c.x, s.x);
+      turn(z[2], z[3], c.y, s.y);
+      turn(z[4], z[5], c.z, s.z);
+      turn(z[6], z[7], c.w, s.w);
+    } else {
+      turn(x[4 * i], y[4 * i], c.x, s.x);
+      turn(x[4 * i + 1], y[4 * i + 1], c.y, s.y);
+      turn(x[4 * i + 2], y[4 * i + 2], c.z, s.z);
+      turn(x[4 * i + 3], y[4 * i + 3], c.w, s.w);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(x[i], y[i], a.c[i], a.s[i]);
   }
 }
 
@@ -159,123 +155,118 @@ __device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
 }
 
 // Rotates the queries: TPT threads a row, each for kHeadsPerThread heads.
-template <int TPT, bool BF16, bool PAIRS>
-__device__ void rotate_queries(const AppendArgs& a) {
+template <int TPT, int THREADS, bool BF16, bool PAIRS>
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
   const int sub = threadIdx.x % TPT;
   const int chunks = (a.Hq + kHeadsPerThread - 1) / kHeadsPerThread;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) - a.units) * (kThreads / TPT) + threadIdx.x / TPT;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) - a.units) * (THREADS / TPT) + threadIdx.x / TPT;
   if (row >= static_cast<int64_t>(a.c.B) * a.n * chunks) return;
-  const int h0 = static_cast<int>(row % chunks) * kHeadsPerThread;
   const int64_t token = row / chunks;
-  const int b = static_cast<int>(token / a.n), j = static_cast<int>(token % a.n);
+  const int h0 = static_cast<int>(row - token * chunks) * kHeadsPerThread;
+  const int b = static_cast<int>(token / a.n), j = static_cast<int>(token - static_cast<int64_t>(b) * a.n);
+  const Lane l = lane_of<TPT>(sub, a.rot, PAIRS);
+  const int64_t in = b * a.q.sb + j * a.q.sn;
   const Span sp = span_of(a.c, b, a.n);
+  uint4 u[kHeadsPerThread][2];
+#pragma unroll
+  for (int i = 0; i < kHeadsPerThread; ++i)
+    if (h0 + i < a.Hq) {
+      u[i][0] = load8(a.q.data, in + (h0 + i) * a.q.sh + l.off0);
+      u[i][1] = load8(a.q.data, in + (h0 + i) * a.q.sh + l.off1);
+    }
   const int64_t pos = static_cast<int64_t>(sp.first) + j;
   bool there = j < sp.n_new && pos >= 0;
-  const Lane l = lane_of<TPT>(sub, a.rot, PAIRS);
   if (there && a.rot > 0 && pos >= a.max_pos) {
     if (sub == 0) atomicOr(a.status, kErrCacheIndex);
     there = false;
   }
-  Angles g;
-  if (there && l.turns) load_angles<PAIRS>(a.cos, a.sin, pos * (a.rot / 2), l, g);
-  const int D = TPT * 16;
-  float x[kHeadsPerThread][8], y[kHeadsPerThread][8];
-  const int64_t in = b * a.q.sb + j * a.q.sn;
-#pragma unroll
-  for (int i = 0; i < kHeadsPerThread; ++i)
-    if (there && h0 + i < a.Hq) {
-      load8<BF16>(a.q.data, in + (h0 + i) * a.q.sh + l.off0, x[i]);
-      load8<BF16>(a.q.data, in + (h0 + i) * a.q.sh + l.off1, y[i]);
-    }
 #pragma unroll
   for (int i = 0; i < kHeadsPerThread; ++i) {
     if (h0 + i >= a.Hq) break;
-    const int64_t to = (token * a.Hq + h0 + i) * D;
-    if (!there) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = y[i][e] = 0.0f;
-    } else if (l.turns) {
-      rotate<PAIRS>(x[i], y[i], g);
-    }
-    store8<BF16>(a.q_out, to + l.off0, x[i]);
-    store8<BF16>(a.q_out, to + l.off1, y[i]);
+    const int64_t to = (token * a.Hq + h0 + i) * (TPT * 16);
+    float x[8], y[8];
+    unpack8<BF16>(there ? u[i][0] : make_uint4(0, 0, 0, 0), x);
+    unpack8<BF16>(there ? u[i][1] : make_uint4(0, 0, 0, 0), y);
+    if (there && l.turns) rotate<PAIRS>(a.cos, a.sin, pos * (a.rot / 2), l, x, y);
+    store8<BF16>(a.q_out, to + l.off0, x);
+    store8<BF16>(a.q_out, to + l.off1, y);
   }
 }
 
-// TPT threads a token (D = 16 TPT), PASSES * 256 / TPT >= block tokens.
-template <int TPT, int PASSES, bool BF16, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+// TPT threads a token (D = 16 TPT), THREADS / TPT tokens a pass, the new tokens
+// of a block in at most PASSES passes, held in registers.
+// (1,024 threads an SM: 64 registers and a spill of a few words, against 80 and
+// none at 768, take 22.2 us instead of 23.3 for 4,096 tokens, 32 + 16 heads; a
+// form of four passes would spill its values.)
+template <int TPT, int PASSES, int THREADS, bool BF16, bool PAIRS>
+__global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   if (static_cast<int64_t>(blockIdx.x) >= a.units) {
-    rotate_queries<TPT, BF16, PAIRS>(a);
+    rotate_queries<TPT, THREADS, BF16, PAIRS>(a);
     return;
   }
   constexpr int D = 16 * TPT;
-  constexpr int kTokens = kThreads / TPT;  // tokens of one pass
-  __shared__ uint32_t s_max[kThreads / 32];
-  __shared__ float s_sum[kThreads / 32][D];
+  constexpr int kTokens = THREADS / TPT;  // tokens of one pass
+  __shared__ uint32_t s_max[THREADS / 32];
+  __shared__ float s_sum[THREADS / 32][D];
 
   uint32_t u = blockIdx.x;
   const bool is_v = u & 1;
   u >>= 1;
-  const int h = static_cast<int>(u % a.c.Hkv);
-  u /= a.c.Hkv;
-  const int i = static_cast<int>(u % a.blocks_per_seq), b = static_cast<int>(u / a.blocks_per_seq);
+  const uint32_t bi = u / a.c.Hkv;
+  const int h = static_cast<int>(u - bi * a.c.Hkv);
+  const int b = static_cast<int>(bi / a.blocks_per_seq), i = static_cast<int>(bi - b * a.blocks_per_seq);
 
   const Span sp = span_of(a.c, b, a.n);
   const int p0 = max(sp.first, 0);
   if (sp.len <= p0) return;  // no new token
-  const int64_t blk64 = static_cast<int64_t>(p0) / a.c.block + i;
+  const int64_t blk64 = static_cast<int64_t>(p0 / a.c.block) + i;
   const int64_t start64 = blk64 * a.c.block;
   if (start64 >= sp.len) return;
   const int64_t end64 = min(start64 + a.c.block, static_cast<int64_t>(sp.len));
   int page = -1;
   if (blk64 < a.c.max_blocks) page = __ldg(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
-  if (page < 0 || page >= a.c.n_pages || (a.rot > 0 && end64 > a.max_pos)) {
-    if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
-    return;
-  }
-  const int start = static_cast<int>(start64), end = static_cast<int>(end64);
-  const int n_old = max(p0 - start, 0), held = end - start;
 
-  float* const scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hkv + h;
-  const float s_old = n_old > 0 ? *scale_at : 0.0f;
-  uint8_t* const codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * D;
+  // The new tokens: from `from` on, one to a group of TPT threads.
+  const int start = static_cast<int>(start64), end = static_cast<int>(end64);
+  const int from = max(p0, start), n_old = from - start, held = end - start, fresh = end - from;
   const KvRows& src = is_v ? a.v : a.k;
   const int64_t in = b * src.sb + h * src.sh;
   const int sub = threadIdx.x % TPT, tok = threadIdx.x / TPT;
   const Lane l = lane_of<TPT>(sub, is_v ? 0 : a.rot, PAIRS);
-
-  float x[PASSES][8], y[PASSES][8];
+  uint4 raw[PASSES][2];
 #pragma unroll
-  for (int t = 0; t < PASSES; ++t) {
-    const int slot = t * kTokens + tok;
-    if (slot >= n_old && slot < held) {
-      const int64_t row = in + (static_cast<int64_t>(start) + slot - sp.first) * src.sn;
-      load8<BF16>(src.data, row + l.off0, x[t]);
-      load8<BF16>(src.data, row + l.off1, y[t]);
+  for (int t = 0; t < PASSES; ++t)
+    if (t * kTokens + tok < fresh) {
+      const int64_t row = in + (static_cast<int64_t>(from) + t * kTokens + tok - sp.first) * src.sn;
+      raw[t][0] = load8(src.data, row + l.off0);
+      raw[t][1] = load8(src.data, row + l.off1);
     }
+  if (page < 0 || page >= a.c.n_pages || (a.rot > 0 && end64 > a.max_pos)) {
+    if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
+    return;
   }
-  float m = 0.0f;
+  float* const scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hkv + h;
+  const float s_old = n_old > 0 ? *scale_at : 0.0f;
+  uint8_t* const codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * D;
+
+  float x[PASSES][8], y[PASSES][8], m = 0.0f;
 #pragma unroll
-  for (int t = 0; t < PASSES; ++t) {
-    const int slot = t * kTokens + tok;
-    if (slot >= n_old && slot < held) {
-      if (l.turns) {
-        Angles g;
-        load_angles<PAIRS>(a.cos, a.sin, (static_cast<int64_t>(start) + slot) * (a.rot / 2), l, g);
-        rotate<PAIRS>(x[t], y[t], g);
-      }
+  for (int t = 0; t < PASSES; ++t)
+    if (t * kTokens + tok < fresh) {
+      unpack8<BF16>(raw[t][0], x[t]);
+      unpack8<BF16>(raw[t][1], y[t]);
+      if (l.turns)
+        rotate<PAIRS>(a.cos, a.sin, (static_cast<int64_t>(from) + t * kTokens + tok) * (a.rot / 2), l, x[t], y[t]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[t][e]), fabsf(y[t][e])));
     }
-  }
   // Non-negative floats order as their bits.
   const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
   if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = wm;
   __syncthreads();
   uint32_t bm = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) bm = max(bm, s_max[w]);
+  for (int w = 0; w < THREADS / 32; ++w) bm = max(bm, s_max[w]);
   const float s_new = pow2_scale(__uint_as_float(bm));
   const float s = n_old > 0 ? fmaxf(s_old, s_new) : s_new;
   const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
@@ -287,22 +278,31 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  auto add = [&](uint2 c0, uint2 c1) {
+    float f[8];
+    decode8(c0, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    decode8(c1, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[8 + e] += f[e];
+  };
 #pragma unroll
   for (int t = 0; t < PASSES; ++t) {
-    const int slot = t * kTokens + tok;
+    const int slot = n_old + t * kTokens + tok;
     if (slot >= held) continue;
-    uint2* const at0 = reinterpret_cast<uint2*>(codes + slot * D + l.off0);
-    uint2* const at1 = reinterpret_cast<uint2*>(codes + slot * D + l.off1);
-    uint2 c0, c1;
-    if (slot >= n_old) {
-      c0 = encode8(x[t], s, inv, pow2);
-      c1 = encode8(y[t], s, inv, pow2);
-      *at0 = c0;
-      *at1 = c1;
-    } else {
-      if (ratio == 1.0f && !want_kb) continue;
-      c0 = *at0;
-      c1 = *at1;
+    const uint2 c0 = encode8(x[t], s, inv, pow2), c1 = encode8(y[t], s, inv, pow2);
+    *reinterpret_cast<uint2*>(codes + slot * D + l.off0) = c0;
+    *reinterpret_cast<uint2*>(codes + slot * D + l.off1) = c1;
+    if (want_kb) add(c0, c1);
+  }
+  // The older tokens: rounded again where the scale grew, added to the mean.
+  if (n_old > 0 && (want_kb || ratio != 1.0f)) {
+#pragma unroll 4
+    for (int slot = tok; slot < n_old; slot += kTokens) {
+      uint2* const at0 = reinterpret_cast<uint2*>(codes + slot * D + l.off0);
+      uint2* const at1 = reinterpret_cast<uint2*>(codes + slot * D + l.off1);
+      uint2 c0 = *at0, c1 = *at1;
       if (ratio != 1.0f) {
         float f[8];
         decode8(c0, f);
@@ -316,15 +316,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         *at0 = c0;
         *at1 = c1;
       }
-    }
-    if (want_kb) {
-      float f[8];
-      decode8(c0, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[e];
-      decode8(c1, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[8 + e] += f[e];
+      if (want_kb) add(c0, c1);
     }
   }
   if (!want_kb) return;
@@ -344,25 +336,30 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   if (threadIdx.x < D) {
     float total = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w][threadIdx.x];
+    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w][threadIdx.x];
     const float mean = __fdiv_rn(__fmul_rn(total, s), static_cast<float>(held));
     const int64_t at = ((static_cast<int64_t>(b) * a.c.Hkv + h) * a.c.max_blocks + blk64) * D + threadIdx.x;
     a.kb[at] = __half_as_ushort(__float2half_rn(mean));
   }
 }
 
-template <int TPT, int PASSES>
+template <int TPT, int PASSES, int THREADS>
 cudaError_t launch_form(const AppendArgs& a, bool bf16, bool pairs, unsigned grid, cudaStream_t stream) {
   if (bf16) {
-    if (pairs) kv_append_kernel<TPT, PASSES, true, true><<<grid, kThreads, 0, stream>>>(a);
-    else kv_append_kernel<TPT, PASSES, true, false><<<grid, kThreads, 0, stream>>>(a);
+    if (pairs) kv_append_kernel<TPT, PASSES, THREADS, true, true><<<grid, THREADS, 0, stream>>>(a);
+    else kv_append_kernel<TPT, PASSES, THREADS, true, false><<<grid, THREADS, 0, stream>>>(a);
   } else {
-    if (pairs) kv_append_kernel<TPT, PASSES, false, true><<<grid, kThreads, 0, stream>>>(a);
-    else kv_append_kernel<TPT, PASSES, false, false><<<grid, kThreads, 0, stream>>>(a);
+    if (pairs) kv_append_kernel<TPT, PASSES, THREADS, false, true><<<grid, THREADS, 0, stream>>>(a);
+    else kv_append_kernel<TPT, PASSES, THREADS, false, false><<<grid, THREADS, 0, stream>>>(a);
   }
   plan_add("kv_append_kernel");
   return cudaGetLastError();
 }
+
+// With few new tokens a sequence (a decode step) a CTA's work is a chain of
+// loads, and what counts is that all CTAs run at once: 128 threads. Otherwise
+// 256, for the bytes in flight.
+int append_threads(const KvAppendProblem& p) { return p.n * (p.cache.D / 16) <= 128 ? 128 : 256; }
 
 }  // namespace
 
@@ -374,7 +371,7 @@ int64_t kv_append_grid(const KvAppendProblem& p, int64_t* units, int32_t* blocks
   if (!p.q.data) return *units;
   const int64_t rows =
       static_cast<int64_t>(p.cache.B) * p.n * ((p.Hq + kHeadsPerThread - 1) / kHeadsPerThread);
-  const int per_cta = kThreads / (p.cache.D / 16);
+  const int per_cta = append_threads(p) / (p.cache.D / 16);
   return *units + (rows + per_cta - 1) / per_cta;
 }
 
@@ -394,13 +391,16 @@ cudaError_t launch_kv_append(const KvAppendProblem& p, const DeviceInfo& dev, cu
   a.rot = p.rot;
   a.max_pos = p.max_pos;
   const unsigned grid = static_cast<unsigned>(kv_append_grid(p, &a.units, &a.blocks_per_seq));
+  const bool few = append_threads(p) == 128;
   if (p.cache.D == 128) {
-    if (p.cache.block <= 32) return launch_form<8, 1>(a, p.bf16, p.interleaved, grid, stream);
-    if (p.cache.block <= 64) return launch_form<8, 2>(a, p.bf16, p.interleaved, grid, stream);
-    return launch_form<8, 4>(a, p.bf16, p.interleaved, grid, stream);
+    if (few) return launch_form<8, 1, 128>(a, p.bf16, p.interleaved, grid, stream);
+    if (p.cache.block <= 32) return launch_form<8, 1, 256>(a, p.bf16, p.interleaved, grid, stream);
+    if (p.cache.block <= 64) return launch_form<8, 2, 256>(a, p.bf16, p.interleaved, grid, stream);
+    return launch_form<8, 4, 256>(a, p.bf16, p.interleaved, grid, stream);
   }
-  if (p.cache.block <= 64) return launch_form<4, 1>(a, p.bf16, p.interleaved, grid, stream);
-  return launch_form<4, 2>(a, p.bf16, p.interleaved, grid, stream);
+  if (few) return launch_form<4, 1, 128>(a, p.bf16, p.interleaved, grid, stream);
+  if (p.cache.block <= 64) return launch_form<4, 1, 256>(a, p.bf16, p.interleaved, grid, stream);
+  return launch_form<4, 2, 256>(a, p.bf16, p.interleaved, grid, stream);
 }
 
 }  // namespace qsa

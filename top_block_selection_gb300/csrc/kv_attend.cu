@@ -78,17 +78,6 @@ size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, 
   return sizeof(float) * 2 * kKvMaxCtas * kKvMaxGroup * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
 }
 
-cudaError_t init_kv_attend_kernels(const DeviceInfo&) {
-  const CUtensorMap none{};
-  const AttendArgs a{};
-  for (const AttendLaunch form : {attend_d64_t2, attend_d64_t3, attend_d128_t2, attend_d128_t3})
-    for (int rt = 4; rt <= 32; rt *= 2) {
-      const cudaError_t e = form(rt, none, none, a, 0, true, nullptr);
-      if (e != cudaSuccess) return e;
-    }
-  return cudaSuccess;
-}
-
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
   AttendArgs a{};
   a.c = p.cache;
@@ -121,7 +110,7 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
     return cudaErrorInvalidValue;
   const AttendLaunch form = p.cache.D == 64 ? (p.bf16 ? attend_d64_t2 : attend_d64_t3)
                                             : (p.bf16 ? attend_d128_t2 : attend_d128_t3);
-  cudaError_t e = form(rt, tk, tv, a, grid, false, stream);
+  cudaError_t e = form(rt, tk, tv, a, grid, dev.id, stream);
   if (e != cudaSuccess) return e;
   plan_add("kv_attend_kernel");
   // Items of one tile are never split.

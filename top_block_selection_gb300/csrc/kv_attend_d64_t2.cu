@@ -4,7 +4,7 @@
 
 namespace qsa {
 cudaError_t attend_d64_t2(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
-                         bool init, cudaStream_t stream) {
-  return attend_rows<64, 2>(rt, tk, tv, a, grid, init, stream);
+                         int device, cudaStream_t stream) {
+  return attend_rows<64, 2>(rt, tk, tv, a, grid, device, stream);
 }
 }  // namespace qsa

@@ -49,6 +49,8 @@
 // workspace, which kv_combine_kernel joins.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1162,15 +1164,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (warp == 0) tmem_dealloc(s.tmem, C::kTmemCols);
 }
 
-// Launch with the given tensor maps; grid CTAs.
+// Launch with the given tensor maps on the current device; grid CTAs.
 template <int D, int RT, int T>
-cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid, bool init,
+cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid, int device,
                         cudaStream_t stream) {
   using C = AttendCfg<D, RT, T>;
   constexpr int smem = 1024 + C::kStages * C::kStageBytes + 2 * C::kQBytes + C::kPRegion +
                        static_cast<int>(sizeof(AttendShared<C>));
   static_assert(smem <= 227 * 1024, "shared memory");
-  if (init) return cudaFuncSetAttribute(kv_attend_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // Set when a form is first used on a device: loading all of them with the
+  // library would slow down the first call of programs that use none.
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << device;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   kv_attend_kernel<C><<<grid, C::kThreads, smem, stream>>>(tk, tv, a);
   return cudaGetLastError();
 }
@@ -1178,19 +1188,19 @@ cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const Atte
 // All row counts of one head size and term count (kv_attend_d*_t*.cu).
 template <int D, int T>
 cudaError_t attend_rows(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
-                        bool init, cudaStream_t stream) {
+                        int device, cudaStream_t stream) {
   switch (rt) {
-    case 4: return attend_form<D, 4, T>(tk, tv, a, grid, init, stream);
-    case 8: return attend_form<D, 8, T>(tk, tv, a, grid, init, stream);
-    case 16: return attend_form<D, 16, T>(tk, tv, a, grid, init, stream);
-    default: return attend_form<D, 32, T>(tk, tv, a, grid, init, stream);
+    case 4: return attend_form<D, 4, T>(tk, tv, a, grid, device, stream);
+    case 8: return attend_form<D, 8, T>(tk, tv, a, grid, device, stream);
+    case 16: return attend_form<D, 16, T>(tk, tv, a, grid, device, stream);
+    default: return attend_form<D, 32, T>(tk, tv, a, grid, device, stream);
   }
 }
 using AttendLaunch = cudaError_t (*)(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a,
-                                     int grid, bool init, cudaStream_t stream);
-cudaError_t attend_d64_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
-cudaError_t attend_d64_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
-cudaError_t attend_d128_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
-cudaError_t attend_d128_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, bool, cudaStream_t);
+                                     int grid, int device, cudaStream_t stream);
+cudaError_t attend_d64_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend_d64_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend_d128_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend_d128_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
 
 }  // namespace qsa

@@ -56,7 +56,6 @@ struct KvAttendProblem {
 };
 // 0 for sizes the attention does not take.
 size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
-cudaError_t init_kv_attend_kernels(const DeviceInfo& dev);
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream);
 
 constexpr int kKvMaxGroup = 32;             // query heads per KV head

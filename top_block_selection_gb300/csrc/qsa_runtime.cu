@@ -2,7 +2,6 @@
 // attributes, one-time kernel setup, and the driver's tensor-map encoder.
 #include <mutex>
 
-#include "kv_internal.h"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
 
@@ -46,8 +45,7 @@ const DeviceInfo* current_device(cudaError_t* err) {
     }
     d.status_word = static_cast<uint32_t*>(p);
     if ((e = init_score_kernels(d)) != cudaSuccess || (e = init_select_kernels(d)) != cudaSuccess ||
-        (e = init_fused_kernels(d)) != cudaSuccess || (e = init_split_reduce_kernel(d)) != cudaSuccess ||
-        (e = init_kv_attend_kernels(d)) != cudaSuccess) {
+        (e = init_fused_kernels(d)) != cudaSuccess || (e = init_split_reduce_kernel(d)) != cudaSuccess) {
       *err = e;
       return nullptr;
     }
