@@ -246,29 +246,72 @@ def test_attend_ragged_batch(tbs):
     assert (out[3] == 0).all() and (out[2, 1] == 0).all()
 
 
-@pytest.mark.parametrize("lens,Hkv,R,D,block", [([20011, 9000], 8, 4, 64, 64), ([40000], 4, 5, 128, 128),
-                                                ([30001], 8, 16, 64, 32), ([25000, 1, 17001], 4, 32, 64, 64),
-                                                ([200] * 300, 4, 1, 64, 64), ([90, 0, 700] * 40, 8, 8, 128, 16)])
-def test_attend_many_tiles(tbs, lens, Hkv, R, D, block):
+@pytest.mark.parametrize("lens,Hkv,R,D,block,dtype", [
+    ([20011, 9000], 8, 4, 64, 64, "f16"), ([40000], 4, 5, 128, 128, "f16"), ([30001], 8, 16, 64, 32, "f16"),
+    ([25000, 1, 17001], 4, 32, 64, 64, "f16"), ([200] * 300, 4, 1, 64, 64, "f16"),
+    ([90, 0, 700] * 40, 8, 8, 128, 16, "f16"), ([5, 130, 0, 300] * 200, 2, 3, 64, 64, "bf16"),
+    ([21000, 3], 4, 16, 128, 64, "bf16"), ([30000], 3, 32, 128, 64, "bf16"), ([9999, 20000], 8, 8, 128, 32, "bf16")])
+def test_attend_many_tiles(tbs, lens, Hkv, R, D, block, dtype):
     """Several turns of every stage, items that begin, lie and end inside a
     CTA's share, and items that span CTAs. A row of each sequence and head is
     compared with the oracle."""
     c = kc.make_long_cache(lens, Hkv, block, D, seed=R)
-    q = kc.as_f16(np.random.default_rng(R).standard_normal((len(lens), 1, Hkv * R, D)))
+    q = kc.ROUND[dtype](np.random.default_rng(R).standard_normal((len(lens), 1, Hkv * R, D)))
+    args, _ = on_gpu(c)
+    g = dev(q, dtype)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
+    out = tbs.qsa_kv_attend(g, *args, lse=lse)
+    for _ in range(20):
+        assert torch.equal(tbs.qsa_kv_attend(g, *args), out)
+    assert not torch.isnan(out).any()
+    rows = np.random.default_rng(1).permutation([(b, h) for b in range(len(lens)) for h in range(Hkv)])[:40]
+    check_rows(c, q, out, lse, dtype, [(b, 0, h * R + (b + h) % R) for b, h in rows])
+
+
+def check_rows(c, q, out, lse, dtype, rows, ids=None):
+    """These (sequence, row, head) of a result against the oracle."""
+    got, D, n = out.double().cpu().numpy(), q.shape[3], q.shape[1]
+    R = q.shape[2] // c["k"].shape[1]
+    for b, j, hq in rows:
+        h = hq // R
+        listed = None if ids is None else ids[b, h if ids.shape[1] > 1 else 0, j]
+        want, wlse, bound = ko.attend_row(c, q[b, j, hq], b, j, n, h, D ** -0.5, listed, terms=3 if dtype == "f16" else 2)
+        err = np.abs(got[b, j, hq] - want)
+        assert (err <= bound + UNIT[dtype] * (np.abs(want) + bound) + TINY[dtype]).all(), (b, j, hq)
+        assert np.linalg.norm(err) <= 2 * UNIT[dtype] * np.linalg.norm(want)
+        if lse is not None:
+            g = float(lse[b, j, hq])
+            assert wlse == g or abs(wlse - g) <= 1e-4 + 1e-5 * abs(wlse)
+
+
+@pytest.mark.parametrize("n,Hkv,R,block,k,dtype", [(70, 2, 16, 64, 33, "f16"), (300, 1, 8, 32, 12, "bf16"),
+                                                   (33, 4, 4, 128, 9, "f16"), (17, 8, 32, 16, 64, "f16")])
+def test_attend_many_lists(tbs, n, Hkv, R, block, k, dtype):
+    """Many queries with lists of their own, more items than CTAs and fewer."""
+    c = kc.make_long_cache([5003], Hkv, block, 128, seed=n)
+    rng = np.random.default_rng(n)
+    ids = kc.blocks_of(rng, c, n, Hkv, k, block)
+    q = kc.ROUND[dtype](rng.standard_normal((1, n, Hkv * R, 128)))
     args, _ = on_gpu(c)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
-    out = tbs.qsa_kv_attend(dev(q, "f16"), *args, lse=lse)
-    for _ in range(20):
-        assert torch.equal(tbs.qsa_kv_attend(dev(q, "f16"), *args), out)
-    assert not torch.isnan(out).any()
-    got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
-    rows = np.random.default_rng(1).permutation([(b, h) for b in range(len(lens)) for h in range(Hkv)])[:40]
-    for b, h in rows:
-        hq = h * R + (b + h) % R
-        want, wlse, bound = ko.attend_row(c, q[b, 0, hq], b, 0, 1, h, D ** -0.5)
-        assert (np.abs(got[b, 0, hq] - want) <= bound + UNIT["f16"] * (np.abs(want) + bound) + TINY["f16"]).all(), (b, h)
-        assert np.linalg.norm(got[b, 0, hq] - want) <= 2 * UNIT["f16"] * np.linalg.norm(want)
-        assert wlse == glse[b, 0, hq] or abs(wlse - glse[b, 0, hq]) <= 1e-4 + 1e-5 * abs(wlse)
+    out = tbs.qsa_kv_attend(dev(q, dtype), *args, ids=dev(ids), lse=lse)
+    assert torch.equal(tbs.qsa_kv_attend(dev(q, dtype), *args, ids=dev(ids)), out)
+    check_rows(c, q, out, lse, dtype, [(0, int(rng.integers(n)), int(rng.integers(Hkv * R))) for _ in range(40)], ids)
+
+
+def test_attend_strides_and_given_buffers(tbs):
+    """Queries inside a wider projection, with swapped axes, one row for every
+    head; a given output and workspace."""
+    c = kc.make_cache([150, 70], 2, 32, 64, seed=30)
+    args, _ = on_gpu(c)
+    wide = torch.randn((2, 3, 12, 64), dtype=torch.float16, device="cuda")
+    ws = torch.full((tbs.qsa_kv_attend_workspace_bytes(2, 3, 4, 2, 64),), 255, dtype=torch.uint8, device="cuda")
+    for q in (wide[:, :, 5:9], wide.transpose(1, 2)[:, 2:5, :2].transpose(1, 2)[:, :2, :2],
+              wide[:, :, :1].expand(2, 3, 4, 64), wide[:1, :, :4].expand(2, 3, 4, 64)):
+        want = tbs.qsa_kv_attend(q.contiguous(), *args)
+        out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+        assert tbs.qsa_kv_attend(q, *args, out=out, workspace=ws) is out
+        assert torch.equal(out, want)
 
 
 @pytest.mark.parametrize("amp", [0.0, 1e-3, 30.0])

@@ -7,45 +7,48 @@
 namespace qsa {
 namespace {
 
-constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 4;  // rows of a CTA, 128 threads each
 
-// One CTA per (CTA that began a split item, row): the item's parts are that
-// CTA's second slot and the first slots of the CTAs after it, added in order.
-__global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float s_f[kKvMaxCtas];
-  __shared__ float s_red[kCombineThreads / 32], s_sum[kCombineThreads / 32];
+// Joins the parts of the item that CTA blockIdx.x of the attention began and
+// others ended: that CTA's second slot and the first slots of the CTAs after
+// it, added in order. A CTA a row would be up to 4,900 CTAs, nearly all with
+// nothing to do, and their launch longer than the work.
+__global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float s_f[kCombineRows][kKvMaxCtas];
+  __shared__ float s_max[kCombineRows][4], s_sum[kCombineRows][4];
   pdl_wait();
-  const int c0 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, rows = a.qt * a.R, D = a.c.D;
-  const int e = a.jobs[4 * c0];
-  if (e < 0) return;
-  const int h = a.jobs[4 * c0 + 1], parts = a.jobs[4 * c0 + 2] - c0 + 1;
+  const int group = threadIdx.x / 128, tid = threadIdx.x % 128, rows = a.qt * a.R, D = a.c.D;
+  const int c0 = blockIdx.x, r = blockIdx.y * kCombineRows + group;
+  const int4 job = *reinterpret_cast<const int4*>(a.jobs + 4 * c0);
+  if (job.x < 0) return;
+  const int e = job.x, h = job.y, parts = job.z - c0 + 1;
   const int b = e / a.n_qt, j = (e - b * a.n_qt) * a.qt + r / a.R;
-  if (j >= a.n) return;
+  const bool there = r < rows && j < a.n;
+  auto part = [&](int i) { return part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r); };
   float m = -INFINITY, l = 0.0f;
-  for (int i = tid; i < parts; i += kCombineThreads) {
-    const float* const p = part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r);
-    m = fmaxf(m, p[D]);
-  }
+  if (there)
+    for (int i = tid; i < parts; i += 128) m = fmaxf(m, part(i)[D]);
   m = warp_max(m);
-  if (tid % 32 == 0) s_red[tid / 32] = m;
+  if (tid % 32 == 0) s_max[group][tid / 32] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  for (int i = tid; i < parts; i += kCombineThreads) {
-    const float* const p = part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r);
-    const float f = exp2_approx(p[D] - m);
-    s_f[i] = f;
-    l += p[D + 1] * f;
-  }
+  m = fmaxf(fmaxf(s_max[group][0], s_max[group][1]), fmaxf(s_max[group][2], s_max[group][3]));
+  if (there)
+    for (int i = tid; i < parts; i += 128) {
+      const float f = exp2_approx(part(i)[D] - m);
+      s_f[group][i] = f;
+      l += part(i)[D + 1] * f;
+    }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-  if (tid % 32 == 0) s_sum[tid / 32] = l;
+  if (tid % 32 == 0) s_sum[group][tid / 32] = l;
   __syncthreads();
-  l = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  if (!there) return;
+  l = (s_sum[group][0] + s_sum[group][1]) + (s_sum[group][2] + s_sum[group][3]);
   const int64_t at = (static_cast<int64_t>(b) * a.n + j) * a.Hq + h * a.R + r % a.R;
   if (tid < D) {
-    float v = part_row(a, 2 * c0 + 1, rows, r)[tid] * s_f[0];
+    float v = 0.0f;
 #pragma unroll 8
-    for (int i = 1; i < parts; ++i) v += part_row(a, 2 * (c0 + i), rows, r)[tid] * s_f[i];
+    for (int i = 0; i < parts; ++i) v += part(i)[tid] * s_f[group][i];
     v = l == 0.0f ? 0.0f : v / l;
     if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + tid] = __float2bfloat16_rn(v);
     else static_cast<__half*>(a.out)[at * D + tid] = __float2half_rn(v);
@@ -101,7 +104,10 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   a.n_qt = (p.n + a.qt - 1) / a.qt;
   a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
   const int rt = rows_form(a.qt * a.R);
-  const int grid = std::min(dev.sm_count, kKvMaxCtas);
+  // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
+  const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
+  const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * p.cache.Hkv * item_tiles;
+  const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sm_count, kKvMaxCtas), most));
   a.jobs = static_cast<int32_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
 
@@ -114,8 +120,9 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   if (e != cudaSuccess) return e;
   plan_add("kv_attend_kernel");
   // Items of one tile are never split.
-  if (a.fixed == 1 || (a.fixed == 0 && p.cache.max_blocks * p.cache.block <= kKvTile)) return cudaSuccess;
-  e = launch_pdl(kv_combine_kernel, dim3(grid, a.qt * a.R), dim3(kCombineThreads), 0, stream, a);
+  if (item_tiles == 1) return cudaSuccess;
+  e = launch_pdl(kv_combine_kernel, dim3(grid, (a.qt * a.R + kCombineRows - 1) / kCombineRows),
+                 dim3(128 * kCombineRows), 0, stream, a);
   if (e == cudaSuccess) plan_add("kv_combine_kernel");
   return e;
 }
