@@ -353,6 +353,7 @@ struct StageMeta {
   int32_t base[kKvMaxSlots];  // position of the slot's first token, kKvNoToken if none
   float ks[kKvMaxSlots];      // key scale
   float vs[kKvMaxSlots];      // value scale (0: no block)
+  float vmax;                 // the largest of them
 };
 
 template <int RT>
@@ -373,7 +374,7 @@ struct AttendShared {
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
   alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
   float mx[C::RT], sum[C::RT], inv[C::RT];  // joined, 1 / sum
-  int32_t poison[128];           // first position whose value code is NaN, per dimension
+  alignas(16) int32_t poison[128];  // first position whose value code is NaN, per dimension
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_bar[C::W];
@@ -469,7 +470,10 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
           }
           __syncwarp();
         }
+        float vmax = vs;
+        for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
         if (my_k == i) {
+          if (my_slot == 0) s.meta[st].vmax = vmax;
           s.meta[st].base[my_slot] = base;
           s.meta[st].ks[my_slot] = ks;
           s.meta[st].vs[my_slot] = vs;
@@ -844,10 +848,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           o[r] *= alpha;
           e[r] -= mn;
         }
-#pragma unroll
-        for (int k = 0; k < kKvMaxSlots; ++k)
-          if (k < a.spt) vref = fmaxf(vref, meta.vs[k]);
-        inv_vref = vref > 0.0f ? __fdiv_rn(kProbScale, vref) : 0.0f;
+        vref = fmaxf(vref, meta.vmax);
+        inv_vref = vref > 0.0f ? __fdividef(kProbScale, vref) : 0.0f;
         v_mul = v_scale * inv_vref;
       }
       // The scores have been read: the next tile's may overwrite them.
@@ -971,7 +973,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     }
     bar_sync(1 + wg, 128);
     float* const join = reinterpret_cast<float*>(p_smem);
-    const int rows = info.rows, first_poison = t < D ? s.poison[t] : kKvNoToken, part = info.slot;
+    const int rows = info.rows, part = info.slot;
 #pragma unroll
     for (int r0 = 0; r0 < RT; r0 += C::kJoinRows) {
       if (r0 > 0) bar_sync(8, kAll);
@@ -981,36 +983,43 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r];
       }
       bar_sync(8, kAll);
+      // Four dimensions of a row a thread.
+      for (int c = threadIdx.x; c < C::kJoinRows * (D / 4); c += kAll) {
+        const int row = c / (D / 4), r = r0 + row, d = c % (D / 4) * 4;
+        if (r >= rows) break;
+        float4 v = *reinterpret_cast<const float4*>(&join[row * D + d]);
 #pragma unroll
-      for (int k = 0; k < (C::kJoinRows + W - 1) / W; ++k) {
-        const int r = r0 + wg + k * W;
-        if (r >= r0 + C::kJoinRows || r >= rows) break;
-        const int row_pos = info.row_pos[r];
-        float v = 0.0f;
-        if (t < D) {
-#pragma unroll
-          for (int w = 0; w < W; ++w) v += join[(w * C::kJoinRows + r - r0) * D + t];
-          if (row_pos >= first_poison) v = __int_as_float(0x7FC00000);
+        for (int w = 1; w < W; ++w) {
+          const float4 u = *reinterpret_cast<const float4*>(&join[(w * C::kJoinRows + row) * D + d]);
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
         }
-        const float sum = s.sum[r];
+        const int4 bad_from = *reinterpret_cast<const int4*>(&s.poison[d]);
+        const int row_pos = info.row_pos[r];
+        const int64_t at = info.row_at[r];
+        const float sum = s.sum[r], inv = s.inv[r], mx = s.mx[r], nan = __int_as_float(0x7FC00000);
+        if (row_pos >= bad_from.x) v.x = nan;
+        if (row_pos >= bad_from.y) v.y = nan;
+        if (row_pos >= bad_from.z) v.z = nan;
+        if (row_pos >= bad_from.w) v.w = nan;
         if (part >= 0) {
           float* const to = part_row(a, part, rows, r);
-          if (t < D) to[t] = v;
-          if (t == 0) {
-            to[D] = row_pos < 0 ? kUnset : s.mx[r];
-            to[D + 1] = row_pos < 0 ? 0.0f : sum;
+          *reinterpret_cast<float2*>(to + d) = make_float2(v.x, v.y);
+          *reinterpret_cast<float2*>(to + d + 2) = make_float2(v.z, v.w);
+          if (d == 0) *reinterpret_cast<float2*>(to + D) = row_pos < 0 ? make_float2(kUnset, 0.0f) : make_float2(mx, sum);
+        } else if (at >= 0) {
+          const bool none = row_pos < 0 || sum == 0.0f;
+          v = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          uint2 packed;
+          if (a.bf16) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+            packed = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+          } else {
+            const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
+            packed = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
           }
-          continue;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + d) = packed;
+          if (a.lse && d == 0) a.lse[at] = none ? kNegInf : mx * 0.6931471805599453f + logf(sum);
         }
-        const int64_t at = info.row_at[r];
-        if (at < 0) continue;
-        const bool none = row_pos < 0 || sum == 0.0f;
-        if (t < D) {
-          v = none ? 0.0f : v * s.inv[r];
-          if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + t] = __float2bfloat16_rn(v);
-          else static_cast<__half*>(a.out)[at * D + t] = __float2half_rn(v);
-        }
-        if (a.lse && t == 0) a.lse[at] = none ? kNegInf : s.mx[r] * 0.6931471805599453f + logf(sum);
       }
     }
     bar_sync(8, kAll);
