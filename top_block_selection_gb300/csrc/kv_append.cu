@@ -43,7 +43,7 @@ struct AppendArgs {
 };
 
 __device__ __forceinline__ uint4 load8(const void* base, int64_t off) {
-  return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+  return load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
 }
 
 template <bool BF16>
@@ -117,8 +117,8 @@ __device__ __forceinline__ void rotate(const float* cos, const float* sin, int64
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t at = row + (i == 0 ? l.ang0 : (PAIRS ? l.ang1 : l.ang0 + 4));
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cos + at));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(sin + at));
+    const float4 c = load_global(reinterpret_cast<const float4*>(cos + at));
+    const float4 s = load_global(reinterpret_cast<const float4*>(sin + at));
     if (PAIRS) {
       float(&z)[8] = i == 0 ? x : y;
       turn(z[0], z[1], c.x, s.x);
@@ -200,6 +200,8 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
 // form of four passes would spill its values.)
 template <int TPT, int PASSES, int THREADS, bool BF16, bool PAIRS>
 __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();  // after the wait: at most one kernel ahead of the one that runs
   if (static_cast<int64_t>(blockIdx.x) >= a.units) {
     rotate_queries<TPT, THREADS, BF16, PAIRS>(a);
     return;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
   if (start64 >= sp.len) return;
   const int64_t end64 = min(start64 + a.c.block, static_cast<int64_t>(sp.len));
   int page = -1;
-  if (blk64 < a.c.max_blocks) page = __ldg(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
+  if (blk64 < a.c.max_blocks) page = load_global(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
 
   // The new tokens: from `from` on, one to a group of TPT threads.
   const int start = static_cast<int>(start64), end = static_cast<int>(end64);
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
     return;
   }
   float* const scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hkv + h;
-  const float s_old = n_old > 0 ? *scale_at : 0.0f;
+  const float s_old = n_old > 0 ? load_global(scale_at) : 0.0f;
   uint8_t* const codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * D;
 
   float x[PASSES][8], y[PASSES][8], m = 0.0f;
@@ -345,15 +347,19 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
 
 template <int TPT, int PASSES, int THREADS>
 cudaError_t launch_form(const AppendArgs& a, bool bf16, bool pairs, unsigned grid, cudaStream_t stream) {
+  // Programmatic dependent launch: the CTAs are there when the work before them
+  // on the stream ends (pdl_wait), which saves about 2 us of a step's calls.
+  cudaError_t e;
   if (bf16) {
-    if (pairs) kv_append_kernel<TPT, PASSES, THREADS, true, true><<<grid, THREADS, 0, stream>>>(a);
-    else kv_append_kernel<TPT, PASSES, THREADS, true, false><<<grid, THREADS, 0, stream>>>(a);
+    e = pairs ? launch_pdl(kv_append_kernel<TPT, PASSES, THREADS, true, true>, dim3(grid), dim3(THREADS), 0, stream, a)
+              : launch_pdl(kv_append_kernel<TPT, PASSES, THREADS, true, false>, dim3(grid), dim3(THREADS), 0, stream, a);
   } else {
-    if (pairs) kv_append_kernel<TPT, PASSES, THREADS, false, true><<<grid, THREADS, 0, stream>>>(a);
-    else kv_append_kernel<TPT, PASSES, THREADS, false, false><<<grid, THREADS, 0, stream>>>(a);
+    e = pairs ? launch_pdl(kv_append_kernel<TPT, PASSES, THREADS, false, true>, dim3(grid), dim3(THREADS), 0, stream, a)
+              : launch_pdl(kv_append_kernel<TPT, PASSES, THREADS, false, false>, dim3(grid), dim3(THREADS), 0, stream, a);
   }
+  if (e != cudaSuccess) return e;
   plan_add("kv_append_kernel");
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 // With few new tokens a sequence (a decode step) a CTA's work is a chain of

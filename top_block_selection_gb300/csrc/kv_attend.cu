@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __
   __shared__ float s_f[kCombineRows][kKvMaxCtas];
   __shared__ float s_max[kCombineRows][4], s_sum[kCombineRows][4];
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: at most one kernel ahead of the one that runs
   const int group = threadIdx.x / 128, tid = threadIdx.x % 128, rows = a.qt * a.R, D = a.c.D;
   const int c0 = blockIdx.x, r = blockIdx.y * kCombineRows + group;
   const int4 job = *reinterpret_cast<const int4*>(a.jobs + 4 * c0);

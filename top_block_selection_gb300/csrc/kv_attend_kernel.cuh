@@ -433,21 +433,21 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
       const int slot = (w.t + first + (k0 + my_k) * W) * spt + my_slot;
       const bool in_part = k0 + my_k < own;
       int blk = in_part ? slot : -1;
-      if (list) blk = in_part && slot < a.k ? __ldg(list + slot) : -1;
+      if (list) blk = in_part && slot < a.k ? load_global(list + slot) : -1;
       if (list && blk >= a.c.max_blocks) {
         bad = true;
         blk = -1;
       }
       if (blk >= 0 && static_cast<int64_t>(blk) * a.c.block >= keys) blk = -1;
-      int page = blk >= 0 ? __ldg(table + blk) : -1;
+      int page = blk >= 0 ? load_global(table + blk) : -1;
       if (blk >= 0 && (page < 0 || page >= a.c.n_pages)) {
         bad = true;
         blk = page = -1;
       }
       float ks = 0.0f, vs = 0.0f;
       if (page >= 0) {
-        ks = __ldg(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
-        vs = __ldg(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+        ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+        vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
       }
       const int z = page >= 0 ? page : a.c.n_pages;  // no block: reads past the last page give zeros
       const int base = page >= 0 ? blk * a.c.block : kKvNoToken;
@@ -523,11 +523,11 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
                                   static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
                                   lane * kPer;
       if (kPer == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 v = load_global(reinterpret_cast<const uint2*>(src));
         u[k][0] = v.x;
         u[k][kPer / 2 - 1] = v.y;
       } else {
-        u[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        u[k][0] = load_global(reinterpret_cast<const uint32_t*>(src));
       }
     }
   }
@@ -1039,9 +1039,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   AttendShared<C>& s = *reinterpret_cast<AttendShared<C>*>(p_smem + C::kPRegion);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
-  pdl_launch_dependents();
   if (tid == 0) {
-    a.jobs[4 * blockIdx.x] = -1;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&s.full[i], 2);
       mbar_init(&s.empty[i], 1);
@@ -1058,10 +1056,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  // What is above overlaps the end of the work before this launch.
+  pdl_wait();
+  fence_proxy_async_global();  // its plain stores, before this kernel's bulk loads
+  // The accumulators' memory is asked for only now, and later kernels of the
+  // stream may start only once every CTA has it: a kernel that waits for this
+  // one, or that this one waits for, then never holds what the other needs.
   if (warp == 0) {
     tmem_alloc(&s.tmem, C::kTmemCols);
     tmem_relinquish();
   }
+  if (tid == 0) a.jobs[4 * blockIdx.x] = -1;
 
   // This CTA's share of all tiles, [total c / grid, total (c + 1) / grid), and
   // the item that its first tile belongs to. Every item of a list has the same
@@ -1159,6 +1164,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  pdl_launch_dependents();
   if (hi > lo) {
     if (warp < C::W * 4) {
       attend_consume<C>(a, s, ring, q_smem, p_smem, start, lo - start.walk.t, total, grid);
@@ -1190,8 +1196,7 @@ cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const Atte
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  kv_attend_kernel<C><<<grid, C::kThreads, smem, stream>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_pdl(kv_attend_kernel<C>, dim3(grid), dim3(C::kThreads), smem, stream, tk, tv, a);
 }
 
 // All row counts of one head size and term count (kv_attend_d*_t*.cu).

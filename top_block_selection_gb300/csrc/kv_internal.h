@@ -62,6 +62,47 @@ constexpr int kKvMaxGroup = 32;             // query heads per KV head
 constexpr uint32_t kKvIndexBit = 1u << 5;   // kErrCacheIndex (qsa_device.cuh) for host code
 
 #ifdef __CUDACC__
+// Loads of what an earlier kernel on the stream may have written. These kernels
+// start before that one has ended (programmatic dependent launch) and wait for
+// it, so the read-only path, which takes memory to be constant over a kernel's
+// life, is not for them.
+__device__ __forceinline__ int32_t load_global(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_global(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_global(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load_global(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_global(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_global(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // The new tokens of sequence b: the first n_new of its n rows, at positions
 // first .. len - 1 (first < 0: those before position 0 do not exist).
 struct Span {
@@ -69,8 +110,8 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const KvCacheArgs& c, int b, int n) {
   Span s;
-  s.len = __ldg(c.lens + b);
-  s.n_new = c.n_new ? min(max(__ldg(c.n_new + b), 0), n) : n;
+  s.len = load_global(c.lens + b);
+  s.n_new = c.n_new ? min(max(load_global(c.n_new + b), 0), n) : n;
   s.len = max(s.len, 0);
   s.first = s.len - s.n_new;
   return s;
