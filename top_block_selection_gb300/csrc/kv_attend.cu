@@ -12,7 +12,10 @@ constexpr int kCombineRows = 4;  // rows of a CTA, 128 threads each
 // Joins the parts of the item that CTA blockIdx.x of the attention began and
 // others ended: that CTA's second slot and the first slots of the CTAs after
 // it, added in order. A CTA a row would be up to 4,900 CTAs, nearly all with
-// nothing to do, and their launch longer than the work.
+// nothing to do, and their launch longer than the work: one token over 1,000
+// tokens took 10.8 us instead of 9.7. The sums are fp32 and the parts added in
+// the order of the tokens, so a call repeats its bits. It is bound by its
+// launch and two dependent loads: about 2 us.
 __global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ float s_f[kCombineRows][kKvMaxCtas];
   __shared__ float s_max[kCombineRows][4], s_sum[kCombineRows][4];
