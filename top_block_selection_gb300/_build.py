@@ -29,10 +29,10 @@ BINDINGPATH = os.path.join(LIBDIR, "_qsa_kv.so")
 SOURCES = ["qsa_runtime.cu", "score_tc.cu", "select.cu", "convert.cu", "fused.cu", "fused_h1.cu",
            "fused_h2.cu", "fused_h4.cu", "fused_h8.cu", "fused_h16.cu", "fused_h32.cu",
            "split_reduce.cu", "split_reduce_static.cu", "kv_append.cu", "kv_attend.cu",
-           "kv_attend_d64_t2.cu", "kv_attend_d64_t3.cu", "kv_attend_d128_t2.cu", "kv_attend_d128_t3.cu",
+           "kv_attend_many.cu", "kv_attend_d64_t2.cu", "kv_attend_d64_t3.cu", "kv_attend_d128_t2.cu", "kv_attend_d128_t3.cu",
            "qsa_api.cpp"]
 HEADERS = ["qsa_device.cuh", "qsa_internal.h", "select_row.cuh", "select_warp.cuh", "fused_kernel.cuh",
-           "kv_internal.h", "kv_attend_kernel.cuh"]
+           "kv_internal.h", "kv_attend_kernel.cuh", "kv_attend_many.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

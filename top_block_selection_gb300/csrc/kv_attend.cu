@@ -1,6 +1,6 @@
 // kv_attend.cu - launcher of the cache attention, and the kernel that joins
 // the partial results of items that were split over several CTAs.
-#include "kv_attend_kernel.cuh"
+#include "kv_attend_many.cuh"
 
 #include <algorithm>
 
@@ -61,6 +61,16 @@ __global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __
     a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
+// Whether kv_attend_many_kernel takes a call over the whole cache: where a tile
+// of its rows is full, and there are so many rows in all that joining parts of
+// 256 rows does not outweigh its faster tiles. Both forms, 4 to 32 heads of 128
+// dimensions, us (many | kv_attend_kernel): 8 KV heads x 128 rows over 8,192
+// tokens 33.5 | 29.3, 8 x 256 36.1 | 40.2, 8 x 512 45.7 | 65.4; 64 x 128 rows
+// over 4,096 53.6 | 67.9; 1 x 256 over 32,768 42.5 | 28.3, 1 x 512 41 | 39.
+bool takes_many(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
+  return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 2048;
+}
+
 // Rows of the instantiation for `rows` of them.
 int rows_form(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
@@ -82,7 +92,8 @@ bool encode_cache_map(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c
 size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kKvMaxGroup || (D != 64 && D != 128))
     return 0;
-  return sizeof(float) * 2 * kKvMaxCtas * kKvMaxGroup * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
+  const size_t rows = takes_many(B, n, Hq, Hkv) ? 2 * kManyRows : kKvMaxGroup;
+  return sizeof(float) * 2 * kKvMaxCtas * rows * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
 }
 
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
@@ -102,11 +113,14 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   a.spt = kKvTile / p.cache.block;
   a.bf16 = p.bf16;
   // Chosen blocks are each query's own; over the whole cache, consecutive
-  // queries of a sequence share a tile, up to 16 rows: the form of 32 rows holds
-  // too much state for its threads and takes more than twice as long a tile.
-  a.qt = p.ids ? 1 : std::max(1, std::min(p.n, 16 / a.R));
+  // queries of a sequence share a tile, of up to 16 rows (the form of 32 rows
+  // holds too much state for its threads and takes more than twice as long a
+  // tile) or two of up to 128.
+  const bool many = !p.ids && takes_many(p.cache.B, p.n, p.Hq, p.cache.Hkv);
+  a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / a.R));
   a.n_qt = (p.n + a.qt - 1) / a.qt;
   a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
+  a.item_cost = many ? kManyItemCost : 0;
   const int rt = rows_form(a.qt * a.R);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
   const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
@@ -114,6 +128,8 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sm_count, kKvMaxCtas), most));
   a.jobs = static_cast<int32_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
+
+  if (many) return launch_attend_many(a, grid, item_tiles > 1, dev.id, stream);
 
   CUtensorMap tk, tv;
   if (!encode_cache_map(&tk, p.cache.k, p.cache) || !encode_cache_map(&tv, p.cache.v, p.cache))

@@ -85,6 +85,7 @@ struct AttendArgs {
   int32_t n_lists, k;
   int32_t spt;       // blocks of a tile
   int32_t fixed;     // tiles of every item over chosen blocks, else 0
+  int32_t item_cost; // what an item costs beside its tiles, in tiles: counts where they are dealt out
   bool bf16;
 };
 
@@ -1033,6 +1034,107 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   }
 }
 
+// This CTA's share of all tiles, [total c / grid, total (c + 1) / grid), and
+// the item that its first tile belongs to. An item counts item_cost tiles more
+// than it has, in front of them. Every item of a list has the same
+// tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
+// to the CTA's threads (by way of scan and shared, in shared memory). Every
+// thread of the CTA calls it.
+template <int kThreads>
+__device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, Start& shared, Start& start,
+                                           int64_t& total, int64_t& lo, int64_t& hi, int& grid) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int entries = a.c.B * a.n_qt, heads = a.c.Hkv;
+  auto share = [&](int64_t tiles) {
+    total = tiles * heads;
+    grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int cta = blockIdx.x;
+    lo = hi = 0;
+    if (cta < grid) {
+      lo = divide(total * cta, grid);
+      hi = divide(total * (cta + 1), grid);
+    }
+    start.walk.left = hi - lo;
+  };
+  // The walk starts in the item of entry e, whose tiles begin at `at`.
+  auto begin = [&](int e, const Entry& en, int64_t at) {
+    const int each = en.tiles + a.item_cost;
+    const int64_t h = divide(lo - at, each);
+    start.walk.e = e;
+    start.walk.h = static_cast<int32_t>(h);
+    start.walk.t = static_cast<int32_t>(lo - at - h * each) - a.item_cost;
+    start.entry = en;
+  };
+  if (a.fixed > 0) {
+    const int64_t each = static_cast<int64_t>(a.fixed) * heads;
+    share(static_cast<int64_t>(entries) * a.fixed);
+    const int64_t e = divide(lo, each);
+    begin(static_cast<int>(e), entry_of(a, static_cast<int>(e)), e * each);
+  } else if (entries <= 32) {
+    Entry mine{};
+    if (lane < entries) mine = entry_of(a, lane);
+    const int units = lane < entries ? mine.tiles + a.item_cost : 0;
+    int64_t before = units;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += v;
+    }
+    share(__shfl_sync(0xFFFFFFFFu, before, 31));
+    before = (before - units) * heads;
+    const int e = __popc(__ballot_sync(0xFFFFFFFFu, lane < entries && before <= lo)) - 1;
+    Entry en;
+    en.b = __shfl_sync(0xFFFFFFFFu, mine.b, e);
+    en.j0 = __shfl_sync(0xFFFFFFFFu, mine.j0, e);
+    en.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, e);
+    en.first_pos = __shfl_sync(0xFFFFFFFFu, mine.first_pos, e);
+    en.last_pos = __shfl_sync(0xFFFFFFFFu, mine.last_pos, e);
+    en.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, e);
+    begin(e, en, __shfl_sync(0xFFFFFFFFu, before, e));
+  } else {
+    const int64_t per = (entries + kThreads - 1) / kThreads;
+    const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
+    int64_t sum = 0;
+    Entry mine{};
+    for (int64_t e = e0; e < e1; ++e) {
+      mine = entry_of(a, static_cast<int>(e));
+      sum += mine.tiles + a.item_cost;
+    }
+    int64_t before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += v;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    int64_t all = 0;
+    before -= sum;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+    share(all);
+    int64_t at = before * heads;
+    if (at <= lo && lo < at + sum * heads) {
+      int64_t e = e0;
+      if (per > 1)
+        for (;; ++e) {
+          mine = entry_of(a, static_cast<int>(e));
+          const int64_t units = static_cast<int64_t>(mine.tiles + a.item_cost) * heads;
+          if (lo < at + units) break;
+          at += units;
+        }
+      begin(static_cast<int>(e), mine, at);
+      shared = start;
+    }
+    __syncthreads();
+    start = shared;
+    start.walk.left = hi - lo;
+  }
+}
+
 // -------------------------------------------------------------- the kernel
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1)
@@ -1043,7 +1145,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint8_t* const q_smem = ring + C::kStages * C::kStageBytes;
   uint8_t* const p_smem = q_smem + 2 * C::kQBytes;
   AttendShared<C>& s = *reinterpret_cast<AttendShared<C>*>(p_smem + C::kPRegion);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = tid / 32;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -1074,99 +1176,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   if (tid == 0) a.jobs[4 * blockIdx.x] = -1;
 
-  // This CTA's share of all tiles, [total c / grid, total (c + 1) / grid), and
-  // the item that its first tile belongs to. Every item of a list has the same
-  // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
-  // to the CTA's threads.
-  const int entries = a.c.B * a.n_qt, heads = a.c.Hkv;
   Start start{};
   int64_t total, lo, hi;
   int grid;
-  auto share = [&](int64_t tiles) {
-    total = tiles * heads;
-    grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    const int cta = blockIdx.x;
-    lo = hi = 0;
-    if (cta < grid) {
-      lo = divide(total * cta, grid);
-      hi = divide(total * (cta + 1), grid);
-    }
-    start.walk.left = hi - lo;
-  };
-  // The walk starts in the item of entry e, whose tiles begin at `at`.
-  auto begin = [&](int e, const Entry& en, int64_t at) {
-    const int64_t h = divide(lo - at, en.tiles);
-    start.walk.e = e;
-    start.walk.h = static_cast<int32_t>(h);
-    start.walk.t = static_cast<int32_t>(lo - at - h * en.tiles);
-    start.entry = en;
-  };
-  if (a.fixed > 0) {
-    const int64_t each = static_cast<int64_t>(a.fixed) * heads;
-    share(static_cast<int64_t>(entries) * a.fixed);
-    const int64_t e = divide(lo, each);
-    begin(static_cast<int>(e), entry_of(a, static_cast<int>(e)), e * each);
-  } else if (entries <= 32) {
-    Entry mine{};
-    if (lane < entries) mine = entry_of(a, lane);
-    int64_t before = mine.tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
-      if (lane >= d) before += v;
-    }
-    share(__shfl_sync(0xFFFFFFFFu, before, 31));
-    before = (before - mine.tiles) * heads;
-    const int e = __popc(__ballot_sync(0xFFFFFFFFu, lane < entries && before <= lo)) - 1;
-    Entry en;
-    en.b = __shfl_sync(0xFFFFFFFFu, mine.b, e);
-    en.j0 = __shfl_sync(0xFFFFFFFFu, mine.j0, e);
-    en.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, e);
-    en.first_pos = __shfl_sync(0xFFFFFFFFu, mine.first_pos, e);
-    en.last_pos = __shfl_sync(0xFFFFFFFFu, mine.last_pos, e);
-    en.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, e);
-    begin(e, en, __shfl_sync(0xFFFFFFFFu, before, e));
-  } else {
-    const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
-    const int64_t e0 = min(per * tid, static_cast<int64_t>(entries)), e1 = min(e0 + per, static_cast<int64_t>(entries));
-    int64_t sum = 0;
-    Entry mine{};
-    for (int64_t e = e0; e < e1; ++e) {
-      mine = entry_of(a, static_cast<int>(e));
-      sum += mine.tiles;
-    }
-    int64_t before = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
-      if (lane >= d) before += v;
-    }
-    if (lane == 31) s.scan[warp] = before;
-    __syncthreads();
-    int64_t all = 0;
-    before -= sum;
-#pragma unroll 1
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += s.scan[w];
-      all += s.scan[w];
-    }
-    share(all);
-    int64_t at = before * heads;
-    if (at <= lo && lo < at + sum * heads) {
-      int64_t e = e0;
-      if (per > 1)
-        for (;; ++e) {
-          mine = entry_of(a, static_cast<int>(e));
-          if (lo < at + static_cast<int64_t>(mine.tiles) * heads) break;
-          at += static_cast<int64_t>(mine.tiles) * heads;
-        }
-      begin(static_cast<int>(e), mine, at);
-      s.start = start;
-    }
-    __syncthreads();
-    start = s.start;
-    start.walk.left = hi - lo;
-  }
+  find_share<C::kThreads>(a, s.scan, s.start, start, total, lo, hi, grid);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
