@@ -43,6 +43,11 @@ constexpr int kManyItemCost = 3;   // an item's queries and results, and its til
 constexpr float kManyLag = 8.0f;   // log2 that a reference may fall behind
 constexpr float kManyScale = 64.0f;  // of a probability 1 at the largest value scale: 2^14 at most
 
+// Places for scores in tensor memory: 128 columns each beside the two outputs.
+// With three of them the scores of a row tile's next key tile are there when
+// its warpgroup has done with the last one's.
+__host__ __device__ constexpr int many_buffers(int D) { return (512 - 2 * D) / 128; }
+
 struct ManyMeta {
   alignas(16) float ks[8], vs[8];  // key and value scales of 16 tokens each
   alignas(16) int32_t page[8];     // -1: no block
@@ -58,7 +63,7 @@ struct ManyShared {
   float row_mul[2][kManyRows];
   uint64_t meta_full[kManyRing], meta_empty[kManyRing];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[many_buffers(D)], p_full[many_buffers(D)], o_full[2];
   int64_t scan[kManyThreads / 32];
   Start start;
   uint32_t tmem, stop;
@@ -141,8 +146,12 @@ __device__ __forceinline__ void many_items(const AttendArgs& a, const Start& sta
     }
   }
 }
+// Whether row tile w has rows to work on. With three places for scores both row
+// tiles always work (on zeros, if need be): a place's barrier is then waited for
+// by the two in turn, each after the other's unit, and none runs ahead of it.
+template <int D>
 __device__ __forceinline__ bool many_active(const AttendArgs& a, const Entry& en, int w) {
-  return en.nq > w * (a.qt / 2);
+  return many_buffers(D) > 2 || en.nq > w * (a.qt / 2);
 }
 
 // ------------------------------------------------------------ pages, scales
@@ -319,81 +328,83 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
 }
 
 // ---------------------------------------------------------------- products
-// One warp, in a fixed order: the output of row tile 0 and its next scores,
-// then those of row tile 1. Whatever the two warpgroups begin with, one then
-// has its products while the other has the exponentials. (A warp for each row
-// tile let both fall into step: 1.9 times as long a tile.)
+// One warp, in a fixed order: units of a row tile and a key tile, the row tiles
+// in turn; a unit's output, then the scores of the unit that gets its place.
+// Whatever the two warpgroups begin with, one then has its products while the
+// other has the exponentials. (A warp for each row tile let both fall into step:
+// 1.9 times as long a tile.)
 template <int D, bool BF16>
 __device__ void many_products(const AttendArgs& a, ManyShared<D>& s, uint32_t q_addr, uint32_t k_addr, uint32_t v_addr,
                               const Start& start) {
-  constexpr uint32_t kBytes = kKvTile * D * 2, kPanel = kKvTile * 128;
-  const uint32_t tmem = uniform(s.tmem);
+  constexpr uint32_t kBytes = kKvTile * D * 2, kPanel = kKvTile * 128, kBuffers = many_buffers(D);
+  const uint32_t tmem = uniform(s.tmem), tm_out = tmem + kBuffers * 128;
   // Values run along N: the next 64 dimensions a panel further (leading
   // offset), the next 8 tokens 1024 bytes (stride offset).
   const uint64_t v_mn = (smem_desc_rows<128>(0) & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(kPanel >> 4) << 16);
   const bool leader = elect_one();
-  uint32_t g = 0, it[2] = {0, 0}, n[2] = {0, 0};  // tiles; items and tiles of each row tile so far
-  // The scores of row tile w on tile `at`.
-  auto scores = [&](int w, uint32_t at, bool active) {
-    const uint32_t buf = at & 1;
-    wait_or_stop(&s.k_full[buf], (at >> 1) & 1, &s.stop, a.status);
-    __syncwarp();
-    tc_fence_after_sync();
-    if (leader) {
-      if (active) {
-        const uint64_t q_desc = smem_desc_rows<128>(q_addr + w * kBytes);
-        const uint64_t k_desc = smem_desc_rows<128>(k_addr + buf * kBytes);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t step = ((ks / 4) * kPanel + (ks % 4) * 32) >> 4;
-          mma_f16_ss(tmem + w * 128, q_desc + step, k_desc + step, idesc_many(kKvTile, BF16, false), ks > 0);
-        }
-        mma_commit(&s.s_full[w]);
-        mma_commit(&s.k_empty[buf]);
-      } else {
-        mbar_arrive(&s.k_empty[buf]);
-      }
-    }
-    __syncwarp();
-  };
+  uint32_t g0 = 0, it[2] = {0, 0}, n[2] = {0, 0};  // tiles; items and tiles of each row tile so far
   many_items(a, start, 0, [&](const Entry& en, const ManyItem& wk) {
-    const int part = wk.tiles;
-    const bool active[2] = {many_active(a, en, 0), many_active(a, en, 1)};
+    const bool active[2] = {many_active<D>(a, en, 0), many_active<D>(a, en, 1)};
+    const uint32_t end = 2 * (g0 + wk.tiles);
+    // Unit u: row tile u % 2 on tile u / 2.
+    auto scores = [&](uint32_t u) {
+      const uint32_t buf = u / 2 & 1, at = u % kBuffers;
+      wait_or_stop(&s.k_full[buf], (u >> 2) & 1, &s.stop, a.status);
+      __syncwarp();
+      tc_fence_after_sync();
+      if (leader) {
+        if (u & 1 ? active[1] : active[0]) {
+          const uint64_t q_desc = smem_desc_rows<128>(q_addr + (u & 1) * kBytes);
+          const uint64_t k_desc = smem_desc_rows<128>(k_addr + buf * kBytes);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (active[w]) wait_or_stop(&s.q_full[w], it[w]++ & 1, &s.stop, a.status);
-      scores(w, g, active[w]);
-    }
-    for (int i = 0; i < part; ++i, ++g) {
-      const uint32_t buf = g & 1;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (active[w]) wait_or_stop(&s.p_full[w], n[w] & 1, &s.stop, a.status);
-        wait_or_stop(&s.v_full[buf], (g >> 1) & 1, &s.stop, a.status);
-        __syncwarp();
-        tc_fence_after_sync();
-        if (leader) {
-          if (active[w]) {
-            const uint64_t v_desc = v_mn | ((v_addr + buf * kBytes) >> 4);
-            const uint32_t tm_s = tmem + w * 128, tm_o = tmem + 256 + w * D;
-#pragma unroll
-            for (int ks = 0; ks < kKvTile / 16; ++ks) {
-              const uint32_t p_at = tm_s + (ks / 2) * 32 + (ks % 2) * 8;
-              mma_f16_ts(tm_o, p_at, v_desc + ks * (2048 >> 4), idesc_many(D, false, true), i > 0 || ks > 0);
-              if (!BF16) mma_f16_ts(tm_o, p_at + 16, v_desc + ks * (2048 >> 4), idesc_many(D, false, true), 1u);
-            }
-            mma_commit(&s.o_full[w]);
-            mma_commit(&s.v_empty[buf]);
-          } else {
-            mbar_arrive(&s.v_empty[buf]);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t step = ((ks / 4) * kPanel + (ks % 4) * 32) >> 4;
+            mma_f16_ss(tmem + at * 128, q_desc + step, k_desc + step, idesc_many(kKvTile, BF16, false), ks > 0);
           }
+          mma_commit(&s.s_full[at]);
+          mma_commit(&s.k_empty[buf]);
+        } else {
+          mma_commit(&s.s_full[at]);
+          mbar_arrive(&s.k_empty[buf]);
         }
-        __syncwarp();
-        // The next scores take the place of the probabilities.
-        if (active[w]) wait_or_stop(&s.o_full[w], n[w]++ & 1, &s.stop, a.status);
-        if (i + 1 < part) scores(w, g + 1, active[w]);
       }
+      __syncwarp();
+    };
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (active[w]) wait_or_stop(&s.q_full[w], it[w]++ & 1, &s.stop, a.status);
+#pragma unroll 1
+    for (uint32_t u = 2 * g0; u < min(end, 2 * g0 + kBuffers); ++u) scores(u);
+#pragma unroll 1
+    for (uint32_t u = 2 * g0; u < end; ++u) {
+      const uint32_t w = u & 1, buf = u / 2 & 1, at = u % kBuffers;
+      wait_or_stop(&s.p_full[at], (u / kBuffers) & 1, &s.stop, a.status);
+      wait_or_stop(&s.v_full[buf], (u >> 2) & 1, &s.stop, a.status);
+      __syncwarp();
+      tc_fence_after_sync();
+      const bool work = w ? active[1] : active[0];
+      if (leader) {
+        if (work) {
+          const uint64_t v_desc = v_mn | ((v_addr + buf * kBytes) >> 4);
+          const uint32_t tm_o = tm_out + w * D;
+#pragma unroll
+          for (int ks = 0; ks < kKvTile / 16; ++ks) {
+            const uint32_t p_at = tmem + at * 128 + (ks / 2) * 32 + (ks % 2) * 8;
+            mma_f16_ts(tm_o, p_at, v_desc + ks * (2048 >> 4), idesc_many(D, false, true), u / 2 > g0 || ks > 0);
+            if (!BF16) mma_f16_ts(tm_o, p_at + 16, v_desc + ks * (2048 >> 4), idesc_many(D, false, true), 1u);
+          }
+          mma_commit(&s.o_full[w]);
+          mma_commit(&s.v_empty[buf]);
+        } else {
+          mbar_arrive(&s.v_empty[buf]);
+        }
+      }
+      __syncwarp();
+      // Scores take the place of these probabilities.
+      if (work) wait_or_stop(&s.o_full[w], (w ? n[1]++ : n[0]++) & 1, &s.stop, a.status);
+      if (u + kBuffers < end) scores(u + kBuffers);
     }
+    g0 += wk.tiles;
   });
 }
 
@@ -515,12 +526,13 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
                           int64_t total, int grid, int w) {
   const int warp = uniform(static_cast<int>(threadIdx.x / 32 % 4)), t = threadIdx.x % 128, lane = t % 32;
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t tm_s = uniform(s.tmem) + w * 128 + lane_addr, tm_o = uniform(s.tmem) + 256 + w * D + lane_addr;
+  constexpr uint32_t kBuffers = many_buffers(D);
+  const uint32_t tm_o = uniform(s.tmem) + kBuffers * 128 + w * D + lane_addr;
   const int qt = a.qt / 2, jt = t / a.R, j = w * qt + jt;
-  uint32_t g = 0, it = 0, n = 0;
+  uint32_t g = 0, it = 0, n = 0;  // tiles, items, tiles of this row tile so far
   many_items(a, start, lo, [&](const Entry& en, const ManyItem& wk) {
     const int part = wk.tiles;
-    const bool active = many_active(a, en, w);
+    const bool active = many_active<D>(a, en, w);
     const bool begins = wk.t == 0, ends = wk.t + part == en.tiles;
     const int slot = begins && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
     if (begins && !ends && w == 0 && t == 0) {
@@ -545,14 +557,20 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
     }
     for (int i = 0; i < part; ++i, ++g) {
       const uint32_t at = g % kManyRing;
+      const uint32_t unit = 2 * g + w, buf = unit % kBuffers;  // as in many_products
       wait_or_stop(&s.meta_full[at], (g / kManyRing) & 1, &s.stop, a.status);
-      if (active) {
+      if (!active) {  // keeps its turn, with nothing to do
+        wait_or_stop(&s.s_full[buf], (unit / kBuffers) & 1, &s.stop, a.status);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[buf]);
+      } else {
         const ManyMeta& meta = s.meta[at];
         const int pos0 = (wk.t + i) * kKvTile;
         const uint32_t holes = meta.holes;
         const bool masked = holes != 0 || pos0 + kKvTile - 1 > lo_pos;
         const float vmax = meta.vmax;
-        wait_or_stop(&s.s_full[w], n & 1, &s.stop, a.status);
+        const uint32_t tm_s = uniform(s.tmem) + buf * 128 + lane_addr;
+        wait_or_stop(&s.s_full[buf], (unit / kBuffers) & 1, &s.stop, a.status);
         __syncwarp();
         tc_fence_after_sync();
         // The loops over 32 columns stay loops: unrolled, the code of a tile does
@@ -623,7 +641,7 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[w]);
+        if (lane == 0) mbar_arrive(&s.p_full[buf]);
         ++n;
       }
       if (i + 1 < part) {
@@ -716,9 +734,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
       mbar_init(&s.v_full[i], 4);
       mbar_init(&s.v_empty[i], 2);
       mbar_init(&s.q_full[i], 4);
+      mbar_init(&s.o_full[i], 1);
+    }
+    for (int i = 0; i < many_buffers(D); ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
-      mbar_init(&s.o_full[i], 1);
     }
     s.stop = 0;
     fence_mbarrier_init();
