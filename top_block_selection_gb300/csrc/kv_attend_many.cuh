@@ -475,6 +475,12 @@ __device__ __forceinline__ void many_queries(const AttendArgs& a, ManyShared<D>&
   if (lane == 0) mbar_arrive(&s.q_full[w]);
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {  // NaN counts as nothing
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // A row's scores of 32 tokens against its reference -> their probabilities'
 // sum and, times the value scales, fp16 terms in the place of the scores. MASK:
 // of the first and second 16 tokens those up to limit0 and limit1 count, and the
@@ -576,6 +582,7 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
         // The loops over 32 columns stay loops: unrolled, the code of a tile does
         // not fit the instruction caches (a quarter of all stalls).
         float top = -INFINITY;
+        float2 ks = *reinterpret_cast<const float2*>(&meta.ks[0]);  // a step ahead
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           float x[32];
@@ -592,11 +599,13 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
           }
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float mx = x[hf * 16];
+            float mx = max3(x[hf * 16], x[hf * 16 + 1], x[hf * 16 + 2]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[hf * 16 + e]);
-            top = fmaxf(top, mx * (mul * meta.ks[2 * c + hf]));
+            for (int e = 3; e < 15; e += 2) mx = max3(mx, x[hf * 16 + e], x[hf * 16 + e + 1]);
+            mx = fmaxf(mx, x[hf * 16 + 15]);
+            top = fmaxf(top, mx * (mul * (hf == 0 ? ks.x : ks.y)));
           }
+          ks = *reinterpret_cast<const float2*>(&meta.ks[(2 * c + 2) & 7]);
         }
         const bool move = top > m + kManyLag, grow = vmax > vref;
         if (__any_sync(0xFFFFFFFFu, move) || grow) {
@@ -626,10 +635,12 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
         }
         const bool huge = __any_sync(0xFFFFFFFFu, m > 1048576.0f || (m < -1048576.0f && m != kUnset));
         const float inv = vref > 0.0f ? __fdividef(kManyScale, vref) : 0.0f;
+        float2 vs = *reinterpret_cast<const float2*>(&meta.vs[0]);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const float f0 = mul * meta.ks[2 * c], f1 = mul * meta.ks[2 * c + 1];
-          const float v0 = meta.vs[2 * c] * inv, v1 = meta.vs[2 * c + 1] * inv;
+          const float f0 = mul * ks.x, f1 = mul * ks.y, v0 = vs.x * inv, v1 = vs.y * inv;
+          ks = *reinterpret_cast<const float2*>(&meta.ks[(2 * c + 2) & 7]);
+          vs = *reinterpret_cast<const float2*>(&meta.vs[(2 * c + 2) & 7]);
           if (masked || huge) {
             const int limit = row_pos - pos0 - c * 32;
             many_probabilities<BF16, true>(tm_s + c * 32, f0, f1, v0, v1, m, (holes >> (2 * c)) & 1 ? -1 : limit,
