@@ -193,3 +193,21 @@ def test_many_and_few_rows_agree(tbs):  # noqa: F811
         one = tbs.qsa_kv_attend(q[:, j:j + 1], *args[:5], lens)
         diff = (one.double() - many[:, j:j + 1].double()).norm() / one.double().norm()
         assert float(diff) <= 4 * UNIT["f16"]
+
+
+def test_many_offsets_past_32_bits(tbs):  # noqa: F811
+    """Pages behind 2^32 bytes of a cache."""
+    Hkv, block, D = 8, 128, 128
+    pages = (1 << 32) // (Hkv * block * D) + 10
+    c = kc.make_cache([300], Hkv, block, D, seed=1)
+    args, _ = on_gpu(c)
+    used = args[0].shape[0]
+    far = []
+    for t in args[:4]:
+        f = torch.zeros((pages, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        f[pages - used:] = t
+        far.append(f)
+    table = torch.where(args[4] >= 0, args[4] + pages - used, args[4])
+    q = torch.randn((1, 128, 2 * Hkv, D), dtype=torch.float16, device="cuda")
+    assert torch.equal(tbs.qsa_kv_attend(q, *far, table, args[5]), tbs.qsa_kv_attend(q, *args))
+    assert "kv_attend_many_kernel" in tbs.qsa_arm()

@@ -114,7 +114,7 @@ def test_chosen_order_does_not_matter(seed):
     assert np.allclose(a[0], b[0], rtol=1e-13) and np.allclose(a[1], b[1], rtol=1e-13)
 
 
-def test_checker_sees_a_wrong_result():
+def test_bound_sees_a_wrong_result():
     """The bound rejects a result that lost a token, or took its scale twice."""
     c = kc.make_cache([60], 1, 32, 64, seed=5)
     q = np.random.default_rng(6).standard_normal((1, 1, 1, 64))
