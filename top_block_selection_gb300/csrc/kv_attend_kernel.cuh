@@ -133,6 +133,13 @@ struct Start {
   Entry entry;  // of walk.e
 };
 
+// A CTA's share of all tiles, [lo, hi) of total dealt to `grid` CTAs.
+struct Share {
+  Start start;
+  int64_t lo, hi, total;
+  int32_t grid;
+};
+
 // ------------------------------------------------------------ tcgen05 pieces
 // D[tmem] (+)= A[smem] * B[smem]^T on e4m3 codes, issued by one thread.
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -385,8 +392,8 @@ struct AttendShared {
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_bar[C::W];
-  int64_t scan[C::kThreads / 32];
-  Start start;
+  int64_t scan[C::W + 1];
+  Share share;
   uint32_t tmem;
   uint32_t stop;
 };
@@ -708,13 +715,12 @@ constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
-                               uint8_t* p_smem, const Start& start, int64_t at0, int64_t total, int grid) {
+                               uint8_t* p_smem) {
   constexpr int RT = C::RT, N = C::N, W = C::W, D = C::D;
   constexpr int kAll = W * 128;
   const int wg = uniform(static_cast<int>(threadIdx.x / 128)), warp = uniform(static_cast<int>(threadIdx.x / 32 % 4));
   const int t = threadIdx.x % 128, lane = t % 32;
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t tm_s = uniform(s.tmem) + wg * 2 * N, tm_o = tm_s + N;
   uint8_t* const p_buf = p_smem + wg * C::kPBytes;
   const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem), p_addr = smem_u32(p_buf);
   const int my_slot = t / a.c.block, my_off = t - my_slot * a.c.block;
@@ -724,6 +730,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const bool leader = elect_one();
   bool bad = false;     // a wait ran out: what follows is not used
   const float kNegInf = -INFINITY;
+  uint32_t tm_s = 0, tm_o = 0;
 
   // Scores of a tile, issued by one thread of the warpgroup's last warp.
   auto issue_scores = [&](uint32_t st, int buf) {
@@ -738,9 +745,20 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     __syncwarp();
   };
 
+  // The service warps have found the share by now, or will.
+  bar_sync(9, C::kThreads);
+  tc_fence_after_sync();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t total = s.share.total;
+  const int grid = s.share.grid;
+  if (s.share.hi <= s.share.lo) return;
+  tm_s = uniform(s.tmem) + wg * 2 * N;
+  tm_o = tm_s + N;
   {
-    const Walk& walk = start.walk;
-    const Entry& en = start.entry;
+    const Walk walk = s.share.start.walk;
+    const Entry en = s.share.start.entry;
+    const int64_t at0 = s.share.lo - walk.t;
     if (wg * 4 + warp < RT)
       query_rows<C, (RT + W * 4 - 1) / (W * 4)>(a, s.item[0], q_smem, en, walk.h, wg * 4 + warp, W * 4);
     if (threadIdx.x == W * 128 - 1)
@@ -1038,12 +1056,12 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 // the item that its first tile belongs to. An item counts item_cost tiles more
 // than it has, in front of them. Every item of a list has the same
 // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
-// to the CTA's threads (by way of scan and shared, in shared memory). Every
-// thread of the CTA calls it.
-template <int kThreads>
+// to the calling threads: kThreads of them, whole warps from kFirst on (by way
+// of scan and shared, in shared memory, and barrier kBarrier).
+template <int kThreads, int kFirst, int kBarrier>
 __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, Start& shared, Start& start,
                                            int64_t& total, int64_t& lo, int64_t& hi, int& grid) {
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x - kFirst, warp = tid / 32, lane = tid % 32;
   const int entries = a.c.B * a.n_qt, heads = a.c.Hkv;
   auto share = [&](int64_t tiles) {
     total = tiles * heads;
@@ -1107,7 +1125,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
       if (lane >= d) before += v;
     }
     if (lane == 31) scan[warp] = before;
-    __syncthreads();
+    bar_sync(kBarrier, kThreads);
     int64_t all = 0;
     before -= sum;
 #pragma unroll 1
@@ -1129,7 +1147,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
       begin(static_cast<int>(e), mine, at);
       shared = start;
     }
-    __syncthreads();
+    bar_sync(kBarrier, kThreads);
     start = shared;
     start.walk.left = hi - lo;
   }
@@ -1164,38 +1182,46 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  // What is above overlaps the end of the work before this launch.
-  pdl_wait();
-  fence_proxy_async_global();  // its plain stores, before this kernel's bulk loads
-  // The accumulators' memory is asked for only now, and later kernels of the
-  // stream may start only once every CTA has it: a kernel that waits for this
-  // one, or that this one waits for, then never holds what the other needs.
-  if (warp == 0) {
-    tmem_alloc(&s.tmem, C::kTmemCols);
-    tmem_relinquish();
-  }
-  if (tid == 0) a.jobs[4 * blockIdx.x] = -1;
-
-  Start start{};
-  int64_t total, lo, hi;
-  int grid;
-  find_share<C::kThreads>(a, s.scan, s.start, start, total, lo, hi, grid);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  pdl_launch_dependents();
-  if (hi > lo) {
-    if (warp < C::W * 4) {
-      attend_consume<C>(a, s, ring, q_smem, p_smem, start, lo - start.walk.t, total, grid);
-    } else if (warp < C::W * 5) {
-      attend_produce<C>(a, &tm_k, &tm_v, s, ring, start, warp - C::W * 4);
-    } else {
-      attend_queries<C>(a, s, q_smem, start, lo - start.walk.t, total, grid);
+  // The service warps find the CTA's share while the warpgroups enter their code:
+  // its first instructions come from a far cache (1 us of a call's start).
+  constexpr int kService = C::W * 128;
+  if (warp < C::W * 4) {
+    attend_consume<C>(a, s, ring, q_smem, p_smem);
+  } else {
+    // What is above overlaps the end of the work before this launch.
+    pdl_wait();
+    fence_proxy_async_global();  // its plain stores, before this kernel's bulk loads
+    // The accumulators' memory is asked for only now, and later kernels of the
+    // stream may start only once every CTA has it: a kernel that waits for this
+    // one, or that this one waits for, then never holds what the other needs.
+    if (warp == C::W * 4) {
+      tmem_alloc(&s.tmem, C::kTmemCols);
+      tmem_relinquish();
+    }
+    if (tid == kService) a.jobs[4 * blockIdx.x] = -1;
+    Start start{};
+    int64_t total, lo, hi;
+    int grid;
+    find_share<C::kThreads - kService, kService, 10>(a, s.scan, s.share.start, start, total, lo, hi, grid);
+    if (tid == kService) {
+      s.share.start = start;
+      s.share.lo = lo;
+      s.share.hi = hi;
+      s.share.total = total;
+      s.share.grid = grid;
+    }
+    tc_fence_before_sync();
+    bar_sync(9, C::kThreads);
+    tc_fence_after_sync();
+    pdl_launch_dependents();
+    if (hi > lo) {
+      if (warp < C::W * 5) attend_produce<C>(a, &tm_k, &tm_v, s, ring, start, warp - C::W * 4);
+      else attend_queries<C>(a, s, q_smem, start, lo - start.walk.t, total, grid);
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(s.tmem, C::kTmemCols);
+  if (warp == C::W * 4) tmem_dealloc(s.tmem, C::kTmemCols);
 }
 
 // Launch with the given tensor maps on the current device; grid CTAs.

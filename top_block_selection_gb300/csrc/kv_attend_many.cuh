@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
   Start start{};
   int64_t total, lo, hi;
   int grid;
-  find_share<kManyThreads>(a, s.scan, s.start, start, total, lo, hi, grid);
+  find_share<kManyThreads, 0, 0>(a, s.scan, s.start, start, total, lo, hi, grid);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
