@@ -72,8 +72,8 @@ struct ManyShared {
   uint64_t meta_full[kManyRing], meta_empty[kManyRing];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[many_buffers(D)], p_full[many_buffers(D)], o_full[2];
-  int64_t scan[kManyThreads / 32];
-  Start start;
+  int64_t scan[4];
+  Share share;
   uint32_t tmem, stop;
 };
 
@@ -154,6 +154,16 @@ __device__ __forceinline__ void many_items(const AttendArgs& a, const Start& sta
     }
   }
 }
+// Until the CTA's share is known and the accumulators' memory is there.
+template <class S>
+__device__ __forceinline__ void many_begin(S& s) {
+  tc_fence_before_sync();
+  bar_sync(9, kManyThreads);
+  tc_fence_after_sync();
+  pdl_wait();
+  pdl_launch_dependents();
+}
+
 // Whether row tile w has rows to work on. With three places for scores both row
 // tiles always work (on zeros, if need be): a place's barrier is then waited for
 // by the two in turn, each after the other's unit, and none runs ahead of it.
@@ -536,14 +546,18 @@ __device__ __forceinline__ void many_probabilities(uint32_t taddr, float f0, flo
 }
 
 template <int D, bool BF16>
-__device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem, const Start& start, int64_t lo,
-                          int64_t total, int grid, int w) {
+__device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem, int w) {
   const int warp = uniform(static_cast<int>(threadIdx.x / 32 % 4)), t = threadIdx.x % 128, lane = t % 32;
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
   constexpr uint32_t kBuffers = many_buffers(D);
-  const uint32_t tm_o = uniform(s.tmem) + kBuffers * 128 + w * D + lane_addr;
   const int qt = a.qt / 2, jt = t / a.R, j = w * qt + jt;
   uint32_t g = 0, it = 0, n = 0;  // tiles, items, tiles of this row tile so far
+  many_begin(s);
+  if (s.share.hi <= s.share.lo) return;
+  const uint32_t tm_o = uniform(s.tmem) + kBuffers * 128 + w * D + lane_addr;
+  const Start start = s.share.start;
+  const int64_t lo = s.share.lo, total = s.share.total;
+  const int grid = s.share.grid;
   many_items(a, start, lo, [&](const Entry& en, const ManyItem& wk) {
     const int part = wk.tiles;
     const bool active = many_active<D>(a, en, w);
@@ -762,29 +776,38 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
     s.stop = 0;
     fence_mbarrier_init();
   }
-  pdl_wait();
-  if (warp == 0) {  // after the wait, and before later kernels may start: see kv_attend_kernel
-    tmem_alloc(&s.tmem, 512);
-    tmem_relinquish();
+  // The converting warps find the CTA's share, the products' warp asks for
+  // tensor memory (after the wait, and before later kernels may start: see
+  // kv_attend_kernel), and the others enter their code.
+  if (warp < 8) {
+    many_rows<D, BF16>(a, s, q_smem, warp / 4);
+  } else {
+    if (warp < 12) {
+      pdl_wait();
+      if (threadIdx.x == 256) a.jobs[4 * blockIdx.x] = -1;
+      Share found{};
+      int grid;
+      find_share<128, 256, 1>(a, s.scan, s.share.start, found.start, found.total, found.lo, found.hi, grid);
+      if (threadIdx.x == 256) {
+        found.grid = grid;
+        s.share = found;
+      }
+    } else if (warp == 12) {
+      pdl_wait();
+      tmem_alloc(&s.tmem, 512);
+      tmem_relinquish();
+    }
+    many_begin(s);
+    const Start start = s.share.start;
+    if (s.share.hi > s.share.lo) {
+      if (warp < 12) many_convert<D, BF16>(a, s, k16, v16, start);
+      else if (warp == 12) many_products<D, BF16>(a, s, smem_u32(q_smem), smem_u32(k16), smem_u32(v16), start);
+      else many_lookup<D>(a, s, start);
+    }
   }
-  if (threadIdx.x == 0) a.jobs[4 * blockIdx.x] = -1;
-  Start start{};
-  int64_t total, lo, hi;
-  int grid;
-  find_share<kManyThreads, 0, 0>(a, s.scan, s.start, start, total, lo, hi, grid);
   tc_fence_before_sync();
   __syncthreads();
-  tc_fence_after_sync();
-  pdl_launch_dependents();
-  if (hi > lo) {
-    if (warp < 8) many_rows<D, BF16>(a, s, q_smem, start, lo, total, grid, warp / 4);
-    else if (warp < 12) many_convert<D, BF16>(a, s, k16, v16, start);
-    else if (warp == 12) many_products<D, BF16>(a, s, smem_u32(q_smem), smem_u32(k16), smem_u32(v16), start);
-    else many_lookup<D>(a, s, start);
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(s.tmem, 512);
+  if (warp == 12) tmem_dealloc(s.tmem, 512);
 }
 
 // Joins the parts of an item as kv_combine_kernel does: a lane a row, 32 rows a
