@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __
 // of its rows is full, and there are so many rows in all that joining parts of
 // 256 rows does not outweigh its faster tiles. Both forms, 4 to 32 heads of 128
 // dimensions, us (many | kv_attend_kernel): 8 KV heads x 128 rows over 8,192
-// tokens 33.5 | 29.3, 8 x 256 36.1 | 40.2, 8 x 512 45.7 | 65.4; 64 x 128 rows
-// over 4,096 53.6 | 67.9; 1 x 256 over 32,768 42.5 | 28.3, 1 x 512 41 | 39.
+// tokens 33.5 | 29.3, 8 x 256 35.0 | 40.2, 8 x 512 44.1 | 65.4; 64 x 128 rows
+// over 4,096 50.9 | 67.9; 1 x 256 over 32,768 42.5 | 28.3, 1 x 512 41 | 39.
 bool takes_many(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
   return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 2048;
 }

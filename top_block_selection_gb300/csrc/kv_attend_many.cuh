@@ -35,9 +35,9 @@
 // tiles and 128 tokens at D = 128 (fp16), the rest is waiting for
 // probabilities; at D = 64 the instructions of the exponentials. Measured with
 // the join, 32 heads on 8 KV heads, 4,096 queries over 32,768 tokens: fp16
-// 2,161 us, 954 TFLOP/s, bf16 1,870 us, 1,102 TFLOP/s; over their own 4,096
-// tokens 197 and 187 us. 2,048 queries of 64 dimensions over 32,768 tokens,
-// fp16: 915 us, 582 TFLOP/s.
+// 2,127 us, 969 TFLOP/s, bf16 1,835 us, 1,123 TFLOP/s; over their own 4,096
+// tokens 193 and 180 us. 2,048 queries of 64 dimensions over 32,768 tokens,
+// fp16: 889 us, 599 TFLOP/s.
 #pragma once
 
 #include "kv_attend_kernel.cuh"
@@ -349,8 +349,8 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
 // One warp, in a fixed order: units of a row tile and a key tile, the row tiles
 // in turn; a unit's output, then the scores of the unit that gets its place.
 // Whatever the two warpgroups begin with, one then has its products while the
-// other has the exponentials. (A warp for each row tile let both fall into step:
-// 1.9 times as long a tile.)
+// other has the exponentials. (With a warp for each row tile both
+// fell into step: 8,600 cycles a tile instead of 7,700, at that time.)
 template <int D, bool BF16>
 __device__ void many_products(const AttendArgs& a, ManyShared<D>& s, uint32_t q_addr, uint32_t k_addr, uint32_t v_addr,
                               const Start& start) {
