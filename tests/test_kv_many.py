@@ -211,3 +211,20 @@ def test_many_offsets_past_32_bits(tbs):  # noqa: F811
     q = torch.randn((1, 128, 2 * Hkv, D), dtype=torch.float16, device="cuda")
     assert torch.equal(tbs.qsa_kv_attend(q, *far, table, args[5]), tbs.qsa_kv_attend(q, *args))
     assert "kv_attend_many_kernel" in tbs.qsa_arm()
+
+
+@pytest.mark.parametrize("lens,n,Hkv,R,D", [([60] * 40 + [6000] * 6, 1, 4, 4, 64), ([9000] + [3] * 300, 1, 2, 2, 128),
+                                            ([100, 2000] * 20, 3, 2, 5, 64), ([1] * 700 + [129], 1, 1, 8, 64)])
+def test_mixed_lengths(tbs, lens, n, Hkv, R, D):  # noqa: F811
+    """Short and long sequences in one call of few rows: shares that begin or
+    end in the cost of an item, or hold nothing else."""
+    c = kc.make_long_cache(lens, Hkv, 32, D, seed=R)
+    q = kc.ROUND["f16"](np.random.default_rng(n).standard_normal((len(lens), n, Hkv * R, D)))
+    args, _ = on_gpu(c)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
+    out = tbs.qsa_kv_attend(dev(q, "f16"), *args, lse=lse)
+    assert "kv_attend_kernel" in tbs.qsa_arm()
+    assert torch.equal(tbs.qsa_kv_attend(dev(q, "f16"), *args), out)
+    rng = np.random.default_rng(7)
+    at = [(int(rng.integers(len(lens))), int(rng.integers(n)), int(rng.integers(Hkv * R))) for _ in range(80)]
+    check_rows(c, q, out, lse, "f16", at + [(len(lens) - 1, 0, 0), (0, 0, 0)])

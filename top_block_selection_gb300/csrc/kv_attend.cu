@@ -8,6 +8,11 @@ namespace qsa {
 namespace {
 
 constexpr int kCombineRows = 4;  // rows of a CTA, 128 threads each
+// What an item costs beside its tiles, in tiles: a batch of 32 requests of 100
+// tokens and 32 of 16,384 takes 168 us instead of 484 at 0, 256 requests of 64 to
+// 1,000 tokens 50 us instead of 114, 64 requests of 1,000 to 16,384 tokens 175 at
+// both. (At 3 the first two take 165 and 57, at 8 169 and 50.)
+constexpr int kItemCost = 5;
 
 // Joins the parts of the item that CTA blockIdx.x of the attention began and
 // others ended: that CTA's second slot and the first slots of the CTAs after
@@ -120,12 +125,13 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / a.R));
   a.n_qt = (p.n + a.qt - 1) / a.qt;
   a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
-  a.item_cost = many ? kManyItemCost : 0;
   const int rt = rows_form(a.qt * a.R);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
   const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
   const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * p.cache.Hkv * item_tiles;
   const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sm_count, kKvMaxCtas), most));
+  // (No item costs more than another where a CTA has a tile or two.)
+  a.item_cost = many ? kManyItemCost : p.ids || most <= 2 * grid ? 0 : kItemCost;
   a.jobs = static_cast<int32_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
 

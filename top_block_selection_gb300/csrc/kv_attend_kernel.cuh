@@ -398,16 +398,24 @@ struct AttendShared {
   uint32_t stop;
 };
 
+// Past what is left of an item's cost, which lies in front of its tiles (t < 0).
+__device__ __forceinline__ void skip_cost(Walk& w) {
+  if (w.t >= 0) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(-w.t), w.left));
+  w.t += n;
+  w.left -= n;
+}
 // Advances the walk past `part` tiles of an item of `tiles`.
-__device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads) {
+__device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads, int cost) {
   w.left -= part;
   w.t += part;
   if (w.t >= tiles) {
-    w.t = 0;
+    w.t = -cost;
     if (++w.h == heads) {
       w.h = 0;
       ++w.e;
     }
+    skip_cost(w);
   }
 }
 
@@ -500,7 +508,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
     }
     if (bad && (a.ids || lane == 0)) atomicOr(a.status, kErrCacheIndex);
     g0 += part;
-    step(w, part, en.tiles, a.c.Hkv);
+    step(w, part, en.tiles, a.c.Hkv, a.item_cost);
   }
   if (!ok) {  // let the copies in flight land before the CTA gives its memory back
     const uint32_t n = min(last, static_cast<uint32_t>(C::kStages / W));
@@ -648,8 +656,8 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_full[buf]);
     }
-    at += w.t + part;
-    step(w, part, en.tiles, a.c.Hkv);
+    at += w.t + part + a.item_cost;
+    step(w, part, en.tiles, a.c.Hkv, a.item_cost);
   }
 }
 
@@ -1057,7 +1065,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 
 // This CTA's share of all tiles, [total c / grid, total (c + 1) / grid), and
 // the item that its first tile belongs to. An item counts item_cost tiles more
-// than it has, in front of them. Every item of a list has the same
+// than it has, in front of them; lo is given as the first tile's place. Every item of a list has the same
 // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
 // to the calling threads: kThreads of them, whole warps from kFirst on (by way
 // of scan and shared, in shared memory, and barrier kBarrier).
@@ -1154,6 +1162,8 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     start = shared;
     start.walk.left = hi - lo;
   }
+  skip_cost(start.walk);
+  lo = hi - start.walk.left;
 }
 
 // -------------------------------------------------------------- the kernel

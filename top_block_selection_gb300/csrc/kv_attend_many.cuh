@@ -128,30 +128,21 @@ struct ManyItem {
   int64_t at;
 };
 // f(entry, item) for each of the CTA's items, in the same order in every warp.
-// The walk's t is negative in an item's cost, which has no tiles.
 template <class F>
 __device__ __forceinline__ void many_items(const AttendArgs& a, const Start& start, int64_t lo, F&& f) {
   Walk w = start.walk;
   Entry en = start.entry;
   int en_of = w.e;
+  int64_t at = lo - w.t;
   while (w.left > 0) {
     if (en_of != w.e) {
       en = entry_of(a, w.e);
       en_of = w.e;
     }
-    const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
-    const int t = max(w.t, 0), tiles = w.t + part - t;
-    if (tiles > 0) f(en, ManyItem{w.e, w.h, t, tiles, lo - w.t});
-    lo += part;
-    w.left -= part;
-    w.t += part;
-    if (w.t >= en.tiles) {
-      w.t = -a.item_cost;
-      if (++w.h == a.c.Hkv) {
-        w.h = 0;
-        ++w.e;
-      }
-    }
+    const int tiles = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
+    f(en, ManyItem{w.e, w.h, w.t, tiles, at});
+    at += en.tiles + a.item_cost;
+    step(w, tiles, en.tiles, a.c.Hkv, a.item_cost);
   }
 }
 // Until the CTA's share is known and the accumulators' memory is there.
