@@ -157,7 +157,8 @@ __device__ __forceinline__ void many_begin(S& s) {
 
 // Whether row tile w has rows to work on. With three places for scores both row
 // tiles always work (on zeros, if need be): a place's barrier is then waited for
-// by the two in turn, each after the other's unit, and none runs ahead of it.
+// by the two in turn, each after the other's unit, and none runs ahead of it. (The
+// outputs' barriers are each row tile's own; see the wait at an item's last tile.)
 template <int D>
 __device__ __forceinline__ bool many_active(const AttendArgs& a, const Entry& en, int w) {
   return many_buffers(D) > 2 || en.nq > w * (a.qt / 2);
@@ -662,6 +663,12 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
             many_probabilities<BF16, false>(tm_s + c * 32, f0, f1, v0, v1, m, 0, 0, zero, l);
           }
         }
+        // With three places for scores, a warp that has its last tile's scores only
+        // knows that the output two tiles back is done: these came after another
+        // row tile's. The last tile's output may only be asked for by its parity
+        // when the one before it is done, so that one is waited for here: ahead
+        // of this warp's arrival, without which the last one cannot be done yet.
+        if (kBuffers > 2 && i > 0 && i + 1 == part) wait_or_stop(&s.o_full[w], (n - 1) & 1, &s.stop, a.status);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
