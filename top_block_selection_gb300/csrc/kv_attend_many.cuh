@@ -174,6 +174,7 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
   many_items(a, start, 0, [&](const Entry& en, const ManyItem& w) {
     const int part = w.tiles;
     const int32_t* const table = a.c.page_table + static_cast<int64_t>(en.b) * a.c.max_blocks;
+    if (en.last_pos >= a.c.max_blocks * a.c.block) bad = true;  // longer than its page table
     for (int t = 0; t < part; ++t, ++g) {
       const int blk = (w.t + t) * a.spt + i * 16 / a.c.block;
       int page = -1;
