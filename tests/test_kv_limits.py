@@ -37,3 +37,20 @@ def test_longer_than_the_page_table(tbs, D, dtype, n, Hq):  # noqa: F811
     args[5].fill_(320)
     tbs.qsa_kv_attend(dev(q, dtype), *args)
     assert tbs.qsa_device_status(clear=True) == (0, 0)
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("n,Hq", [(1, 4), (128, 16)])
+def test_pages_outside_in_any_place_of_a_tile(tbs, block, n, Hq):  # noqa: F811
+    """One page id outside the cache, at each of the blocks in turn."""
+    blocks = 256 // block + 2
+    c = kc.make_cache([blocks * block - 3], 1, block, 64, seed=block)
+    args, _ = on_gpu(c)
+    q = kc.as_f16(np.random.default_rng(2).standard_normal((1, n, Hq, 64)))
+    for i in range(blocks):
+        table = args[4].clone()
+        table[0, i] = -1 if i % 2 else c["k"].shape[0]
+        got = tbs.qsa_kv_attend(dev(q, "f16"), *args[:4], table, args[5])
+        assert tbs.qsa_device_status(clear=True) == (1, 32), i
+        if n == 1 or i in (0, 1, blocks - 1):
+            close(got, c, q, "f16", [[[[k for k in range(blocks) if k != i]] * n]])

@@ -506,7 +506,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         if (lane == 0) mbar_arrive(&s.full[st]);
       }
     }
-    if (bad && (a.ids || lane == 0)) atomicOr(a.status, kErrCacheIndex);
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, kErrCacheIndex);
     g0 += part;
     step(w, part, en.tiles, a.c.Hkv, a.item_cost);
   }
