@@ -1,0 +1,107 @@
+"""GPU tests of what the cache attention holds in fewer bits than fp32: its
+probabilities and queries (sums of 8-bit terms where there are few rows, 16-bit
+ones where there are many). Errors may not grow with the context, nor with the
+scales and dimensions that carry no weight.
+
+Tolerances come from the contract (include/qsa.h): a probability times its
+value scale is off by at most U of itself or F of the largest among the RUN
+tokens around it, U = 2^-12, F = 2^-22, RUN = 1,024 of fp16 calls and 2^-9,
+2^-19, 512 of bf16 calls."""
+import numpy as np
+import pytest
+
+import kv_cases as kc
+from oracle import kv_oracle as ko
+from test_kv_parity import UNIT, dev, on_gpu, tbs  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = {"f16": 2.0 ** -12, "bf16": 2.0 ** -9}
+F = {"f16": 2.0 ** -22, "bf16": 2.0 ** -19}
+RUN = {"f16": 1024, "bf16": 512}
+
+
+def one_head(B, k, v, ks, vs, block, seed=0):
+    """B sequences in the same pages (one KV head) of code values k, v
+    [tokens, D] and block scales ks, vs."""
+    tokens, D = k.shape
+    pages = -(-tokens // block)
+    order = np.random.default_rng(seed).permutation(pages).astype(np.int32)
+    c = dict(table=np.broadcast_to(order, (B, pages)).copy(), lens=np.full(B, tokens, np.int32), n_new=None)
+    for name, x, s in (("k", k, ks), ("v", v, vs)):
+        full = np.full((pages * block, D), 0x7F, np.uint8)
+        full[:tokens] = ko.encode(x)
+        c[name] = np.empty((pages, 1, block, D), np.uint8)
+        c[name][order, 0] = full.reshape(pages, block, D)
+        c[name + "_scale"] = np.empty((pages, 1), np.float32)
+        c[name + "_scale"][order, 0] = s
+    return c
+
+
+def rounded(x, dtype):
+    return x.astype(np.float16).astype(np.float64) if dtype == "f16" else kc.as_bf16(x.astype(np.float32)).astype(np.float64)
+
+
+def expected(c, q, b, j, n, scale, dtype):
+    """(result, rms error of each of its elements before its rounding) of a row:
+    each probability off by a uniform error of its bound, the scores' fp32 sums
+    and exp2 by 2^-20 (1 + |x|) of it."""
+    seen = ko.seen_tokens(c, b, j, n)
+    page, off = np.array([t[0] for t in seen]), np.array([t[1] for t in seen])
+    kk = ko.decode(c["k"][page, 0, off]) * c["k_scale"][page, 0].astype(np.float64)[:, None]
+    code, vs = ko.decode(c["v"][page, 0, off]), c["v_scale"][page, 0].astype(np.float64)
+    x = scale * (kk @ q.astype(np.float64))
+    p = np.exp(x - x.max())
+    w = p * vs
+    d = np.maximum(U[dtype] * w, F[dtype] * w.max()) + 2.0 ** -20 * (1 + np.abs(x - x.max())) * w
+    return (w @ code) / p.sum(), np.sqrt((d * d / 3) @ (code * code)) / p.sum()
+
+
+def check_norm(tbs, c, q, dtype, rows, scale, kernel):  # noqa: F811
+    """The error's norm over these rows is that of the bounds' uniform errors and
+    of the result's rounding, give or take a quarter."""
+    args, _ = on_gpu(c)
+    got = tbs.qsa_kv_attend(dev(q, dtype), *args, scale=scale)
+    assert kernel + " " in tbs.qsa_arm() + " "
+    got = got.double().cpu().numpy()
+    err = room = 0.0
+    for b, j, h in rows:
+        want, rms = expected(c, q[b, j, h], b, j, q.shape[1], scale, dtype)
+        err += ((got[b, j, h] - want) ** 2).sum()
+        room += (rms ** 2).sum() + ((rounded(want, dtype) - want) ** 2).sum()
+    assert np.sqrt(err) <= 1.25 * np.sqrt(room), (np.sqrt(err), np.sqrt(room))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_errors_do_not_grow_with_the_context(tbs, dtype):  # noqa: F811
+    """49,152 tokens for each CTA, scores of standard deviation 0.4 to 3 by block."""
+    rng = np.random.default_rng(1)
+    tokens, D, block = 49152, 64, 128
+    pages = tokens // block
+    ks, vs = 2.0 ** rng.integers(-8, -4, pages), 2.0 ** rng.integers(-8, -5, pages)
+    c = one_head(152, rng.standard_normal((tokens, D)) * 100, rng.standard_normal((tokens, D)) * 100, ks, vs, block)
+    q = kc.ROUND[dtype](rng.standard_normal((152, 1, 4, D)))
+    rows = [(int(b), 0, int(h)) for b, h in zip(rng.integers(152, size=24), rng.integers(4, size=24))]
+    check_norm(tbs, c, q, dtype, rows, D ** -0.5, "kv_attend_kernel")
+
+
+@pytest.mark.parametrize("n,R", [(1, 4), (1, 16), (1, 32)])
+@pytest.mark.parametrize("dtype,bits", [("f16", 18.2), ("bf16", 15.2)])
+def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
+    """One token whose score is `bits` (in log2) above those of 49,151 equal ones,
+    which together still carry some weight: value -1 against 1."""
+    tokens, D, block = 49152, 64, 128
+    k, v = np.zeros((tokens, D)), np.ones((tokens, D))
+    k[5, 0], v[5] = 1.0, -1.0
+    c = one_head(152, k, v, np.ones(tokens // block), np.ones(tokens // block), block)
+    q = np.zeros((152, n, R, D))
+    q[..., 0] = 1.0
+    scale = bits * np.log(2.0)
+    args, _ = on_gpu(c)
+    got = tbs.qsa_kv_attend(dev(q, dtype), *args, scale=scale).double().cpu().numpy()
+    rest = (tokens - n + np.arange(n)) * 2.0 ** -bits  # the weight of the others, for each row
+    want = ((rest - 1) / (rest + 1))[None, :, None, None]
+    tol = U[dtype] + RUN[dtype] * F[dtype] + UNIT[dtype] + 2.0 ** -16
+    assert np.abs(got - want).max() <= tol, (float(np.abs(got - want).max()), tol)

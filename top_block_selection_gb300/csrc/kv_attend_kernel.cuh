@@ -18,12 +18,10 @@
 //                  row's largest, the rest to 2^-19 of that;
 //   probabilities  T = 3: cut, cut and rounded, to 2^-12 of each; T = 2:
 //                  rounded twice, to 2^-9: a fraction of the rounding of the
-//                  result (2^-11 and 2^-8 at most). With T = 3 the second and
-//                  third term are scaled by 8 and 128 so that a small
-//                  probability does not end in e4m3's subnormals: it is off
-//                  by 2^-17 of the row's largest at most (T = 2: 2^-14). A sum
-//                  over 131,073 tokens of like weight is then as exact as one
-//                  over 1,000 (unscaled: 2.5 times the error of rounding alone).
+//                  result (2^-11 and 2^-8 at most). The later terms are scaled
+//                  up (T = 3 by 8 and 128, T = 2 by 16) and take what the one
+//                  before leaves, its smallest step included. A probability is
+//                  then lost only below 2^-22 of the largest (T = 2: 2^-19).
 // The terms are groups of columns of one product, added in fp32 after it.
 // With few rows a tile's product is bound by reading the M operand from
 // shared memory, so the extra columns cost little.
@@ -688,9 +686,9 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
-// The columns of RT rows at `taddr`, their T terms added (kScaled: the later
-// two of three by 1/8 and 1/128), a few rows at a time (the terms of all would
-// not fit in registers beside the softmax state).
+// The columns of RT rows at `taddr`, their T terms added (kScaled: the later ones
+// by 1/8 and 1/128 of three, by 1/16 of two), a few rows at a time (the terms of
+// all would not fit in registers beside the softmax state).
 template <class C, bool kScaled>
 __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
   constexpr int kPart = C::RT <= 8 ? C::RT : C::RT / 2;
@@ -704,9 +702,10 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
 #pragma unroll
     for (int r = 0; r < kPart; r += 2) {
       F2 sum = f2(t1[r], t1[r + 1]);
-      if (kScaled && C::T == 3) {
-        sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
-        sum = fma2(sum, f2(0.125f, 0.125f), f2(t0[r], t0[r + 1]));
+      if (kScaled) {
+        constexpr float down = C::T == 3 ? 0.125f : 0.0625f;
+        if (C::T == 3) sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
+        sum = fma2(sum, f2(down, down), f2(t0[r], t0[r + 1]));
       } else {
         if (C::T == 3) sum = sum + f2(t2[r], t2[r + 1]);
         sum = sum + f2(t0[r], t0[r + 1]);
@@ -907,24 +906,18 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         for (int term = 0; term < C::T; ++term) {
           f2_get(y, p0, p1);
           uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-          if (term < C::T - 1) {  // 4 significant bits: cut (T = 3) or rounded half up (T = 2)
+          if (term < C::T - 1) {
+            // 4 significant bits: cut (T = 3) or rounded half up (T = 2), and to
+            // e4m3's smallest step (24576 has steps of 2^-9), so that what the
+            // code leaves goes to the next term, whole.
             b0 = (b0 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
             b1 = (b1 + (C::T == 2 ? 0x80000u : 0u)) & 0xFFF00000u;
-            F2 cut = f2(__uint_as_float(b0), __uint_as_float(b1));
-            if (C::T == 3) {
-              // The first term to e4m3's smallest step too (24576 has steps of
-              // 2^-9), so that what it leaves is all that it leaves.
-              if (term == 0) {
-                cut = cut + f2(24576.0f, 24576.0f) + f2(-24576.0f, -24576.0f);
-                f2_get(cut, p0, p1);
-                b0 = __float_as_uint(p0);
-                b1 = __float_as_uint(p1);
-              }
-              const float up = term == 0 ? 8.0f : 16.0f;
-              y = fma2(cut, f2(-up, -up), y * f2(up, up));
-            } else {
-              y = fma2(cut, f2(-1.0f, -1.0f), y);
-            }
+            const F2 cut = f2(__uint_as_float(b0), __uint_as_float(b1)) + f2(24576.0f, 24576.0f) + f2(-24576.0f, -24576.0f);
+            f2_get(cut, p0, p1);
+            b0 = __float_as_uint(p0);
+            b1 = __float_as_uint(p1);
+            const float up = C::T == 3 && term == 0 ? 8.0f : 16.0f;
+            y = fma2(cut, f2(-up, -up), y * f2(up, up));
           }
           const uint32_t pair = e4m3x2(__uint_as_float(b0), __uint_as_float(b1));
           const int col = term * RT + r;
