@@ -105,3 +105,21 @@ def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
     want = ((rest - 1) / (rest + 1))[None, :, None, None]
     tol = U[dtype] + RUN[dtype] * F[dtype] + UNIT[dtype] + 2.0 ** -16
     assert np.abs(got - want).max() <= tol, (float(np.abs(got - want).max()), tol)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n,R", [(64, 1, 4), (128, 1, 16), (128, 64, 32)])
+def test_query_dimension_far_above_the_others(tbs, dtype, D, n, R):  # noqa: F811
+    """One dimension of the queries 512 times the others, where the keys are
+    zero: the scores are those of the other dimensions."""
+    rng = np.random.default_rng(n)
+    tokens, block = 1500, 64
+    pages = -(-tokens // block)
+    k, v = rng.standard_normal((tokens, D)) * 4, rng.standard_normal((tokens, D)) * 100
+    k[:, 3] = 0.0
+    c = one_head(1, k, v, np.full(pages, 0.25), np.full(pages, 2.0 ** -6), block)
+    q = rng.standard_normal((1, n, R, D)) * 4
+    q[..., 3] = 512 * 4
+    q = kc.ROUND[dtype](q)
+    rows = [(0, int(j), int(h)) for j, h in zip(rng.integers(n, size=40), rng.integers(R, size=40))]
+    check_norm(tbs, c, q, dtype, rows, D ** -0.5, "kv_attend_kernel" if n == 1 else "kv_attend_many_kernel")

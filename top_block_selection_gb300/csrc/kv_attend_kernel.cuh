@@ -13,9 +13,9 @@
 // TMA and never touched by a thread. The other operand is made e4m3 without
 // losing its bits, as a sum of T terms of 4 significant bits, T = 3 for fp16
 // and 2 for bf16 calls:
-//   queries        y1 = e4m3(y), y2 = e4m3(y - y1), y3 = ...: exact for every
-//                  fp16 (T = 3) or bf16 (T = 2) element above 2^-18 of its
-//                  row's largest, the rest to 2^-19 of that;
+//   queries        y1 = e4m3(y), y2 = e4m3(16 (y - y1)), y3 = ...: exact for every
+//                  fp16 (T = 3) or bf16 (T = 2) element above 2^-13 of its
+//                  row's largest, the rest to 2^-25 (T = 2: 2^-21) of that;
 //   probabilities  T = 3: cut, cut and rounded, to 2^-12 of each; T = 2:
 //                  rounded twice, to 2^-9: a fraction of the rounding of the
 //                  result (2^-11 and 2^-8 at most). The later terms are scaled
@@ -582,8 +582,8 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
       for (int e = 0; e < kPer / 2; ++e) {
         code[e] = e4m3x2(x[2 * e], x[2 * e + 1]);
         const float2 back = e4m3x2_to_float2(code[e]);
-        x[2 * e] -= back.x;
-        x[2 * e + 1] -= back.y;
+        x[2 * e] = 16.0f * (x[2 * e] - back.x);  // at most half a step of the code: no more than 16
+        x[2 * e + 1] = 16.0f * (x[2 * e + 1] - back.y);
       }
       uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
       if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
@@ -686,10 +686,10 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
-// The columns of RT rows at `taddr`, their T terms added (kScaled: the later ones
-// by 1/8 and 1/128 of three, by 1/16 of two), a few rows at a time (the terms of
-// all would not fit in registers beside the softmax state).
-template <class C, bool kScaled>
+// The columns of RT rows at `taddr`, their T terms added, each 1/16 of the one
+// before it (of three terms of a probability, the second 1/8), a few rows at a
+// time (the terms of all would not fit in registers beside the softmax state).
+template <class C, bool kProbs>
 __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
   constexpr int kPart = C::RT <= 8 ? C::RT : C::RT / 2;
 #pragma unroll
@@ -701,15 +701,10 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
     tmem_ld_wait();
 #pragma unroll
     for (int r = 0; r < kPart; r += 2) {
+      constexpr float down = kProbs && C::T == 3 ? 0.125f : 0.0625f;
       F2 sum = f2(t1[r], t1[r + 1]);
-      if (kScaled) {
-        constexpr float down = C::T == 3 ? 0.125f : 0.0625f;
-        if (C::T == 3) sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
-        sum = fma2(sum, f2(down, down), f2(t0[r], t0[r + 1]));
-      } else {
-        if (C::T == 3) sum = sum + f2(t2[r], t2[r + 1]);
-        sum = sum + f2(t0[r], t0[r + 1]);
-      }
+      if (C::T == 3) sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
+      sum = fma2(sum, f2(down, down), f2(t0[r], t0[r + 1]));
       f2_get(sum, x[r0 + r], x[r0 + r + 1]);
     }
   }
