@@ -88,7 +88,7 @@ def test_errors_do_not_grow_with_the_context(tbs, dtype):  # noqa: F811
 
 
 @pytest.mark.parametrize("n,R", [(1, 4), (1, 16), (1, 32)])
-@pytest.mark.parametrize("dtype,bits", [("f16", 18.2), ("bf16", 15.2)])
+@pytest.mark.parametrize("dtype,bits", [("f16", 18.2), ("f16", 22.5), ("bf16", 15.2), ("bf16", 19.5)])
 def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
     """One token whose score is `bits` (in log2) above those of 49,151 equal ones,
     which together still carry some weight: value -1 against 1."""
@@ -107,6 +107,29 @@ def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
     assert np.abs(got - want).max() <= tol, (float(np.abs(got - want).max()), tol)
 
 
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n,R,far", [(128, 1, 4, 14), (64, 1, 32, 14)])
+def test_large_value_scale_without_weight(tbs, D, dtype, n, R, far, at):  # noqa: F811
+    """A block whose values are 2^far times the others' and whose scores lie 60
+    (in log2) below them changes nothing, whether a row sees it or not."""
+    rng = np.random.default_rng(D + n)
+    tokens, block = 2000, 64
+    pages = -(-tokens // block)
+    k, v = rng.standard_normal((tokens, D)), rng.standard_normal((tokens, D)) * 100
+    i = {"first": 0, "middle": pages // 2, "last": pages - 1}[at]
+    k[:, 0] = 0.0
+    k[i * block:(i + 1) * block, 0] = -15.0
+    vs = np.full(pages, 2.0 ** -12)
+    vs[i] = 2.0 ** (far - 12)
+    c = one_head(1, k, v, np.ones(pages), vs, block)
+    q = rng.standard_normal((1, n, R, D)) * D ** -0.5
+    q[..., 0] = 60 * np.log(2.0) / 15
+    q = kc.ROUND[dtype](q)
+    rows = [(0, int(j), int(h)) for j, h in zip(rng.integers(n, size=40), rng.integers(R, size=40))]
+    check_norm(tbs, c, q, dtype, rows, 1.0, "kv_attend_kernel" if n == 1 else "kv_attend_many_kernel")
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("D,n,R", [(64, 1, 4), (128, 1, 16), (128, 64, 32)])
 def test_query_dimension_far_above_the_others(tbs, dtype, D, n, R):  # noqa: F811
@@ -123,3 +146,31 @@ def test_query_dimension_far_above_the_others(tbs, dtype, D, n, R):  # noqa: F81
     q = kc.ROUND[dtype](q)
     rows = [(0, int(j), int(h)) for j, h in zip(rng.integers(n, size=40), rng.integers(R, size=40))]
     check_norm(tbs, c, q, dtype, rows, D ** -0.5, "kv_attend_kernel" if n == 1 else "kv_attend_many_kernel")
+
+
+@pytest.mark.parametrize("kind", ["zeros first", "zeros far above 30", "zeros far above 45", "rising", "falling"])
+@pytest.mark.parametrize("D,n,R", [(128, 1, 4), (64, 1, 32)])
+def test_weights_far_apart(tbs, D, n, R, kind):  # noqa: F811
+    """Blocks of zeros (the smallest scale there is) before all others, or 30
+    and 45 (in log2) above all others in the score; value scales that rise or
+    fall by 2^3 from block to block."""
+    rng = np.random.default_rng(D + n)
+    tokens, block = 2000, 64
+    pages = -(-tokens // block)
+    k, v = rng.standard_normal((tokens, D)), rng.standard_normal((tokens, D)) * 100
+    k[:, 0] = 0.0
+    vs = np.full(pages, 2.0 ** -6)
+    if kind.startswith("zeros"):
+        i = 0 if kind == "zeros first" else 3
+        v[i * block:(i + 1) * block] = 0.0
+        vs[i] = 2.0 ** -100
+        if i:
+            k[i * block:(i + 1) * block, 0] = 15.0
+    else:
+        vs = 2.0 ** (3.0 * np.arange(pages) - 40)[::1 if kind == "rising" else -1]
+    c = one_head(1, k, v, np.ones(pages), vs, block)
+    q = rng.standard_normal((1, n, R, D)) * D ** -0.5
+    q[..., 0] = (45 if kind.endswith("45") else 30) * np.log(2.0) / 15
+    q = kc.ROUND["bf16"](q)
+    rows = [(0, int(j), int(h)) for j, h in zip(rng.integers(n, size=40), rng.integers(R, size=40))]
+    check_norm(tbs, c, q, "bf16", rows, 1.0, "kv_attend_kernel" if n == 1 else "kv_attend_many_kernel")

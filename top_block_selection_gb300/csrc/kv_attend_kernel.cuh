@@ -27,12 +27,16 @@
 // shared memory, so the extra columns cost little.
 //
 // The softmax reference m_r is not each tile's maximum but one that lags: it
-// is set above the largest score (by two in log2), and a tile keeps it as long
-// as its codes still fit below 448. Most tiles thus need one vote of the
-// warpgroup instead of a maximum over its tokens for each row, and the output
-// stays in TMEM, accumulated by the product itself, until a reference moves
-// or the item ends. The value scales ride on the probabilities, relative to
-// the largest at the last move.
+// is set above the largest weight, score plus logarithm of the value scale (by
+// two in log2), and a tile keeps it as long as its codes still fit below 448.
+// Most tiles thus need one vote of the warpgroup instead of a maximum over its
+// tokens for each row, and the output stays in TMEM, accumulated by the product
+// itself, until a reference moves or the item ends. Every 8th tile (T = 2: 4th)
+// of a warpgroup since is looked at for each row, and a reference more than
+// five above its largest weight goes down: codes have steps, and behind one
+// token far above all others (the first of a context often is) every later
+// one would be lost below them, however much they are together. The value
+// scales ride on the probabilities, relative to the largest at the last move.
 //
 // What bounds it: decoding reads every code once from HBM (about 23 bytes a
 // cycle and SM); over chosen blocks of many queries the codes come from L2.
@@ -359,6 +363,9 @@ struct AttendCfg {
   static constexpr int kPRegion = W * kPBytes > kJoinBytes ? W * kPBytes : kJoinBytes;
   static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
   static_assert(2 * N * W <= 512, "TMEM");
+  // Tiles of a warpgroup after which it looks whether its references stand too
+  // high for the tokens that come now.
+  static constexpr int kRun = T == 3 ? 8 : 4;
 };
 
 struct StageMeta {
@@ -384,6 +391,8 @@ struct AttendShared {
   ItemInfo<C::RT> item[2];
   StageMeta meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
+  alignas(16) float spread[C::W][4];         // per-warp: the largest value scale over its tokens' smallest (log2)
+  alignas(16) float moved[C::W][C::RT], alpha[C::W][C::RT];  // references, factors of what was summed (all warps write the same)
   alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
   float mx[C::RT], sum[C::RT], inv[C::RT];  // joined, 1 / sum
   alignas(16) int32_t poison[128];  // first position whose value code is NaN, per dimension
@@ -717,6 +726,12 @@ constexpr float kUnset = -3e38f;     // a reference that no score has set yet
 constexpr float kMargin = 2.0f;
 constexpr float kProbScale = 128.0f; // code of a probability 1 at the largest value scale
 constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
+// How far (log2) below the largest value scale a token's counts where references
+// are set, and a reference may go below the largest score: sums of 2^30 tokens
+// then stay in fp32's range.
+constexpr float kRange = 40.0f;
+constexpr float kSlack = 3.0f;        // log2 that a reference may stand too high
+constexpr float kFine = 16777216.0f;  // a sum beyond this goes into the reference
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
@@ -789,7 +804,10 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       l[r] = 0.0f;
       m[r] = kUnset;
     }
-    float vref = 0.0f, inv_vref = 0.0f;  // largest value scale so far, kProbScale / it
+    float vref = 0.0f, inv_vref = 0.0f;  // largest value scale when references were last set, kProbScale / it
+    float mine = kUnset;                 // reference of row `lane`
+    float peak = kNegInf;                // of row `lane`: no score was higher where references were set
+    int rest = C::kRun;                  // tiles until the references are looked at
     bool pending = false;                // a product runs that was not waited for
     bool held = false;                   // TMEM holds output not yet in o[]
     bool issued = false;                 // this tile's scores are under way
@@ -806,9 +824,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       tc_fence_after_sync();
       float x[RT];
       tmem_rows<C, true>(tm_o + lane_addr, x);
-      const float f = vref * (1.0f / kProbScale);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) o[r] += x[r] * f;
+      for (int r = 0; r < RT; ++r) o[r] += x[r];
     };
 
     for (int i = (W - g0 % W + wg) % W; i < tiles; i += W) {
@@ -855,32 +872,61 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 #pragma unroll
       for (int r = 0; r < RT; ++r) top = fmaxf(top, e[r]);
       float v_mul = v_scale * inv_vref;
-      if (bar_any(1 + wg, 128, top + log2_approx(v_mul) > kMaxCode || (vref == 0.0f && v_scale > 0.0f))) {
-        // Move the references above the largest scores and value scales so far.
+      const bool due = --rest == 0;
+      if (bar_any(1 + wg, 128, due || top + fmaxf(log2_approx(v_mul), 7.0f - kRange) > kMaxCode ||
+                                   (vref == 0.0f && v_scale > 0.0f))) {
+        // Each row's largest weight in this tile: a score plus its value scale's
+        // logarithm. (Scores alone where they may pass 2^24, products of two
+        // codes being below 2^17.7: they have no steps below 1 then.)
         scores(false);
+        const float vnow = fmaxf(vref, meta.vmax);
+        const float mul = warp_max(lane < RT ? fabsf(info.row_mul[lane]) : 0.0f) * k_mul;
+        const float lv = mul < 0.5f ? fmaxf(log2_approx(v_scale) - log2_approx(vnow), -kRange) : 0.0f;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float v = warp_max(e[r]);
+          const float v = warp_max(e[r] + lv);
           if (lane == r) top = v;
         }
+        const float spread = warp_max(v_scale > 0.0f ? -lv : 0.0f);
         if (lane < RT) s.red[wg][lane][warp] = top;
-        settle();
-        flush();
+        if (lane == 0) s.spread[wg][warp] = spread;
         tc_fence_before_sync();
         bar_sync(1 + wg, 128);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float4 v = *reinterpret_cast<const float4*>(s.red[wg][r]);
-          const float mn = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) + kMargin);
-          const float alpha = exp2_approx(m[r] - mn);
-          m[r] = mn;
-          l[r] *= alpha;
-          o[r] *= alpha;
-          e[r] -= mn;
+        // Lane r of every warp finds row r's reference.
+        float to = mine;
+        if (lane < RT) {
+          const float4 v = *reinterpret_cast<const float4*>(s.red[wg][lane]);
+          const float4 k = *reinterpret_cast<const float4*>(s.spread[wg]);
+          const float here = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+          peak = fmaxf(peak, here + fmaxf(fmaxf(k.x, k.y), fmaxf(k.z, k.w)));
+          const float want = fmaxf(here + kMargin, peak - kRange);
+          if (here != kNegInf && (want > mine || want < mine - kSlack)) to = want;
         }
-        vref = fmaxf(vref, meta.vmax);
-        inv_vref = vref > 0.0f ? __fdividef(kProbScale, vref) : 0.0f;
-        v_mul = v_scale * inv_vref;
+        if (__any_sync(0xFFFFFFFFu, to != mine) || vnow != vref) {
+          settle();
+          flush();
+          const float less = vref > 0.0f ? __fdividef(vref, vnow) : 1.0f;
+          if (lane < RT) {
+            s.moved[wg][lane] = to;
+            s.alpha[wg][lane] = exp2_approx(mine - to);
+          }
+          mine = to;
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < RT; r += 4) {
+            const float4 mn = *reinterpret_cast<const float4*>(&s.moved[wg][r]);
+            const float4 f = *reinterpret_cast<const float4*>(&s.alpha[wg][r]);
+            m[r] = mn.x, m[r + 1] = mn.y, m[r + 2] = mn.z, m[r + 3] = mn.w;
+            l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+            o[r] *= f.x * less, o[r + 1] *= f.y * less, o[r + 2] *= f.z * less, o[r + 3] *= f.w * less;
+          }
+          vref = vnow;
+          inv_vref = vref > 0.0f ? __fdividef(kProbScale, vref) : 0.0f;
+          v_mul = v_scale * inv_vref;
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) e[r] -= m[r];
+        rest = C::kRun;
       }
       // The scores have been read: the next tile's may overwrite them.
       issued = false;
@@ -971,25 +1017,28 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         if (RT * d < 32) l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], d);
       }
       if (lane % (32 / RT) == 0) s.red[wg][lane / (32 / RT)][warp] = l[0];
-      if (t == 0) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) s.ml[0][wg][r] = m[r];
-      }
+      if (t < RT) s.ml[0][wg][t] = mine;
     }
     bar_sync(8, kAll);
-    // Then the common reference, and each warpgroup's weight against it.
+    // Then the common reference, and each warpgroup's weight against it. (A sum
+    // that is large because the reference went down goes into the reference.)
     if (t < RT) {
-      float mx = s.ml[0][0][t];
+      float mx = s.ml[0][0][t], sum;
 #pragma unroll
       for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][t]);
-      s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
-      if (wg == 0) {
-        float sum = 0.0f;
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float4 v = *reinterpret_cast<const float4*>(s.red[w][t]);
           sum += ((v.x + v.y) + (v.z + v.w)) * exp2_approx(s.ml[0][w][t] - mx);
         }
+        if (again || !(sum > kFine)) break;
+        mx += floorf(log2_approx(sum));
+      }
+      s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
+      if (wg == 0) {
         s.mx[t] = mx;
         s.sum[t] = sum;
         s.inv[t] = __fdividef(1.0f, sum);
@@ -1004,7 +1053,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       if (t < D) {
 #pragma unroll
         for (int r = 0; r < C::kJoinRows; ++r)
-          join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r];
+          join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r] * (vref * (1.0f / kProbScale));
       }
       bar_sync(8, kAll);
       // Four dimensions of a row a thread.
