@@ -87,7 +87,7 @@ def test_errors_do_not_grow_with_the_context(tbs, dtype):  # noqa: F811
     check_norm(tbs, c, q, dtype, rows, D ** -0.5, "kv_attend_kernel")
 
 
-@pytest.mark.parametrize("n,R", [(1, 4), (1, 16), (1, 32)])
+@pytest.mark.parametrize("n,R", [(1, 4), (1, 16), (1, 32), (64, 2)])
 @pytest.mark.parametrize("dtype,bits", [("f16", 18.2), ("f16", 22.5), ("bf16", 15.2), ("bf16", 19.5)])
 def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
     """One token whose score is `bits` (in log2) above those of 49,151 equal ones,

@@ -651,6 +651,9 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
         const bool huge = __any_sync(0xFFFFFFFFu, m > 1048576.0f || (m < -1048576.0f && m != kUnset));
         const float inv = vref > 0.0f ? __fdividef(kManyScale, vref) : 0.0f;
         float2 vs = *reinterpret_cast<const float2*>(&meta.vs[0]);
+        // A tile's sum apart: added one by one to a sum that one token above all
+        // others made large, the small ones would lose bits each.
+        F2 lt = f2(0.0f, 0.0f);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           const float f0 = mul * ks.x, f1 = mul * ks.y, v0 = vs.x * inv, v1 = vs.y * inv;
@@ -659,11 +662,12 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
           if (masked || huge) {
             const int limit = row_pos - pos0 - c * 32;
             many_probabilities<BF16, true>(tm_s + c * 32, f0, f1, v0, v1, m, (holes >> (2 * c)) & 1 ? -1 : limit,
-                                           (holes >> (2 * c + 1)) & 1 ? -1 : limit, zero, l);
+                                           (holes >> (2 * c + 1)) & 1 ? -1 : limit, zero, lt);
           } else {
-            many_probabilities<BF16, false>(tm_s + c * 32, f0, f1, v0, v1, m, 0, 0, zero, l);
+            many_probabilities<BF16, false>(tm_s + c * 32, f0, f1, v0, v1, m, 0, 0, zero, lt);
           }
         }
+        l = l + lt;
         // With three places for scores, a warp that has its last tile's scores only
         // knows that the output two tiles back is done: these came after another
         // row tile's. The last tile's output may only be asked for by its parity
