@@ -109,7 +109,7 @@ def test_one_token_above_very_many(tbs, dtype, bits, n, R):  # noqa: F811
 
 @pytest.mark.parametrize("at", ["first", "middle", "last"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("D,n,R,far", [(128, 1, 4, 14), (64, 1, 32, 14)])
+@pytest.mark.parametrize("D,n,R,far", [(128, 1, 4, 14), (64, 1, 32, 14), (128, 128, 16, 26), (64, 128, 16, 26)])
 def test_large_value_scale_without_weight(tbs, D, dtype, n, R, far, at):  # noqa: F811
     """A block whose values are 2^far times the others' and whose scores lie 60
     (in log2) below them changes nothing, whether a row sees it or not."""
@@ -149,7 +149,7 @@ def test_query_dimension_far_above_the_others(tbs, dtype, D, n, R):  # noqa: F81
 
 
 @pytest.mark.parametrize("kind", ["zeros first", "zeros far above 30", "zeros far above 45", "rising", "falling"])
-@pytest.mark.parametrize("D,n,R", [(128, 1, 4), (64, 1, 32)])
+@pytest.mark.parametrize("D,n,R", [(128, 1, 4), (64, 1, 32), (128, 128, 16), (64, 128, 16)])
 def test_weights_far_apart(tbs, D, n, R, kind):  # noqa: F811
     """Blocks of zeros (the smallest scale there is) before all others, or 30
     and 45 (in log2) above all others in the score; value scales that rise or

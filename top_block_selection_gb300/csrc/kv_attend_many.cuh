@@ -13,9 +13,10 @@
 //                  an error as large as the result's rounding. Of bf16 calls
 //                  one term (2^-11) is a quarter of it.
 // A thread owns a row: maximum, sum and rescaling need no other thread. Its
-// reference follows the largest score, but only once it is 2^8 too low: the
-// probabilities of fp16 have the range for that, and the output in tensor
-// memory is then seldom touched before the end of the item.
+// reference follows the largest score (where value scales lie far apart, the
+// largest score plus logarithm of the value scale), but only once it is 2^8 too
+// low: the probabilities of fp16 have the range for that, and the output in
+// tensor memory is then seldom touched before the end of the item.
 //
 // One CTA an SM takes two tiles of 128 rows (consecutive queries of a
 // sequence, the R heads of a KV head each) through the same key tiles of 128
@@ -49,6 +50,7 @@ constexpr int kManyRing = 4;       // tiles that are looked up ahead
 constexpr int kManyThreads = 448;  // 2 x 4 warps of rows, 4 converting, 1 issuing products, 1 looking up
 constexpr int kManyItemCost = 3;   // an item's queries and results, and its tiles' start, in tiles
 constexpr float kManyLag = 8.0f;   // log2 that a reference may fall behind
+constexpr float kManyNear = 6.0f;  // log2 between value scales that costs probabilities nothing
 constexpr float kManyScale = 64.0f;  // of a probability 1 at the largest value scale: 2^14 at most
 
 // Places for scores in tensor memory: 128 columns each beside the two outputs.
@@ -58,9 +60,11 @@ __host__ __device__ constexpr int many_buffers(int D) { return (512 - 2 * D) / 1
 
 struct ManyMeta {
   alignas(16) float ks[8], vs[8];  // key and value scales of 16 tokens each
+  alignas(16) float lv[8];         // log2 of the value scales against vmax, -kRange at least
   alignas(16) int32_t page[8];     // -1: no block
-  float vmax;
-  uint32_t holes;                  // bit i: tokens 16 i .. 16 i + 15 have no block
+  float vmax, shift;               // the largest value scale of the item so far; log2 of its growth here
+  uint32_t holes;                  // bit i: tokens 16 i .. 16 i + 15 have no block; bit 8: a value
+                                   // scale is below 2^-kManyNear of vmax
 };
 
 template <int D>
@@ -173,6 +177,7 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
   bool bad = false;
   many_items(a, start, 0, [&](const Entry& en, const ManyItem& w) {
     const int part = w.tiles;
+    float vmax = 0.0f, room = kRange;  // what shifts may add up to: sums stay in fp32's range
     const int32_t* const table = a.c.page_table + static_cast<int64_t>(en.b) * a.c.max_blocks;
     if (en.last_pos >= a.c.max_blocks * a.c.block) bad = true;  // longer than its page table
     for (int t = 0; t < part; ++t, ++g) {
@@ -190,7 +195,12 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
         ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
         vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
       }
-      const float vmax = warp_max(vs);
+      const float vnow = fmaxf(vmax, warp_max(vs)), lnow = log2_approx(vnow);
+      const float lv = fmaxf(log2_approx(vs) - lnow, -kRange);
+      const float shift = vmax > 0.0f ? fminf(lnow - log2_approx(vmax), room) : 0.0f;
+      room -= shift;
+      vmax = vnow;
+      const bool far = __any_sync(0xFFFFFFFFu, page >= 0 && lv < -kManyNear);
       const uint32_t holes = __ballot_sync(0xFFFFFFFFu, page < 0) & 0xFFu;
       const uint32_t at = g % kManyRing;
       if (g >= kManyRing) wait_or_stop(&s.meta_empty[at], (g / kManyRing + 1) & 1, &s.stop, a.status);
@@ -199,10 +209,12 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
       if (lane < 8) {
         m.ks[i] = ks;
         m.vs[i] = vs;
+        m.lv[i] = lv;
         m.page[i] = page;
         if (lane == 0) {
           m.vmax = vmax;
-          m.holes = holes;
+          m.shift = shift;
+          m.holes = holes | (far ? 0x100u : 0u);
         }
       }
       __syncwarp();
@@ -622,9 +634,30 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
           }
           ks = *reinterpret_cast<const float2*>(&meta.ks[(2 * c + 2) & 7]);
         }
-        const bool move = top > m + kManyLag, grow = vmax > vref;
-        if (__any_sync(0xFFFFFFFFu, move) || grow) {
-          const float mn = move ? top : m;
+        // Where value scales lie far apart, the row's largest weight: a score plus
+        // its value scale's logarithm (scores beyond 2^24, which have no steps
+        // below 1, count alone).
+        if (holes & 0x100u) {
+          float weight = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float x[16];
+            tmem_ld_cols<16>(tm_s + c * 16, x);
+            tmem_ld_wait();
+            const int limit = (holes >> c) & 1 ? -1 : row_pos - pos0 - c * 16;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e <= limit) mx = fmaxf(mx, x[e]);
+            weight = fmaxf(weight, fmaf(mx, mul * meta.ks[c], meta.lv[c]));
+          }
+          if (fabsf(top) < kFine) top = weight;
+        }
+        const bool grow = vmax > vref;
+        if (__any_sync(0xFFFFFFFFu, top > m + kManyLag) || grow) {
+          // Weights are relative to the largest value scale: a reference moves with it.
+          const float base = grow && fabsf(m) < kFine ? m - meta.shift : m;
+          const float mn = top > base + kManyLag ? top : base;
           float f = exp2_approx(m - mn);
           l = l * f2(f, f);
           m = mn;
@@ -691,9 +724,15 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
       tc_fence_after_sync();
       float l0, l1;
       f2_get(l, l0, l1);
-      const float sum = l0 + l1;
+      float sum = l0 + l1, all = 1.0f;
+      if (sum > kFine) {  // scores above the weights' reference: into the reference
+        const float mn = m + floorf(log2_approx(sum));
+        all = exp2_approx(m - mn);
+        sum *= all;
+        m = mn;
+      }
       const bool none = row_pos < 0 || sum == 0.0f;
-      const float f = vref * (1.0f / kManyScale) * (slot >= 0 ? 1.0f : __fdividef(1.0f, sum));
+      const float f = vref * (1.0f / kManyScale) * (slot >= 0 ? all : __fdividef(all, sum));
       const int64_t at = (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + wk.h * a.R + (t - jt * a.R);
       const bool mine = t < qt * a.R && en.j0 + j < a.n;
       float* const part_at = many_part<D>(a, slot, 0, w * kManyRows + t);
