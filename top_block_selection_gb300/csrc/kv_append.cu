@@ -11,9 +11,11 @@
 // not depend on the scale), and when a block's scale grows the older codes
 // are multiplied by a power of two: exact unless they fall below 2^-6, where
 // they are rounded again.
-// The block key is the mean of the block's stored keys, s * sum(codes) / n.
-// Every partial sum of up to 64 codes is a multiple of 2^-9 below 2^15, exact
-// in fp32 in any order.
+// The block key is the mean of the block's stored keys, s * sum(codes) / n. A
+// sum of up to 73 codes is a multiple of 2^-9 below 2^15, exact in fp32 in any
+// order; a warp adds at most 40. The warps' sums are added as integers, in
+// units of 2^-9, so that the sum of 128 codes is rounded once: it depends on
+// the codes alone.
 //
 // What bounds it: bytes. One CTA owns one (block, head, K or V): it holds the
 // block's new values in registers between the maximum and the rounding, so
@@ -339,8 +341,14 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
   __syncthreads();
   if (threadIdx.x < D) {
     float total = 0.0f;
+    int units = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w][threadIdx.x];
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const float part = s_sum[w][threadIdx.x];
+      total += part;
+      units += __float2int_rn(part * 512.0f);
+    }
+    if (!isnan(total)) total = __int2float_rn(units) * 0.001953125f;
     const float mean = __fdiv_rn(__fmul_rn(total, s), static_cast<float>(held));
     const int64_t at = ((static_cast<int64_t>(b) * a.c.Hkv + h) * a.c.max_blocks + blk64) * D + threadIdx.x;
     a.kb[at] = __half_as_ushort(__float2half_rn(mean));
