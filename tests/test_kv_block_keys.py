@@ -1,5 +1,6 @@
 """GPU tests of the block keys that the append makes: the fp16 mean of the
-block's stored keys, the same however its sum is split over threads."""
+block's stored keys, the same however its sum is split over threads, and what a
+selection next on the stream reads."""
 import numpy as np
 import pytest
 
@@ -54,3 +55,28 @@ def test_a_nan_key_makes_its_mean_nan(tbs):  # noqa: F811
     kb = dev(np.zeros((1, 1, 1, 64), np.float16))
     tbs.qsa_kv_append(dev(x, "f16"), dev(x, "f16"), *args, kb=kb)
     assert torch.isnan(kb).flatten().nonzero().flatten().tolist() == [9]
+
+
+@pytest.mark.parametrize("nq,n", [(1, 1), (16, 40), (300, 300)])
+def test_selection_reads_what_the_append_before_it_wrote(tbs, nq, n):  # noqa: F811
+    """Append with block keys and a selection over them, in a stream without a
+    wait between them, against the same with one."""
+    Hkv, D, block, k = 4, 128, 64, 8
+    c = kc.make_cache([n + 2000], Hkv, block, D, seed=n, spread=1.0)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.randn((Hkv, nq, 2, D), generator=g, device="cuda").half()
+    blocks = c["table"].shape[1]
+    for i in range(10):
+        x = torch.randn((1, n, 2 * Hkv, D), generator=g, device="cuda", dtype=torch.float16)
+        ids = []
+        for wait in (False, True):
+            args, _ = on_gpu(c)
+            kb = torch.randn((1, Hkv, blocks, D), generator=torch.Generator(device="cuda").manual_seed(i),
+                             device="cuda").half()
+            torch.cuda.synchronize()
+            tbs.qsa_kv_append(x[:, :, :Hkv], x[:, :, Hkv:], *args, kb=kb)
+            if wait:
+                torch.cuda.synchronize()
+            ids.append(tbs.qsa_score_select_batched(q, kb[0], n + 2000, k, block))
+        for a, b in zip(*ids):
+            assert torch.equal(a, b)

@@ -352,6 +352,9 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
     const float mean = __fdiv_rn(__fmul_rn(total, s), static_cast<float>(held));
     const int64_t at = ((static_cast<int64_t>(b) * a.c.Hkv + h) * a.c.max_blocks + blk64) * D + threadIdx.x;
     a.kb[at] = __half_as_ushort(__float2half_rn(mean));
+    // A scorer next on the stream may start early and reads block keys by bulk
+    // copies, without a fence between these plain stores and its copies.
+    fence_proxy_async_global();
   }
 }
 

@@ -131,8 +131,8 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) 
                : "memory");
 }
 
-// Orders this thread's view of global memory (e.g. data acquired from other
-// CTAs) before its later async-proxy (bulk copy) accesses.
+// Orders this thread's plain accesses of global memory (its own, or data acquired
+// from other CTAs) before later async-proxy (bulk copy) accesses.
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
