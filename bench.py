@@ -50,11 +50,11 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 NCU_TRAFFIC = {
     "fused_step_kernel": {"bytes_per_launch": 1651200,
                           "sources": ["fused_kernel.cuh", "select_row.cuh", "qsa_device.cuh"],
-                          "source_sha": "0f670db82810e77e",
+                          "source_sha": "921c26e4f2d5b228",
                           "workload": "long128k_nq256_h8_d128_kv131072"},
     "split_cluster_kernel": {"bytes_per_launch": 17340544,
                              "sources": ["split_reduce.cu", "qsa_device.cuh", "qsa_internal.h"],
-                             "source_sha": "d789cc2cc8faa7dc",
+                             "source_sha": "7cba59a035eab04b",
                              "workload": "split_g4_r8_c128_b2048"},
 }
 
