@@ -4,12 +4,14 @@ Each translation unit compiles in parallel; the objects link into
 ``top_block_selection_gb300/lib/libqsa.so`` with the CUDA runtime linked
 statically, so the library needs only the NVIDIA driver at run time. Beside it,
 ``_qsa_kv.so`` is the CPython module through which PyTorch tensors reach the
-paged-cache calls (g++, PyTorch's headers).
+paged-cache calls (g++, PyTorch's and Python's headers). Where these are not
+installed the library is built without it.
 Run ``python -m top_block_selection_gb300._build`` or call ``build()``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -25,6 +27,7 @@ LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIBPATH = os.path.join(LIBDIR, "libqsa.so")
 BINDINGPATH = os.path.join(LIBDIR, "_qsa_kv.so")
+BINDINGSRC = os.path.join(CSRC, "kv_binding.cpp")
 
 SOURCES = ["qsa_runtime.cu", "score_tc.cu", "select.cu", "convert.cu", "fused.cu", "fused_h1.cu",
            "fused_h2.cu", "fused_h4.cu", "fused_h8.cu", "fused_h16.cu", "fused_h32.cu",
@@ -51,14 +54,36 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_command(src: str) -> list:
+def _binding_needs():
+    """Why the CPython module cannot be built here, or None."""
+    if importlib.util.find_spec("torch") is None:
+        return "PyTorch is not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    return None
+
+
+def _binding_versions() -> str:
+    """What the CPython module was compiled against; it is built anew for others."""
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
+def _binding_stale() -> bool:
+    stamp = BINDINGPATH + ".versions"
+    if _stale(BINDINGPATH, [BINDINGSRC, __file__, os.path.join(INCLUDE, "qsa.h")]) or not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != _binding_versions()
+
+
+def _binding_command() -> list:
     """g++ command of the CPython module that marshals PyTorch tensors."""
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
-    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *(x for i in include for x in ("-isystem", i)), src, "-o",
-            BINDINGPATH, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *(x for i in include for x in ("-isystem", i)), BINDINGSRC,
+            "-o", BINDINGPATH, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
@@ -74,9 +99,12 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         objs.append(op)
         if _stale(op, [sp, __file__] + hdrs):
             jobs.append([nvcc, *ARCH, *COMMON, *extra_flags, "-c", sp, "-o", op])
-    binding = os.path.join(CSRC, "kv_binding.cpp")
-    if _stale(BINDINGPATH, [binding, __file__, os.path.join(INCLUDE, "qsa.h")]):
-        jobs.append(_binding_command(binding))
+    missing = _binding_needs()
+    binding = missing is None and _binding_stale()
+    if missing:
+        sys.stderr.write(f"{os.path.basename(BINDINGPATH)} not built: {missing}\n")
+    if binding:
+        jobs.append(_binding_command())
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for cmd, res in zip(jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs)):
@@ -84,6 +112,9 @@ def build(verbose: bool = False, extra_flags=()) -> str:
                     sys.stderr.write(res.stdout + res.stderr)
                 if res.returncode != 0:
                     raise RuntimeError("compilation failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    if binding:
+        with open(BINDINGPATH + ".versions", "w") as f:
+            f.write(_binding_versions())
     if jobs or _stale(LIBPATH, objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIBPATH, *objs, "-lrt", "-ldl", "-lpthread"]
         res = subprocess.run(cmd, capture_output=True, text=True)
