@@ -228,7 +228,12 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
   const int64_t blk64 = static_cast<int64_t>(p0 / a.c.block) + i;
   const int64_t start64 = blk64 * a.c.block;
   if (start64 >= sp.len) return;
-  const int64_t end64 = min(start64 + a.c.block, static_cast<int64_t>(sp.len));
+  int64_t end64 = min(start64 + a.c.block, static_cast<int64_t>(sp.len));
+  if (a.rot > 0 && end64 > a.max_pos) {  // positions past the angles are left out
+    if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
+    end64 = a.max_pos;
+    if (end64 <= max(static_cast<int64_t>(p0), start64)) return;
+  }
   int page = -1;
   if (blk64 < a.c.max_blocks) page = load_global(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
 
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, (PASSES < 4 ? 1024 : 768) / THREADS) 
       raw[t][0] = load8(src.data, row + l.off0);
       raw[t][1] = load8(src.data, row + l.off1);
     }
-  if (page < 0 || page >= a.c.n_pages || (a.rot > 0 && end64 > a.max_pos)) {
+  if (page < 0 || page >= a.c.n_pages) {
     if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
     return;
   }
