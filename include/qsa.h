@@ -372,8 +372,8 @@ qsa_status qsa_split_reduce_static(const float* partial_max, const float* partia
  * Supported: D 64 or 128; block 16, 32, 64 or 128; max_blocks * block <= 2^30;
  * Hkv <= 65535. The table, lens, n_new and ids are device data the host does
  * not see: a page outside [0, n_pages), a block past max_blocks or a position
- * past the angle table is skipped (no memory outside the buffers is touched)
- * and recorded; qsa_device_status then returns QSA_ERR_INVALID_ARG.
+ * past the angle table is skipped, alone (no memory outside the buffers is
+ * touched), and recorded; qsa_device_status then returns QSA_ERR_INVALID_ARG.
  */
 typedef enum { QSA_F16 = 0, QSA_BF16 = 1 } qsa_dtype;
 
@@ -410,8 +410,9 @@ typedef struct {
  *          rotated queries, rounded once; rows that do not exist are zero.
  *   kb     optional f16 [B, Hkv, max_blocks, D]: the mean of the stored keys
  *          of every block this call wrote to (block keys for
- *          qsa_select_step_batched with a kb for each head); other blocks keep
- *          theirs.
+ *          qsa_select_step_batched with a kb for each head), their sum, the
+ *          scaled sum, the mean and its fp16 each rounded once; other blocks
+ *          keep theirs.
  * Scales: s_new = the smallest power of two >= 2^-100 with max|x| <= 448 s_new
  * over the call's new tokens of the block and head (NaN left out, infinities
  * as the largest finite number). A block whose first token is new takes s_new;
@@ -443,7 +444,15 @@ qsa_status qsa_kv_append(const qsa_kv_cache* cache, const qsa_rows* k, const qsa
  *          twice. What qsa_select_step and its relatives return fits.
  *   out    [B, n, Hq, D] of `dtype`, contiguous, 16-byte aligned:
  *          sum_t p_t v_t with p = softmax(scale * q.k) over the tokens seen,
- *          rounded once. Sums and softmax statistics are fp32.
+ *          rounded once. Scores, sums and softmax statistics are fp32. A
+ *          probability times its value scale is held to 2^-12 of itself (bf16
+ *          calls: 2^-9). In calls of few rows (Hq / Hkv * n < 128, or
+ *          B * n * Hq < 2048, or ids) it is held to 2^-22 (2^-19) of the row's
+ *          largest at best, in finer steps where later tokens weigh less: 2^-19
+ *          (2^-16) of the largest among the last 3,000 (1,500) or so; and a
+ *          query's elements to 2^-25 (2^-21) of its largest. (Among tokens
+ *          whose value scales, or weights, lie more than 2^40 apart, the
+ *          lighter ones in coarser steps.)
  *   lse    optional f32 [B, n, Hq]: ln sum_t exp(scale * q.k_t).
  *          A row that does not exist or sees no token gives out 0, lse -inf.
  *   workspace  device, 16-byte aligned, at least

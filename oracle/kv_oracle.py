@@ -128,12 +128,12 @@ def attend_row(cache, q, b, j, n, h, scale, ids=None, terms=3):
     """(out [D], lse, bound [D]) in float64 of one query row on KV head h.
 
     `bound` is the first-order error of the GPU path before the rounding of
-    its result, from its number formats: a probability in e4m3 terms is off by
-    at most 2^-12 (three terms) or 2^-9 (two) of itself, or 2^-17 or 2^-14 of the
-    largest value scale among the tokens over the row's maximum; a score (fp32 sums of
-    exact products, a query's terms exact above 2^-18 of the row's largest)
-    by (D + 8) 2^-23 sum|q k| + 2^-18 max|q| sum|k|; exp2 and the scaling of
-    its argument by 2^-21 (1 + |x|)."""
+    its result, from its number formats: a probability times its value scale is
+    off by at most 2^-12 (three terms) or 2^-9 (two) of itself, or 2^-22 or
+    2^-19 of the row's largest; a score (fp32 sums of exact products, a query's
+    elements to 2^-25 or 2^-21 of the row's largest)
+    by (D + 8) 2^-23 sum|q k| + 2^-25 (2^-21) max|q| sum|k|; exp2 and the scaling
+    of its argument by 2^-21 (1 + |x|)."""
     seen = seen_tokens(cache, b, j, n, ids)
     D = q.shape[-1]
     if not seen:
@@ -150,10 +150,10 @@ def attend_row(cache, q, b, j, n, h, scale, ids=None, terms=3):
     total = p.sum()
     out = p @ vv / total
     dx = abs(scale) * ((D + 8) * 2.0 ** -23 * (np.abs(kk) @ np.abs(q))
-                       + 2.0 ** -18 * np.abs(q).max() * np.abs(kk).sum(1)) + 2.0 ** -21 * (1 + np.abs(x - m) + np.abs(x))
+                       + (2.0 ** -25 if terms == 3 else 2.0 ** -21) * np.abs(q).max() * np.abs(kk).sum(1)) + 2.0 ** -21 * (1 + np.abs(x - m) + np.abs(x))
     rel = (2.0 ** -12 if terms == 3 else 2.0 ** -9) + 2 * dx
     bound = ((p * rel)[:, None] * np.abs(vv)).sum(0) / total + (p * 2 * dx).sum() / total * np.abs(out) \
-        + (2.0 ** -17 if terms == 3 else 2.0 ** -14) * vs.max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
+        + (2.0 ** -22 if terms == 3 else 2.0 ** -19) * (p * vs).max() * np.abs(code).sum(0) / total + (len(seen) + 8) * 2.0 ** -23 * (p @ np.abs(vv)) / total
     return out, m + np.log(total), bound
 
 
