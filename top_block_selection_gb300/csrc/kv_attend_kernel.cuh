@@ -392,7 +392,9 @@ struct AttendShared {
   StageMeta meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
   alignas(16) float spread[C::W][4];         // per-warp: the largest value scale over its tokens' smallest (log2)
-  alignas(16) float moved[C::W][C::RT], alpha[C::W][C::RT];  // references, factors of what was summed (all warps write the same)
+  // References and factors of what was summed, where they move (all warps write the
+  // same); at an item's end, references or the largest scores, if these are above.
+  alignas(16) float moved[C::W][C::RT], alpha[C::W][C::RT];
   alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
   float mx[C::RT], sum[C::RT], inv[C::RT];  // joined, 1 / sum
   alignas(16) int32_t poison[128];  // first position whose value code is NaN, per dimension
@@ -731,7 +733,6 @@ constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448
 // then stay in fp32's range.
 constexpr float kRange = 40.0f;
 constexpr float kSlack = 3.0f;        // log2 that a reference may stand too high
-constexpr float kFine = 16777216.0f;  // a sum beyond this goes into the reference
 
 template <class C>
 __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t* ring, uint8_t* q_smem,
@@ -1017,28 +1018,26 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         if (RT * d < 32) l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], d);
       }
       if (lane % (32 / RT) == 0) s.red[wg][lane / (32 / RT)][warp] = l[0];
-      if (t < RT) s.ml[0][wg][t] = mine;
+      if (t < RT) {
+        s.ml[0][wg][t] = mine;
+        s.moved[wg][t] = fmaxf(mine, peak);
+      }
     }
     bar_sync(8, kAll);
-    // Then the common reference, and each warpgroup's weight against it. (A sum
-    // that is large because the reference went down goes into the reference.)
+    // Then the common reference, and each warpgroup's weight against it. (At least
+    // the largest score: sums are large where a reference went below it.)
     if (t < RT) {
-      float mx = s.ml[0][0][t], sum;
+      float mx = s.moved[0][t];
 #pragma unroll
-      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.ml[0][w][t]);
-#pragma unroll 1
-      for (bool again = false;; again = true) {
-        sum = 0.0f;
+      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.moved[w][t]);
+      s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
+      if (wg == 0) {
+        float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float4 v = *reinterpret_cast<const float4*>(s.red[w][t]);
           sum += ((v.x + v.y) + (v.z + v.w)) * exp2_approx(s.ml[0][w][t] - mx);
         }
-        if (again || !(sum > kFine)) break;
-        mx += floorf(log2_approx(sum));
-      }
-      s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
-      if (wg == 0) {
         s.mx[t] = mx;
         s.sum[t] = sum;
         s.inv[t] = __fdividef(1.0f, sum);

@@ -51,6 +51,7 @@ constexpr int kManyThreads = 448;  // 2 x 4 warps of rows, 4 converting, 1 issui
 constexpr int kManyItemCost = 3;   // an item's queries and results, and its tiles' start, in tiles
 constexpr float kManyLag = 8.0f;   // log2 that a reference may fall behind
 constexpr float kManyNear = 6.0f;  // log2 between value scales that costs probabilities nothing
+constexpr float kFine = 16777216.0f;  // scores beyond this have no steps below 1
 constexpr float kManyScale = 64.0f;  // of a probability 1 at the largest value scale: 2^14 at most
 
 // Places for scores in tensor memory: 128 columns each beside the two outputs.
