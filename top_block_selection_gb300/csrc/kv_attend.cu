@@ -10,8 +10,9 @@ namespace {
 constexpr int kCombineRows = 4;  // rows of a CTA, 128 threads each
 // What an item costs beside its tiles, in tiles: a batch of 32 requests of 100
 // tokens and 32 of 16,384 takes 168 us instead of 484 at 0, 256 requests of 64 to
-// 1,000 tokens 50 us instead of 114, 64 requests of 1,000 to 16,384 tokens 175 at
-// both. (At 3 the first two take 165 and 57, at 8 169 and 50.)
+// 829 tokens 50 us instead of 114, 64 requests of 1,000 to 16,384 tokens 175 at
+// both (at 3 the first two take 165 and 57, at 8 169 and 50; taken when
+// references only rose, the second is 54 us since).
 constexpr int kItemCost = 5;
 
 // Joins the parts of the item that CTA blockIdx.x of the attention began and
@@ -71,7 +72,10 @@ __global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __
 // 256 rows does not outweigh its faster tiles. Both forms, 4 to 32 heads of 128
 // dimensions, us (many | kv_attend_kernel): 8 KV heads x 128 rows over 8,192
 // tokens 33.5 | 29.3, 8 x 256 35.0 | 40.2, 8 x 512 44.1 | 65.4; 64 x 128 rows
-// over 4,096 50.9 | 67.9; 1 x 256 over 32,768 42.5 | 28.3, 1 x 512 41 | 39.
+// over 4,096 50.9 | 67.9; 1 x 256 over 32,768 42.5 | 28.3, 1 x 512 41 | 39. The
+// rows alone decide, although longer contexts favour the first form (2 x 1,024
+// rows over 100,000 tokens 132 | 268): calls of fewer rows over such contexts were
+// not measured.
 bool takes_many(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
   return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 2048;
 }

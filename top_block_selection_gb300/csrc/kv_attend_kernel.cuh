@@ -52,9 +52,10 @@
 //
 // Measured (with the join): a decode step of 64 requests over 1,000 to 16,384
 // tokens, 8 KV heads, bf16: 175 us, 6.5 TB/s (97% of a plain copy's rate). One
-// token over 2 x 131,073 tokens, 16 heads on each of 4 KV heads, fp16: 52 us,
-// 5.1 TB/s. 4,096 queries with 64 chosen blocks each, 16 heads on one KV head:
-// 460 us, 298 TFLOP/s; there the shared-memory pipe is 75% to 85% busy.
+// token over 2 x 131,073 tokens, 16 heads on each of 4 KV heads, fp16: 53 us,
+// 5.0 TB/s. 4,096 queries with 64 chosen blocks each, 16 heads on one KV head:
+// 491 us, 280 TFLOP/s; there the shared-memory pipe was 75% to 85% busy at 460 us
+// (terms without the steps' remainders, references that only rose).
 #pragma once
 
 #include <atomic>
@@ -722,9 +723,9 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
 }
 
 constexpr float kUnset = -3e38f;     // a reference that no score has set yet
-// A reference is set so far (log2) above the largest score: 3 would move it
-// less often (4,096 queries with chosen blocks 454 us instead of 461) but makes
-// the smallest terms coarser (error 2.5e-4 instead of 2.2e-4).
+// A reference is set so far (log2) above the largest weight: 3 would move it less
+// often (4,096 queries with chosen blocks 454 us instead of 461, when references
+// only rose) but makes the smallest terms coarser.
 constexpr float kMargin = 2.0f;
 constexpr float kProbScale = 128.0f; // code of a probability 1 at the largest value scale
 constexpr float kMaxCode = 8.8f;     // log2 of the largest code, 448

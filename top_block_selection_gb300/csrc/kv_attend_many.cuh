@@ -34,11 +34,12 @@
 //
 // What bounds it: the products take 3,700 of the 5,100 cycles of a pair of row
 // tiles and 128 tokens at D = 128 (fp16), the rest is waiting for
-// probabilities; at D = 64 the instructions of the exponentials. Measured with
-// the join, 32 heads on 8 KV heads, 4,096 queries over 32,768 tokens: fp16
-// 2,127 us, 969 TFLOP/s, bf16 1,835 us, 1,123 TFLOP/s; over their own 4,096
-// tokens 193 and 180 us. 2,048 queries of 64 dimensions over 32,768 tokens,
-// fp16: 889 us, 599 TFLOP/s.
+// probabilities; at D = 64 the latency of tensor memory reads and barriers (no
+// pipe above 42%, an instruction in 54% of the cycles). Measured with the join,
+// 32 heads on 8 KV heads, 4,096 queries over 32,768 tokens: fp16 2,157 us,
+// 956 TFLOP/s, bf16 1,882 us, 1,096 TFLOP/s; over their own 4,096 tokens 197 and
+// 184 us. 2,048 queries of 64 dimensions over 32,768 tokens: fp16 911 us,
+// 585 TFLOP/s, bf16 749 us.
 #pragma once
 
 #include "kv_attend_kernel.cuh"
