@@ -65,7 +65,11 @@ def _binding_needs():
 
 def _binding_versions() -> str:
     """What the CPython module was compiled against; it is built anew for others."""
-    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # importable, but not installed as a package
+        torch = importlib.util.find_spec("torch").origin
+    return f"torch {torch}, {sysconfig.get_config_var('EXT_SUFFIX')}\n"
 
 
 def _binding_stale() -> bool:
