@@ -472,6 +472,133 @@ qsa_status qsa_kv_attend(const qsa_kv_cache* cache, const qsa_rows* q, int32_t n
                          int32_t k, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, qsa_stream_t stream);
 
+/* ------------------------------------------------ the paged 4-bit cache
+ *
+ * The same cache in half the bytes: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), two to a byte, and one bf16 scale per (token, KV head) for
+ * keys and one for values: an element stands for scale * code. Tokens are
+ * independent of each other, so they can be appended, moved and dropped one by
+ * one.
+ *
+ *   k, v        codes [n_pages, Hkv, block, D / 2], device, 32-byte aligned;
+ *               element 2 i in the low half of byte i; page_stride bytes (a
+ *               multiple of 32, at least Hkv*block*D/2) from page to page.
+ *   k_scale, v_scale  bf16 [n_pages, Hkv, block], 16-byte aligned: positive
+ *               and finite, or NaN for a token that held one.
+ *   page_table, lens, n_new  as in qsa_kv_cache. A token's place is its slot,
+ *               0 to lens[b] - 1: row j of sequence b has slot lens[b] -
+ *               n_new[b] + j. Slots are positions until tokens are evicted.
+ * Supported: as for qsa_kv_cache. What is said there of device data that the
+ * host does not see holds here too.
+ */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint16_t* k_scale;
+  uint16_t* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* n_new;
+  int64_t page_stride;
+  int32_t n_pages, max_blocks, B, Hkv, block, D;
+} qsa_kv4_cache;
+
+/*
+ * qsa_kv4_append - rotate, quantise and store the new tokens' keys and values.
+ *
+ *   k, v, q, dtype, cos, sin, rot, max_pos, interleaved, q_out  as for
+ *          qsa_kv_append.
+ *   offset optional int32 [B], not negative: how far the position of each of
+ *          the sequence's new tokens lies beyond its slot (tokens that were
+ *          evicted, see qsa_kv4_evict). The angles are those of the position.
+ *   kb     optional f16 [B, Hkv, max_blocks, D]: the mean of the stored keys
+ *          of every block this call wrote to, summed in fp32 in an order that
+ *          the slots alone decide, rounded once; other blocks keep theirs.
+ * A token's scale is the smallest bf16 s >= 2^-100 with max|x| <= 6 s
+ * (infinities count as the largest finite float), its codes e2m1(x / s) to
+ * nearest even, infinities +-6; where an element is NaN the scale is NaN and
+ * the codes are 0. Older tokens stay as they are.
+ * A page that the call writes must appear once in the table rows of the call's
+ * sequences. No buffer may overlap another. Errors as for qsa_kv_append.
+ */
+qsa_status qsa_kv4_append(const qsa_kv4_cache* cache, const qsa_rows* k, const qsa_rows* v,
+                          const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                          const float* cos, const float* sin, int32_t rot, int32_t max_pos,
+                          int32_t interleaved, const int32_t* offset, void* q_out, uint16_t* kb,
+                          qsa_stream_t stream);
+
+/*
+ * qsa_kv4_read - the rows of the call as the cache holds them.
+ *
+ *   k_out, v_out  [B, n, Hkv, D] of `dtype`, contiguous, 16-byte aligned:
+ *          scale * code, rounded once; rows that do not exist are zero.
+ * Errors as for qsa_kv4_append.
+ */
+qsa_status qsa_kv4_read(const qsa_kv4_cache* cache, int32_t n, qsa_dtype dtype, void* k_out,
+                        void* v_out, qsa_stream_t stream);
+
+/*
+ * qsa_kv4_attend - attention of the n rows over the 4-bit cache, whole (ids
+ * NULL) or over chosen blocks. Everything is as for qsa_kv_attend, with slots
+ * for positions, but: at most 16 query heads on a KV head where D is 64; a NaN
+ * scale makes every dimension of the rows that see its token NaN.
+ */
+size_t qsa_kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
+qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,
+                          qsa_dtype dtype, float scale, const int32_t* ids, int32_t n_lists,
+                          int32_t k, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, qsa_stream_t stream);
+
+/*
+ * qsa_kv4_weights - adds to each cached token's weight what the n rows'
+ * attention gives it:
+ *   w[h, t] = decay * w[h, t] + sum over rows j that see t, over query heads i of
+ *             KV head h, of exp(scale * q[j, i] . k_t - lse[j, i])
+ * with decay * w[h, t] replaced by 0 for the call's own new tokens, and for
+ * every token when decay is 0 (w is then not read).
+ *
+ *   q, n, Hq, dtype, scale  as for qsa_kv4_attend.
+ *   lse    f32 [B, n, Hq], as qsa_kv4_attend wrote it for the same rows; a row
+ *          with -inf gives no token any weight.
+ *   decay  finite, not negative.
+ *   weights  f32 [n_pages, Hkv, block], 4-byte aligned. The tokens of the
+ *          call's sequences are updated, every other slot keeps its value.
+ * A page may appear once in the table rows of the call's sequences. Scores and
+ * sums are fp32, a query's elements held as by qsa_kv4_attend. Results do not
+ * depend on timing. cache->v and v_scale are not read and may be NULL. A token
+ * with a NaN scale gets the weight NaN from rows that see it.
+ * Errors as for qsa_kv4_attend (QSA_ERR_INVALID_ARG for a bad decay).
+ */
+qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,
+                           qsa_dtype dtype, float scale, const float* lse, float decay,
+                           float* weights, qsa_stream_t stream);
+
+/*
+ * qsa_kv4_evict - shortens every sequence of more than `budget` tokens to
+ * `budget`. Each KV head keeps of its own tokens the first `sink`, the last
+ * `recent`, and of those between the ones of the largest weight (equal ones:
+ * the lowest slot first; NaN counts as the largest), moved together in their
+ * order: codes, scales and weights.
+ *
+ *   weights  f32 [n_pages, Hkv, block], 4-byte aligned.
+ *   budget   >= 1; sink, recent >= 0, sink + recent <= budget.
+ *   lens_out int32 [B]: min(lens, budget). May not be lens itself.
+ *   offset   optional int32 [B]: grows by the number of tokens that went, as
+ *            qsa_kv4_append takes it.
+ *   workspace  device, 16-byte aligned, at least
+ *            qsa_kv4_evict_workspace_bytes bytes; needs no initialisation.
+ *            Calls that may run at the same time need separate ones.
+ * Slots from `budget` on keep what they held. A page of the call's sequences may
+ * appear once in their table rows. Block keys are not made anew. A sequence
+ * longer than its page table counts as that long; a page outside [0, n_pages)
+ * is recorded, its tokens have weight 0, and nothing is moved from or to it.
+ * n_new is not read. Errors as for qsa_kv4_append.
+ */
+size_t qsa_kv4_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t budget);
+qsa_status qsa_kv4_evict(const qsa_kv4_cache* cache, float* weights, int32_t budget, int32_t sink,
+                         int32_t recent, int32_t* lens_out, int32_t* offset, void* workspace,
+                         size_t workspace_bytes, qsa_stream_t stream);
+
 /*
  * qsa_device_status - synchronizes `stream`, then reads the current device's
  * status word, where kernels record a bounded wait that ran out and a cache

@@ -23,6 +23,8 @@ __all__ = [
     "qsa_select_step_batched", "qsa_score_select_batched", "qsa_select_step_launches",
     "qsa_split_reduce", "qsa_split_reduce_workspace_bytes", "EXPORTED_SYMBOLS",
     "qsa_kv_append", "qsa_kv_attend", "qsa_kv_attend_workspace_bytes",
+    "qsa_kv4_append", "qsa_kv4_read", "qsa_kv4_attend", "qsa_kv4_attend_workspace_bytes", "qsa_kv4_weights",
+    "qsa_kv4_evict", "qsa_kv4_evict_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +38,8 @@ EXPORTED_SYMBOLS = (
     "qsa_selftest_bounded_wait", "qsa_select_step_batched", "qsa_score_select_batched", "qsa_select_step_launches",
     "qsa_split_reduce_workspace_bytes", "qsa_split_reduce", "qsa_split_reduce_static",
     "qsa_kv_append", "qsa_kv_attend_workspace_bytes", "qsa_kv_attend",
+    "qsa_kv4_append", "qsa_kv4_read", "qsa_kv4_attend_workspace_bytes", "qsa_kv4_attend", "qsa_kv4_weights",
+    "qsa_kv4_evict_workspace_bytes", "qsa_kv4_evict",
 )
 
 STATUS_NAMES = {0: "QSA_OK", 1: "QSA_ERR_INVALID_ARG", 2: "QSA_ERR_UNSUPPORTED_GEOMETRY",
@@ -97,6 +101,14 @@ def load_library():
         "qsa_kv_attend_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "qsa_kv_attend": (ctypes.c_int, [vp, vp, i32, i32, i32, ctypes.c_float, vp, i32, i32, vp, vp, vp,
                                          ctypes.c_size_t, vp]),
+        "qsa_kv4_append": (ctypes.c_int, [vp] * 4 + [i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
+        "qsa_kv4_read": (ctypes.c_int, [vp, i32, i32, vp, vp, vp]),
+        "qsa_kv4_attend_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
+        "qsa_kv4_attend": (ctypes.c_int, [vp, vp, i32, i32, i32, ctypes.c_float, vp, i32, i32, vp, vp, vp,
+                                          ctypes.c_size_t, vp]),
+        "qsa_kv4_weights": (ctypes.c_int, [vp, vp, i32, i32, i32, ctypes.c_float, vp, ctypes.c_float, vp, vp]),
+        "qsa_kv4_evict_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "qsa_kv4_evict": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -576,7 +588,7 @@ def qsa_split_reduce(partial_max, partial_sum, partial_out, out=None, workspace=
     return out
 
 
-# ------------------------------------------------- the paged 8-bit cache
+# -------------------------------------------------------- the paged caches
 # These calls run once per layer and token of a serving loop, so their tensors
 # are checked and marshalled by a compiled module (csrc/kv_binding.cpp).
 _KV = None
@@ -594,7 +606,10 @@ def _kv_binding():
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_qsa_kv", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
-                  for fn in (lib.qsa_kv_append, lib.qsa_kv_attend, lib.qsa_kv_attend_workspace_bytes)))
+                  for fn in (lib.qsa_kv_append, lib.qsa_kv_attend, lib.qsa_kv_attend_workspace_bytes,
+                             lib.qsa_kv4_append, lib.qsa_kv4_read, lib.qsa_kv4_attend,
+                             lib.qsa_kv4_attend_workspace_bytes, lib.qsa_kv4_weights, lib.qsa_kv4_evict,
+                             lib.qsa_kv4_evict_workspace_bytes)))
     _KV = module
     return module
 
@@ -634,4 +649,85 @@ def qsa_kv_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids=N
                                       lse, workspace)
     if r.__class__ is int:
         _check(r, "qsa_kv_attend")
+    return r
+
+
+# ------------------------------------------------- the paged 4-bit cache
+def qsa_kv4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cos=None, sin=None,
+                   interleaved: bool = False, n_new=None, offset=None, q=None, q_out=None, kb=None):
+    """qsa_kv_append for the 4-bit cache: codes uint8 [n_pages, Hkv, block, D / 2],
+    two e2m1 codes to a byte, and scales bf16 [n_pages, Hkv, block], one a token.
+    offset, an optional int32 [B], is how far the positions of a sequence's new
+    tokens lie beyond their slots (the tokens that qsa_kv4_evict took out).
+    Returns q_out (None without q)."""
+    r = (_KV or _kv_binding()).append4(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cos, sin,
+                                       interleaved, n_new, q, q_out, kb, offset)
+    if r.__class__ is int:
+        _check(r, "qsa_kv4_append")
+    return r
+
+
+def qsa_kv4_read(k_cache, v_cache, k_scale, v_scale, page_table, lens, n: int, dtype=None, n_new=None, k_out=None,
+                 v_out=None):
+    """The last n tokens of each sequence (n_new[b] of them when given: the rows
+    that qsa_kv4_append wrote) as the 4-bit cache holds them: k, v [B, n, Hkv, D]
+    of dtype (float16, the default, or bfloat16), zeros where there is no token."""
+    torch = _torch()
+    if dtype not in (None, torch.float16, torch.bfloat16):
+        raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    r = (_KV or _kv_binding()).read4(k_cache, v_cache, k_scale, v_scale, page_table, lens, n, dtype is torch.bfloat16,
+                                     n_new, k_out, v_out)
+    if r.__class__ is int:
+        _check(r, "qsa_kv4_read")
+    return r
+
+
+def qsa_kv4_attend_workspace_bytes(B: int, n: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace qsa_kv4_attend needs."""
+    return int(load_library().qsa_kv4_attend_workspace_bytes(B, n, Hq, Hkv, D))
+
+
+def qsa_kv4_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids=None, scale=None, n_new=None,
+                   out=None, lse=None, workspace=None):
+    """qsa_kv_attend over the 4-bit cache (at most 16 query heads on a KV head
+    where D is 64); workspace: a CUDA uint8 tensor of
+    qsa_kv4_attend_workspace_bytes, allocated here when not given."""
+    r = (_KV or _kv_binding()).attend4(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids, scale, n_new, out,
+                                       lse, workspace)
+    if r.__class__ is int:
+        _check(r, "qsa_kv4_attend")
+    return r
+
+
+def qsa_kv4_weights(q, lse, k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, scale=None, n_new=None,
+                    decay: float = 1.0):
+    """Adds to each cached token's weight (f32 [n_pages, Hkv, block], in place)
+    what the attention of q [B, n, Hq, D] gives it, summed over the rows and the
+    query heads of its KV head, after multiplying it by decay; the call's own new
+    tokens start from 0, and so does every token when decay is 0. lse f32
+    [B, n, Hq] is what qsa_kv4_attend wrote for these rows. Returns weights."""
+    r = (_KV or _kv_binding()).weights4(q, lse, k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, scale,
+                                        n_new, decay)
+    if r.__class__ is int:
+        _check(r, "qsa_kv4_weights")
+    return r
+
+
+def qsa_kv4_evict_workspace_bytes(B: int, Hkv: int, budget: int) -> int:
+    """Bytes of workspace qsa_kv4_evict needs."""
+    return int(load_library().qsa_kv4_evict_workspace_bytes(B, Hkv, budget))
+
+
+def qsa_kv4_evict(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, budget: int, sink: int = 0,
+                  recent: int = 0, offset=None, lens_out=None, workspace=None):
+    """Shortens sequences of more than budget tokens to budget, in place: each KV
+    head keeps its first sink tokens, its last recent ones, and of the others
+    those of the largest weights (equal ones: the lowest slot first), in their
+    order. offset, an optional int32 [B], grows by the tokens that went. Returns
+    lens_out int32 [B], min(lens, budget) (a tensor other than lens, allocated
+    here when not given)."""
+    r = (_KV or _kv_binding()).evict4(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, budget, sink,
+                                      recent, offset, lens_out, workspace)
+    if r.__class__ is int:
+        _check(r, "qsa_kv4_evict")
     return r

@@ -1,0 +1,462 @@
+// kv4_weights.cu - the attention weight that each cached token of the 4-bit
+// cache gathers:
+//     w[h, t] = decay w[h, t] + sum_{j, i} exp(scale q[j, i] . k_t - lse[j, i])
+// over the call's rows j that see t and the query heads i of KV head h.
+//
+// The tokens are the M = 128 operand of the score product, as in
+// kv_attend_kernel.cuh, so that a thread owns a token (of 64 dimensions, two) and
+// adds its weights up alone: no exchange, no atomics, and results that do not
+// depend on timing. The exponent is y (c + c') - lse log2(e), with y the scaled
+// product and c + c' = scale log2(e) in two floats: a weight's relative error is
+// the exponent's absolute one, and one float of c would be the largest part of it.
+//
+// One CTA an SM. The tiles of all (sequence, KV head) items are dealt to the
+// CTAs in equal contiguous shares. A warp loads keys (TMA) and scales ahead, four
+// make the e4m3 terms of up to kGroups x RT rows, one issues the products, and
+// two warpgroups take the tiles in turn, each with two places for scores in
+// tensor memory. More rows than that go over the share's tiles of the item again
+// (from L2), adding to what the pass before left.
+//
+// What bounds it: for a decode step the keys and weights from HBM; for many rows
+// the exponentials.
+#include "kv_attend_kernel.cuh"
+
+#include <algorithm>
+
+namespace qsa {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kGroups = 4;       // of rows, in one pass
+constexpr int kQueryWarps = 4;
+constexpr int kThreads = 2 * 128 + 64 + 32 * kQueryWarps;
+constexpr int kPlace = 128;      // columns of a place for scores
+
+struct WeightsArgs {
+  AttendArgs a;      // out, lse, ids, parts, jobs unused; scale_log2 = 1
+  const float* lse;
+  float* weights;
+  float c_hi, c_lo;  // scale * log2(e)
+  float decay;
+};
+
+struct Sequence {
+  int32_t len, first, n_new, tiles;  // tokens, slot of the first new one, new ones
+};
+__device__ __forceinline__ Sequence sequence_of(const AttendArgs& a, int b) {
+  const Span s = span_of(a.c, b, a.n);
+  Sequence q;
+  q.len = min(s.len, a.c.max_blocks * a.c.block);
+  q.first = s.first;
+  q.n_new = s.n_new;
+  q.tiles = (q.len + (1 << a.tile_log2) - 1) >> a.tile_log2;
+  return q;
+}
+
+template <class C>
+struct GroupRows {
+  ItemInfo<C::RT> info;
+  alignas(16) float hi[C::RT], lo[C::RT], nl[C::RT];  // c of the row, its -lse log2(e)
+};
+
+template <class C>
+struct WeightsShared {
+  GroupRows<C> rows[2][kGroups];
+  alignas(16) uint16_t ks[kStages][C::kTokens];
+  alignas(16) int64_t row0[kStages][C::kSlots];  // of a slot's first token among the weights; -1: no block
+  uint64_t k_full[kStages], k_empty[kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2][2], s_empty[2][2];
+  int64_t scan[kThreads / 32];
+  int64_t lo, hi, total;
+  int32_t b, h, t;  // where the share begins
+  uint32_t tmem, stop;
+};
+
+// f(sequence number, sequence, head, first tile, tiles) for the items of the CTA's share.
+template <class C, class F>
+__device__ __forceinline__ void each_item(const AttendArgs& a, const WeightsShared<C>& s, F&& f) {
+  int64_t left = s.hi - s.lo;
+  int b = s.b, h = s.h, t = s.t;
+  while (left > 0 && b < a.c.B) {
+    const Sequence q = sequence_of(a, b);
+    for (; h < a.c.Hkv && left > 0 && q.tiles > 0; ++h, t = 0) {
+      const int part = static_cast<int>(min(static_cast<int64_t>(q.tiles - t), left));
+      f(b, q, h, t, part);
+      left -= part;
+      if (t + part < q.tiles) return;
+    }
+    ++b;
+    h = t = 0;
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightsArgs w) {
+  constexpr int PAR = C::PAR, RT = C::RT, N = C::N;
+  constexpr int kTile = kKvTile * 128;  // bytes of a key tile
+  extern __shared__ uint8_t raw[];
+  uint8_t* const ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* const q_smem = ring + kStages * kTile;
+  WeightsShared<C>& s = *reinterpret_cast<WeightsShared<C>*>(q_smem + 2 * kGroups * C::kQBytes);
+  const AttendArgs& a = w.a;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.k_full[i], 2);
+      mbar_init(&s.k_empty[i], 5);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], kQueryWarps);
+      mbar_init(&s.q_empty[i], 9);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&s.s_full[i][j], 1);
+        mbar_init(&s.s_empty[i][j], 4);
+      }
+    }
+    s.stop = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tm_k);
+  }
+  pdl_wait();
+  fence_proxy_async_global();  // earlier plain stores, before this kernel's bulk loads
+  // Tensor memory is asked for only now, and later kernels of the stream may start
+  // only once every CTA has it (see kv_attend_kernel).
+  if (warp == 9) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  // The share [lo, hi) of all tiles, and the item that it begins in.
+  {
+    const int B = a.c.B, per = (B + kThreads - 1) / kThreads;
+    const int b0 = min(per * tid, B), b1 = min(b0 + per, B);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += sequence_of(a, b).tiles;
+    int64_t before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += v;
+    }
+    if (lane == 31) s.scan[warp] = before;
+    __syncthreads();
+    int64_t all = 0;
+    before -= sum;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += s.scan[i];
+      all += s.scan[i];
+    }
+    const int64_t total = all * a.c.Hkv;
+    const int64_t lo = divide(total * blockIdx.x, gridDim.x), hi = divide(total * (blockIdx.x + 1), gridDim.x);
+    if (tid == 0) {
+      s.lo = lo;
+      s.hi = hi;
+      if (lo == hi) s.b = B;
+    }
+    int64_t at = before * a.c.Hkv;
+    if (lo < hi && at <= lo && lo < at + sum * a.c.Hkv) {
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = sequence_of(a, b).tiles;
+        const int64_t units = static_cast<int64_t>(tiles) * a.c.Hkv;
+        if (lo < at + units) {
+          s.b = b;
+          s.h = static_cast<int>((lo - at) / tiles);
+          s.t = static_cast<int>((lo - at) % tiles);
+          break;
+        }
+        at += units;
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  pdl_launch_dependents();
+
+  const int n_groups = (a.n + a.qt - 1) / a.qt;  // of rows, a.qt queries each
+  const int passes = (n_groups + kGroups - 1) / kGroups;
+  const int per_pass = min(n_groups, kGroups);
+
+  if (warp < 8) {
+    // ------------------------------------------------------- the weights
+    const int wg = warp / 4, t = tid % 128;
+    const uint32_t lane_addr = static_cast<uint32_t>(warp % 4 * 32) << 16;
+    const uint32_t tm = uniform(s.tmem) + wg * 2 * kPlace + lane_addr;
+    const int slot = t * PAR / a.c.block, off = t * PAR - slot * a.c.block;
+    uint32_t g0 = 0, unit = 0, pc = 0;
+    each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
+      for (int pass = 0; pass < passes; ++pass, ++pc) {
+        const uint32_t buf = pc & 1;
+        wait_or_stop(&s.q_full[buf], (pc >> 1) & 1, &s.stop, a.status);
+        const int groups = min(per_pass, n_groups - pass * kGroups);
+        const int lo_pos = s.rows[buf][0].info.lo_pos;
+        for (uint32_t g = g0 + ((g0 ^ wg) & 1); g < g0 + part; g += 2) {
+          const uint32_t st = g % kStages;
+          wait_or_stop(&s.k_full[st], (g / kStages) & 1, &s.stop, a.status);
+          const int pos = ((t0 + static_cast<int>(g - g0)) << a.tile_log2) + t * PAR;
+          float k_mul[PAR];
+#pragma unroll
+          for (int i = 0; i < PAR; ++i)
+            k_mul[i] = __uint_as_float(static_cast<uint32_t>(s.ks[st][t * PAR + i]) << 16);
+          const int64_t row0 = s.row0[st][slot];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.k_empty[st]);
+          float* const at = w.weights + row0 + off;
+          bool there[PAR];
+          float old[PAR], acc[PAR];
+#pragma unroll
+          for (int i = 0; i < PAR; ++i) {
+            there[i] = row0 >= 0 && pos + i < q.len;
+            old[i] = acc[i] = 0.0f;
+            if (there[i] && (pass > 0 || (w.decay != 0.0f && pos + i < q.first))) old[i] = load_global(at + i);
+          }
+          for (int gr = 0; gr < groups; ++gr, ++unit) {
+            const GroupRows<C>& rows = s.rows[buf][gr];
+            const uint32_t place = unit & 1;
+            wait_or_stop(&s.s_full[wg][place], (unit >> 1) & 1, &s.stop, a.status);
+            __syncwarp();
+            tc_fence_after_sync();
+            float e[RT];
+            tmem_rows<C, false>(tm + place * kPlace, e);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_empty[wg][place]);
+#pragma unroll
+            for (int r = 0; r < RT; r += 2) {
+              const float k = k_mul[r / C::RR];
+              const F2 y = f2(e[r], e[r + 1]) * f2(k, k);
+              const F2 x = fma2(y, f2(rows.hi[r], rows.hi[r + 1]),
+                                fma2(y, f2(rows.lo[r], rows.lo[r + 1]), f2(rows.nl[r], rows.nl[r + 1])));
+              f2_get(x, e[r], e[r + 1]);
+              e[r] = exp2_approx(e[r]);
+              e[r + 1] = exp2_approx(e[r + 1]);
+            }
+            if (pos + PAR - 1 > lo_pos) {
+#pragma unroll
+              for (int r = 0; r < RT; ++r)
+                if (pos + r / C::RR > rows.info.row_pos[r]) e[r] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < PAR; ++i) {
+              F2 sum = f2(0.0f, 0.0f);
+#pragma unroll
+              for (int r = 0; r < C::RR; r += 2) sum = sum + f2(e[i * C::RR + r], e[i * C::RR + r + 1]);
+              float s0, s1;
+              f2_get(sum, s0, s1);
+              acc[i] += s0 + s1;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < PAR; ++i)
+            if (there[i]) at[i] = (pass > 0 ? old[i] : old[i] * w.decay) + acc[i];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_empty[buf]);
+        g0 += part;
+      }
+    });
+  } else if (warp == 8) {
+    // ------------------------------------------------------- keys, scales
+    const int spt = a.spt, per_batch = 32 / spt, my_k = lane / spt, my_slot = lane % spt;
+    uint32_t g = 0;
+    bool bad = false, ok = true;
+    each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
+      if (load_global(a.c.lens + b) > q.len) bad = true;  // longer than its page table
+      const int32_t* const table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks;
+      const int y = h * a.c.block / PAR, slab = a.c.block * C::HD;
+      for (int pass = 0; pass < passes; ++pass)
+        for (int k0 = 0; k0 < part; k0 += per_batch) {
+          const int tiles = min(per_batch, part - k0);
+          const int blk = (t0 + k0 + my_k) * spt + my_slot;
+          int page = -1;
+          if (my_k < tiles && static_cast<int64_t>(blk) * a.c.block < q.len) {
+            page = load_global(table + blk);
+            if (page < 0 || page >= a.c.n_pages) {
+              bad = true;
+              page = -1;
+            }
+          }
+          using Scales = typename std::conditional<PAR == 2, uint4, uint2>::type;
+          Scales next{};
+          auto scales = [&](int i) {
+            const int t = lane * 4 * PAR, from = i * spt + t / a.c.block;
+            const int of = __shfl_sync(0xFFFFFFFFu, page, from & 31);
+            next = Scales{};
+            if (i < tiles && of >= 0)
+              next = load_global(reinterpret_cast<const Scales*>(
+                  a.c.k_scale4 + (static_cast<int64_t>(of) * a.c.Hkv + h) * a.c.block + (t & (a.c.block - 1))));
+          };
+          scales(0);
+          for (int i = 0; i < tiles; ++i, ++g) {
+            const uint32_t st = g % kStages;
+            if (ok && g >= kStages) ok = wait_or_stop(&s.k_empty[st], ((g / kStages) & 1) ^ 1, &s.stop, a.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) continue;
+            const uint32_t there = __ballot_sync(0xFFFFFFFFu, my_k == i && page >= 0);
+            // Bytes count as they are packed, half of a slab's.
+            if (elect_one()) mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2));
+            for (int j = 0; j < spt; ++j) {
+              const int z = __shfl_sync(0xFFFFFFFFu, page, i * spt + j);
+              if (z >= 0 && elect_one()) tma_load_3d(ring + st * kTile + j * slab, &tm_k, 0, y, z, &s.k_full[st]);
+              __syncwarp();
+            }
+            *reinterpret_cast<Scales*>(&s.ks[st][lane * 4 * PAR]) = next;
+            if (my_k == i)
+              s.row0[st][my_slot] = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
+            scales(i + 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.k_full[st]);
+          }
+        }
+    });
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, kErrCacheIndex);
+    if (!ok)  // let the copies in flight land before the CTA gives its memory back
+      for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s.k_full[i], 0, 10000000ull), mbar_wait_bounded(&s.k_full[i], 1, 10000000ull);
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- products
+    const uint32_t tmem = uniform(s.tmem), ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem);
+    const bool leader = elect_one();
+    uint32_t g0 = 0, pc = 0, unit[2] = {0, 0};
+    each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
+      for (int pass = 0; pass < passes; ++pass, ++pc) {
+        const uint32_t buf = pc & 1;
+        const int groups = min(per_pass, n_groups - pass * kGroups);
+        wait_or_stop(&s.q_full[buf], (pc >> 1) & 1, &s.stop, a.status);
+        // The two warpgroups' tiles side by side, so that both have scores to work on.
+        for (uint32_t pair = g0 & ~1u; pair < g0 + part; pair += 2)
+          for (int gr = 0; gr < groups; ++gr)
+#pragma unroll
+            for (int wg = 0; wg < 2; ++wg) {
+              const uint32_t g = pair + wg, st = g % kStages;
+              if (g < g0 || g >= g0 + part) continue;
+              if (gr == 0) wait_or_stop(&s.k_full[st], (g / kStages) & 1, &s.stop, a.status);
+              const uint32_t place = unit[wg] & 1;
+              if (unit[wg] >= 2) wait_or_stop(&s.s_empty[wg][place], ((unit[wg] >> 1) & 1) ^ 1, &s.stop, a.status);
+              ++unit[wg];
+              __syncwarp();
+              tc_fence_after_sync();
+              if (leader) {
+                const uint64_t ka = smem_desc_rows<128>(ring_addr + st * kTile);
+                const uint64_t qa = smem_desc_rows<128>(q_addr + (buf * kGroups + gr) * C::kQBytes);
+                const uint32_t to = tmem + (wg * 2 + place) * kPlace;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_f8_ss(to, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, true), ks > 0);
+                mma_commit(&s.s_full[wg][place]);
+                if (gr == groups - 1) mma_commit(&s.k_empty[st]);
+              }
+              __syncwarp();
+            }
+        if (leader) mma_commit(&s.q_empty[buf]);
+        __syncwarp();
+        g0 += part;
+      }
+    });
+  } else {
+    // ------------------------------------------------------------ queries
+    uint32_t pc = 0;
+    each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
+      for (int pass = 0; pass < passes; ++pass, ++pc) {
+        const uint32_t buf = pc & 1;
+        if (pc >= 2) wait_or_stop(&s.q_empty[buf], ((pc >> 1) & 1) ^ 1, &s.stop, a.status);
+        const int groups = min(per_pass, n_groups - pass * kGroups);
+        for (int gr = 0; gr < groups; ++gr) {
+          GroupRows<C>& rows = s.rows[buf][gr];
+          Entry en{};
+          en.b = b;
+          en.j0 = (pass * kGroups + gr) * a.qt;
+          en.nq = min(en.j0 + a.qt, q.n_new) - en.j0;
+          en.first_pos = q.first + en.j0;
+          for (int r0 = (warp - 10) * 4; r0 < RT; r0 += 4 * kQueryWarps) {
+            query_rows<C, 4>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, h, r0, 1);
+            __syncwarp();
+            const int r = r0 + lane;
+            if (lane < 4 && r < RT) {
+              const int pos = rows.info.row_pos[r];
+              const bool there = pos >= 0 && pos != kKvNoToken;
+              const float lse = there ? load_global(w.lse + rows.info.row_at[r]) : -INFINITY;
+              const bool gives = there && lse != -INFINITY;
+              const float t = rows.info.row_mul[r];
+              rows.hi[r] = gives ? t * w.c_hi : 0.0f;
+              rows.lo[r] = gives ? t * w.c_lo : 0.0f;
+              rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
+              if (!there) rows.info.row_pos[r] = -1;
+            }
+            __syncwarp();
+          }
+        }
+        // The first position that not all of the pass's rows see.
+        if (warp == 10 && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups * a.qt, 0) : -1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_full[buf]);
+      }
+    });
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(s.tmem, 512);
+}
+
+template <int D, int RT, int T>
+cudaError_t weights_form(const CUtensorMap& tk, const WeightsArgs& w, int grid, int device, cudaStream_t stream) {
+  using C = AttendCfg<D, RT, T, true>;
+  constexpr int smem = 1024 + kStages * kKvTile * 128 + 2 * kGroups * C::kQBytes + static_cast<int>(sizeof(WeightsShared<C>));
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(C::N <= kPlace, "tensor memory");
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << device;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv4_weights_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  const cudaError_t e = launch_pdl(kv4_weights_kernel<C>, dim3(grid), dim3(kThreads), smem, stream, tk, w);
+  if (e == cudaSuccess) plan_add("kv4_weights_kernel");
+  return e;
+}
+
+template <int D, int T>
+cudaError_t weights_rows(int rt, const CUtensorMap& tk, const WeightsArgs& w, int grid, int device, cudaStream_t stream) {
+  if (rt <= 8) return weights_form<D, 8, T>(tk, w, grid, device, stream);
+  if (rt <= 16) return weights_form<D, 16, T>(tk, w, grid, device, stream);
+  return weights_form<D, 32, T>(tk, w, grid, device, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_weights(const Kv4WeightsProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+  WeightsArgs w{};
+  AttendArgs& a = w.a;
+  a.c = p.cache;
+  a.q = p.q;
+  a.status = dev.status_word;
+  a.scale_log2 = 1.0f;
+  a.n = p.n;
+  a.Hq = p.Hq;
+  a.R = p.Hq / p.cache.Hkv;
+  a.bf16 = p.bf16;
+  const int columns = 128 / p.cache.D;  // of a row: one for each token of an operand row
+  a.tile_log2 = columns == 2 ? 8 : 7;
+  a.spt = (1 << a.tile_log2) / p.cache.block;
+  a.qt = std::min(p.n, std::max(1, 32 / (a.R * columns)));
+  w.lse = p.lse;
+  w.weights = p.weights;
+  w.decay = p.decay;
+  const double c = static_cast<double>(p.scale) * 1.4426950408889634;
+  w.c_hi = static_cast<float>(c);
+  w.c_lo = static_cast<float>(c - w.c_hi);
+  const int64_t most = static_cast<int64_t>(p.cache.B) * p.cache.Hkv * ((p.cache.max_blocks - 1) / a.spt + 1);
+  const int grid = static_cast<int>(std::min<int64_t>(dev.sm_count, most));
+  CUtensorMap tk;
+  if (!encode_cache_map4(&tk, p.cache.k, p.cache)) return cudaErrorInvalidValue;
+  const int rt = a.qt * a.R * columns;
+  if (p.cache.D == 64)
+    return p.bf16 ? weights_rows<64, 2>(rt, tk, w, grid, dev.id, stream)
+                  : weights_rows<64, 3>(rt, tk, w, grid, dev.id, stream);
+  return p.bf16 ? weights_rows<128, 2>(rt, tk, w, grid, dev.id, stream)
+                : weights_rows<128, 3>(rt, tk, w, grid, dev.id, stream);
+}
+
+}  // namespace qsa

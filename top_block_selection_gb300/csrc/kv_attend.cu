@@ -96,16 +96,14 @@ bool encode_cache_map(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
-  if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kKvMaxGroup || (D != 64 && D != 128))
-    return 0;
+size_t workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D, int group) {
+  if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > group || (D != 64 && D != 128)) return 0;
   const size_t rows = takes_many(B, n, Hq, Hkv) ? 2 * kManyRows : kKvMaxGroup;
   return sizeof(float) * 2 * kKvMaxCtas * rows * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
 }
 
-cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+// Either cache's attention.
+cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream, bool four) {
   AttendArgs a{};
   a.c = p.cache;
   a.q = p.q;
@@ -119,17 +117,20 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   a.R = p.Hq / p.cache.Hkv;
   a.n_lists = p.n_lists;
   a.k = p.k;
-  a.spt = kKvTile / p.cache.block;
   a.bf16 = p.bf16;
   // Chosen blocks are each query's own; over the whole cache, consecutive
   // queries of a sequence share a tile, of up to 16 rows (the form of 32 rows
   // holds too much state for its threads and takes more than twice as long a
-  // tile) or two of up to 128.
+  // tile) or two of up to 128. A row of the 4-bit cache's 64 dimensions has a
+  // column for each of the two tokens in an operand row.
   const bool many = !p.ids && takes_many(p.cache.B, p.n, p.Hq, p.cache.Hkv);
-  a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / a.R));
+  const int columns = four && !many ? 128 / p.cache.D : 1;
+  a.tile_log2 = columns == 2 ? 8 : 7;
+  a.spt = (1 << a.tile_log2) / p.cache.block;
+  a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / (a.R * columns)));
   a.n_qt = (p.n + a.qt - 1) / a.qt;
   a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
-  const int rt = rows_form(a.qt * a.R);
+  const int rt = rows_form(a.qt * a.R * columns);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
   const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
   const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * p.cache.Hkv * item_tiles;
@@ -142,19 +143,50 @@ cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cu
   if (many) return launch_attend_many(a, grid, item_tiles > 1, dev.id, stream);
 
   CUtensorMap tk, tv;
-  if (!encode_cache_map(&tk, p.cache.k, p.cache) || !encode_cache_map(&tv, p.cache.v, p.cache))
-    return cudaErrorInvalidValue;
-  const AttendLaunch form = p.cache.D == 64 ? (p.bf16 ? attend_d64_t2 : attend_d64_t3)
-                                            : (p.bf16 ? attend_d128_t2 : attend_d128_t3);
-  cudaError_t e = form(rt, tk, tv, a, grid, dev.id, stream);
+  const auto encode = four ? encode_cache_map4 : encode_cache_map;
+  if (!encode(&tk, p.cache.k, p.cache) || !encode(&tv, p.cache.v, p.cache)) return cudaErrorInvalidValue;
+  const AttendLaunch forms[2][2][2] = {{{attend_d64_t3, attend_d64_t2}, {attend_d128_t3, attend_d128_t2}},
+                                       {{attend4_d64_t3, attend4_d64_t2}, {attend4_d128_t3, attend4_d128_t2}}};
+  cudaError_t e = forms[four][p.cache.D == 128][p.bf16](rt, tk, tv, a, grid, dev.id, stream);
   if (e != cudaSuccess) return e;
-  plan_add("kv_attend_kernel");
+  plan_add(four ? "kv4_attend_kernel" : "kv_attend_kernel");
   // Items of one tile are never split.
   if (item_tiles == 1) return cudaSuccess;
   e = launch_pdl(kv_combine_kernel, dim3(grid, (a.qt * a.R + kCombineRows - 1) / kCombineRows),
                  dim3(128 * kCombineRows), 0, stream, a);
   if (e == cudaSuccess) plan_add("kv_combine_kernel");
   return e;
+}
+
+}  // namespace
+
+// Of the 4-bit cache: operand rows of 128 codes, one token of 128 dimensions or
+// two of 64, which the copy spreads to 128 bytes.
+bool encode_cache_map4(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const int rows = c.block * c.D / 128;
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(c.Hkv) * rows, static_cast<cuuint64_t>(c.n_pages)};
+  const cuuint64_t strides[2] = {64, static_cast<cuuint64_t>(c.page_stride)};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<uint8_t*>(base), dims, strides, box, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  return workspace_bytes(B, n, Hq, Hkv, D, kKvMaxGroup);
+}
+size_t kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  return workspace_bytes(B, n, Hq, Hkv, D, D == 64 ? kKvMaxGroup / 2 : kKvMaxGroup);
+}
+
+cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+  return launch(p, dev, stream, false);
+}
+cudaError_t launch_kv4_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
+  return launch(p, dev, stream, true);
 }
 
 }  // namespace qsa

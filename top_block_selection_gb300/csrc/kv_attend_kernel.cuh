@@ -59,6 +59,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -69,7 +70,7 @@
 namespace qsa {
 
 constexpr int kKvTile = 128;       // tokens of a tile
-constexpr int kKvMaxSlots = 8;     // blocks of a tile (block >= 16)
+constexpr int kKvMaxSlots = 8;     // blocks of 128 tokens (block >= 16)
 constexpr int kKvMaxCtas = 192;    // bound of the grid, sizes the workspace
 constexpr int kKvNoToken = 0x3FFFFFFF;
 
@@ -89,6 +90,7 @@ struct AttendArgs {
   int32_t spt;       // blocks of a tile
   int32_t fixed;     // tiles of every item over chosen blocks, else 0
   int32_t item_cost; // what an item costs beside its tiles, in tiles: counts where they are dealt out
+  int32_t tile_log2; // log2 of a tile's tokens
   bool bf16;
 };
 
@@ -121,7 +123,7 @@ __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
     t.tiles = a.fixed;
   } else {
     const int keys = min(t.last_pos + 1, a.c.max_blocks * a.c.block);
-    t.tiles = keys > 0 ? (keys - 1) / kKvTile + 1 : 1;
+    t.tiles = keys > 0 ? ((keys - 1) >> a.tile_log2) + 1 : 1;
   }
   return t;
 }
@@ -157,9 +159,11 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
 
 // Instruction descriptor: fp32 D (bits 4-5 = 1), e4m3 A and B (formats 0), A
 // and B MN-major when asked (bits 15, 16), N >> 3 at bits 17-22, M >> 4 at
-// bits 24-28.
-__host__ __device__ constexpr uint32_t idesc_f8(int N, bool mn_major) {
-  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// bits 24-28. With `e2m1` A holds 4-bit codes (format 5), 16 of them in the
+// first half of 16 bytes each, as the tensor map of 16U4_ALIGN16B lays them out.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, bool mn_major, bool e2m1 = false) {
+  return (1u << 4) | (e2m1 ? 5u << 7 : 0u) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (8u << 24);
 }
 
 // Shared-memory descriptor of rows of ROW bytes (128 or 64) swizzled over
@@ -344,13 +348,21 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
 }
 
 // ------------------------------------------------------------ configuration
-template <int D_, int RT_, int T_>
+template <int D_, int RT_, int T_, bool FOUR_ = false>
 struct AttendCfg {
-  static constexpr int D = D_;
-  static constexpr int RT = RT_;                            // rows
+  static constexpr bool kFour = FOUR_;                      // the 4-bit cache
+  static constexpr int HD = D_;                             // dimensions of a head
+  static constexpr int PAR = FOUR_ ? 128 / D_ : 1;          // tokens of an operand row
+  static constexpr int D = HD * PAR;                        // elements of an operand row
+  static constexpr int RT = RT_;                            // columns of a term: PAR for each row
+  static constexpr int RR = RT / PAR;                       // rows
+  static constexpr int kTokens = kKvTile * PAR;             // of a tile
+  static constexpr int kSlots = kKvMaxSlots * PAR;          // its blocks
   static constexpr int T = T_;                              // e4m3 terms of a value
   static constexpr int N = (T * RT + 15) / 16 * 16;         // columns: the terms of each row
-  static constexpr int W = RT >= 32 ? 2 : 3;                // warpgroups
+  // Warpgroups. (Beside the scales of its tokens, the 4-bit cache's form of 16
+  // columns in three terms has no room in shared memory for a third one's probabilities.)
+  static constexpr int W = RT >= 32 || (kFour && RT == 16 && T_ == 3) ? 2 : 3;
   static constexpr int kThreads = W * 128 + W * 32 + 32;    // they, a producer warp for each, the query warp
   static constexpr int kStageBytes = 2 * kKvTile * D;       // K then V
   // A stage serves one warpgroup only: a parity wait may not run two phases
@@ -359,7 +371,7 @@ struct AttendCfg {
   static_assert(kStages % W == 0, "a stage serves one warpgroup");
   static constexpr int kQBytes = N * D;                     // one of two buffers
   static constexpr int kPBytes = N * kKvTile;               // one of W
-  static constexpr int kJoinRows = RT <= 8 ? RT : RT / 2;   // rows joined at a time, over the P buffers
+  static constexpr int kJoinRows = RT <= 8 ? RR : RR / 2;   // rows joined at a time, over the P buffers
   static constexpr int kJoinBytes = W * kJoinRows * D * 4;
   static constexpr int kPRegion = W * kPBytes > kJoinBytes ? W * kPBytes : kJoinBytes;
   static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
@@ -369,7 +381,17 @@ struct AttendCfg {
   static constexpr int kRun = T == 3 ? 8 : 4;
 };
 
+// What a producer says of a stage. Of the 4-bit cache, the scales of each token
+// (bf16 bits; 0 where there is none, or none that a row sees).
+template <class C, bool FOUR = C::kFour>
 struct StageMeta {
+  alignas(16) uint16_t ks[C::kTokens];
+  alignas(16) uint16_t vs[C::kTokens];
+  int32_t base[C::kSlots];
+  float vmax;
+};
+template <class C>
+struct StageMeta<C, false> {
   int32_t base[kKvMaxSlots];  // position of the slot's first token, kKvNoToken if none
   float ks[kKvMaxSlots];      // key scale
   float vs[kKvMaxSlots];      // value scale (0: no block)
@@ -390,14 +412,14 @@ struct ItemInfo {
 template <class C>
 struct AttendShared {
   ItemInfo<C::RT> item[2];
-  StageMeta meta[C::kStages];
+  StageMeta<C> meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
   alignas(16) float spread[C::W][4];         // per-warp: the largest value scale over its tokens' smallest (log2)
   // References and factors of what was summed, where they move (all warps write the
   // same); at an item's end, references or the largest scores, if these are above.
   alignas(16) float moved[C::W][C::RT], alpha[C::W][C::RT];
   alignas(16) float ml[2][C::W][C::RT];  // the warpgroups' references (then weights) and sums
-  float mx[C::RT], sum[C::RT], inv[C::RT];  // joined, 1 / sum
+  float mx[C::RR], sum[C::RR], inv[C::RR];  // joined, 1 / sum
   alignas(16) int32_t poison[128];  // first position whose value code is NaN, per dimension
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
@@ -427,6 +449,28 @@ __device__ __forceinline__ void step(Walk& w, int part, int tiles, int heads, in
     }
     skip_cost(w);
   }
+}
+
+// bf16 scales of consecutive tokens: the last `n` (or all) made 0; the largest
+// (NaN counts as nothing).
+template <class V>
+__device__ __forceinline__ void drop_last(V& v, int n) {
+  uint32_t* const w = reinterpret_cast<uint32_t*>(&v);
+  constexpr int kWords = sizeof(V) / 4;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int left = 2 * kWords - n - 2 * i;  // of this word's two
+    w[i] = left >= 2 ? w[i] : left == 1 ? w[i] & 0xFFFFu : 0u;
+  }
+}
+template <class V>
+__device__ __forceinline__ float largest_scale(const V& v) {
+  const uint32_t* const w = reinterpret_cast<const uint32_t*>(&v);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(V) / 4); ++i)
+    m = fmaxf(m, fmaxf(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+  return m;
 }
 
 // ------------------------------------------------------------------ producer
@@ -477,14 +521,32 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         blk = page = -1;
       }
       float ks = 0.0f, vs = 0.0f;
-      if (page >= 0) {
+      if (!C::kFour && page >= 0) {
         ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
         vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
       }
       const int z = page >= 0 ? page : a.c.n_pages;  // no block: reads past the last page give zeros
       const int base = page >= 0 ? blk * a.c.block : kKvNoToken;
       const int tiles = min(per_batch, own - k0);
-      const int y = uniform(w.h * a.c.block), slab = a.c.block * C::D;
+      const int y = uniform(w.h * a.c.block / C::PAR), slab = a.c.block * C::HD;
+      // The scales of a lane's 4 (or 8) tokens of tile i, asked for a tile ahead.
+      using Scales = typename std::conditional<C::PAR == 2, uint4, uint2>::type;
+      Scales next_k{}, next_v{};
+      auto scales = [&](int i) {
+        const int t = lane * 4 * C::PAR, from = i * spt + t / a.c.block, in_block = t & (a.c.block - 1);
+        const int of = __shfl_sync(0xFFFFFFFFu, page, from & 31), at = __shfl_sync(0xFFFFFFFFu, base, from & 31);
+        next_k = next_v = Scales{};
+        if (i >= tiles || of < 0) return;
+        const int64_t row = (static_cast<int64_t>(of) * a.c.Hkv + w.h) * a.c.block + in_block;
+        next_k = load_global(reinterpret_cast<const Scales*>(a.c.k_scale4 + row));
+        next_v = load_global(reinterpret_cast<const Scales*>(a.c.v_scale4 + row));
+        const int over = at + in_block + 4 * C::PAR - keys;  // tokens that no row sees
+        if (over > 0) {
+          drop_last(next_k, over);
+          drop_last(next_v, over);
+        }
+      };
+      if (C::kFour) scales(0);
       for (int i = 0; i < tiles; ++i) {
         const uint32_t g = uniform(g0 + first + (k0 + i) * W);
         const uint32_t st = g % C::kStages;
@@ -493,22 +555,44 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         uint8_t* const k_at = ring + st * C::kStageBytes;
-        if (elect_one()) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
-        for (int j = 0; j < spt; ++j) {
-          const int zj = __shfl_sync(0xFFFFFFFFu, z, i * spt + j);
-          if (elect_one()) {
-            tma_load_3d(k_at + j * slab, tm_k, 0, y, zj, &s.full[st]);
-            tma_load_3d(k_at + kKvTile * C::D + j * slab, tm_v, 0, y, zj, &s.full[st]);
+        if constexpr (C::kFour) {
+          // A block that is not there is not loaded: whatever bits stand there are
+          // finite codes, and their probabilities 0. Bytes count as they are packed.
+          const uint32_t there = __ballot_sync(0xFFFFFFFFu, my_k == i && page >= 0);
+          if (elect_one()) mbar_arrive_expect_tx(&s.full[st], __popc(there) * slab);
+          for (int j = 0; j < spt; ++j) {
+            const int zj = __shfl_sync(0xFFFFFFFFu, z, i * spt + j);
+            if ((there >> (i * spt + j) & 1) && elect_one()) {
+              tma_load_3d(k_at + j * slab, tm_k, 0, y, zj, &s.full[st]);
+              tma_load_3d(k_at + kKvTile * C::D + j * slab, tm_v, 0, y, zj, &s.full[st]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        float vmax = vs;
-        for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
-        if (my_k == i) {
-          if (my_slot == 0) s.meta[st].vmax = vmax;
-          s.meta[st].base[my_slot] = base;
-          s.meta[st].ks[my_slot] = ks;
-          s.meta[st].vs[my_slot] = vs;
+          StageMeta<C>& meta = s.meta[st];
+          *reinterpret_cast<Scales*>(meta.ks + lane * 4 * C::PAR) = next_k;
+          *reinterpret_cast<Scales*>(meta.vs + lane * 4 * C::PAR) = next_v;
+          const float vmax = warp_max(largest_scale(next_v));
+          if (lane == 0) meta.vmax = vmax;
+          if (my_k == i) meta.base[my_slot] = base;
+          scales(i + 1);
+        } else {
+          if (elect_one()) mbar_arrive_expect_tx(&s.full[st], C::kStageBytes);
+          for (int j = 0; j < spt; ++j) {
+            const int zj = __shfl_sync(0xFFFFFFFFu, z, i * spt + j);
+            if (elect_one()) {
+              tma_load_3d(k_at + j * slab, tm_k, 0, y, zj, &s.full[st]);
+              tma_load_3d(k_at + kKvTile * C::D + j * slab, tm_v, 0, y, zj, &s.full[st]);
+            }
+            __syncwarp();
+          }
+          float vmax = vs;
+          for (int d = 1; d < spt; d *= 2) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, d));
+          if (my_k == i) {
+            if (my_slot == 0) s.meta[st].vmax = vmax;
+            s.meta[st].base[my_slot] = base;
+            s.meta[st].ks[my_slot] = ks;
+            s.meta[st].vs[my_slot] = vs;
+          }
         }
         last_g[last % (C::kStages / W)] = g;
         ++last;
@@ -544,16 +628,20 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
   int64_t row_at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int r = r0 + k * step, j = a.qt > 1 ? r / a.R : 0, head = h * a.R + (r - j * a.R);
+    // Of two tokens in an operand row, column r + RR has the row's elements for
+    // the second, and zeros for the first.
+    const int half = C::PAR == 2 && r0 + k * step >= C::RR ? 1 : 0;
+    const int r = r0 + k * step - half * C::RR, j = a.qt > 1 ? r / a.R : 0, head = h * a.R + (r - j * a.R);
     const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
     row_pos[k] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
     row_at[k] = r < rows && en.j0 + j < a.n ? (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + head : -1;
+    const int element = lane * kPer - half * C::HD;
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) u[k][e] = 0;
-    if (there) {
+    if (there && (C::PAR == 1 || (element >= 0 && element < C::HD))) {
       const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
                                   static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
-                                  lane * kPer;
+                                  element;
       if (kPer == 4) {
         const uint2 v = load_global(reinterpret_cast<const uint2*>(src));
         u[k][0] = v.x;
@@ -698,6 +786,11 @@ __device__ __noinline__ void clean_value_row(uint8_t* v_row_base, int t, int pos
   }
 }
 
+// A value of every dimension is NaN at position `pos` (a rare one).
+static __device__ __noinline__ void poison_all(int32_t* poison, int pos) {
+  for (int d = 0; d < 128; ++d) atomicMin(&poison[d], pos);
+}
+
 // The columns of RT rows at `taddr`, their T terms added, each 1/16 of the one
 // before it (of three terms of a probability, the second 1/8), a few rows at a
 // time (the terms of all would not fit in registers beside the softmax state).
@@ -745,7 +838,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
   uint8_t* const p_buf = p_smem + wg * C::kPBytes;
   const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem), p_addr = smem_u32(p_buf);
-  const int my_slot = t / a.c.block, my_off = t - my_slot * a.c.block;
+  const int my_slot = t * C::PAR / a.c.block, my_off = t * C::PAR - my_slot * a.c.block;
   uint32_t g0 = 0;      // tiles of the CTA before this item
   uint32_t phase = 0;   // of this warpgroup's score barrier
   uint32_t last_st = 0, last_turn = 0;  // stage of the last tile, and its phase
@@ -761,7 +854,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     const uint64_t qa = smem_desc_rows<D>(q_addr + buf * C::kQBytes);
     if (leader) {
 #pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(tm_s, ka + ks * 2, qa + ks * 2, idesc_f8(N, false), ks > 0);
+      for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(tm_s, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, C::kFour), ks > 0);
       mma_commit(&s.s_bar[wg]);
     }
     __syncwarp();
@@ -842,12 +935,27 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       // The load (for its description) and the scores, asked for together.
       const bool there = mbar_test(&s.full[st], turn), scored = mbar_test(&s.s_bar[wg], phase);
       if (!there && !wait_or_stop(&s.full[st], turn, &s.stop, a.status)) bad = true;
-      const StageMeta& meta = s.meta[st];
-      const int pos = meta.base[my_slot] + my_off;
-      const float k_mul = meta.ks[my_slot], v_scale = meta.vs[my_slot];
-      const bool masks = pos > lo_pos;
-      if (masks)
-        clean_value_row<D>(ring + st * C::kStageBytes + kKvTile * D, t, pos, pos > hi_pos, s.poison);
+      const StageMeta<C>& meta = s.meta[st];
+      const int pos = meta.base[my_slot] + my_off;  // of the thread's token, or the first of its two
+      float k_mul[C::PAR], v_scale[C::PAR];
+      const bool masks = pos + C::PAR - 1 > lo_pos;
+      if constexpr (C::kFour) {
+#pragma unroll
+        for (int i2 = 0; i2 < C::PAR; ++i2) {
+          k_mul[i2] = __uint_as_float(static_cast<uint32_t>(meta.ks[t * C::PAR + i2]) << 16);
+          v_scale[i2] = __uint_as_float(static_cast<uint32_t>(meta.vs[t * C::PAR + i2]) << 16);
+          // A NaN scale is kept from the rows that do not see its token; those that do get NaN at the end.
+          if (isnan(v_scale[i2])) {
+            v_scale[i2] = 0.0f;
+            poison_all(s.poison, pos + i2);
+          }
+        }
+      } else {
+        k_mul[0] = meta.ks[my_slot];
+        v_scale[0] = meta.vs[my_slot];
+        if (masks)
+          clean_value_row<D>(ring + st * C::kStageBytes + kKvTile * D, t, pos, pos > hi_pos, s.poison);
+      }
       if (!scored && !wait_or_stop(&s.s_bar[wg], phase, &s.stop, a.status)) bad = true;
       phase ^= 1;
       __syncwarp();
@@ -858,38 +966,51 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         tmem_rows<C, false>(tm_s + lane_addr, e);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
-          const F2 f = f2(info.row_mul[r], info.row_mul[r + 1]) * f2(k_mul, k_mul);
+          const float km = k_mul[r / C::RR];
+          const F2 f = f2(info.row_mul[r], info.row_mul[r + 1]) * f2(km, km);
           const F2 base = relative ? f2(-m[r], -m[r + 1]) : f2(0.0f, 0.0f);
           f2_get(fma2(f2(e[r], e[r + 1]), f, base), e[r], e[r + 1]);
         }
         if (masks) {
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            if (pos > info.row_pos[r]) e[r] = kNegInf;
+            if (pos + r / C::RR > info.row_pos[r]) e[r] = kNegInf;
         }
       };
       scores(true);
       tc_fence_before_sync();
-      float top = kNegInf;
+      bool vote = --rest == 0;
+      float v_mul[C::PAR];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) top = fmaxf(top, e[r]);
-      float v_mul = v_scale * inv_vref;
-      const bool due = --rest == 0;
-      if (bar_any(1 + wg, 128, due || top + fmaxf(log2_approx(v_mul), 7.0f - kRange) > kMaxCode ||
-                                   (vref == 0.0f && v_scale > 0.0f))) {
+      for (int i2 = 0; i2 < C::PAR; ++i2) {
+        float top = kNegInf;
+#pragma unroll
+        for (int r = 0; r < C::RR; ++r) top = fmaxf(top, e[i2 * C::RR + r]);
+        v_mul[i2] = v_scale[i2] * inv_vref;
+        vote = vote || top + fmaxf(log2_approx(v_mul[i2]), 7.0f - kRange) > kMaxCode ||
+               (vref == 0.0f && v_scale[i2] > 0.0f);
+      }
+      if (bar_any(1 + wg, 128, vote)) {
         // Each row's largest weight in this tile: a score plus its value scale's
         // logarithm. (Scores alone where they may pass 2^24, products of two
-        // codes being below 2^17.7: they have no steps below 1 then.)
+        // codes being below 2^17.7, of a 4-bit code 2^11.4: they have no steps below 1 then.)
         scores(false);
         const float vnow = fmaxf(vref, meta.vmax);
-        const float mul = warp_max(lane < RT ? fabsf(info.row_mul[lane]) : 0.0f) * k_mul;
-        const float lv = mul < 0.5f ? fmaxf(log2_approx(v_scale) - log2_approx(vnow), -kRange) : 0.0f;
+        const float mul = warp_max(lane < RT ? fabsf(info.row_mul[lane]) : 0.0f);
+        float lv[C::PAR], far = 0.0f, top = kNegInf;
+#pragma unroll
+        for (int i2 = 0; i2 < C::PAR; ++i2) {
+          lv[i2] = mul * k_mul[i2] < (C::kFour ? 32.0f : 0.5f)
+                       ? fmaxf(log2_approx(v_scale[i2]) - log2_approx(vnow), -kRange)
+                       : 0.0f;
+          if (v_scale[i2] > 0.0f) far = fmaxf(far, -lv[i2]);
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float v = warp_max(e[r] + lv);
+          const float v = warp_max(e[r] + lv[r / C::RR]);
           if (lane == r) top = v;
         }
-        const float spread = warp_max(v_scale > 0.0f ? -lv : 0.0f);
+        const float spread = warp_max(far);
         if (lane < RT) s.red[wg][lane][warp] = top;
         if (lane == 0) s.spread[wg][warp] = spread;
         tc_fence_before_sync();
@@ -924,7 +1045,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           }
           vref = vnow;
           inv_vref = vref > 0.0f ? __fdividef(kProbScale, vref) : 0.0f;
-          v_mul = v_scale * inv_vref;
+#pragma unroll
+          for (int i2 = 0; i2 < C::PAR; ++i2) v_mul[i2] = v_scale[i2] * inv_vref;
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) e[r] -= m[r];
@@ -944,7 +1066,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         float p0 = exp2_approx(e[r]), p1 = exp2_approx(e[r + 1]);
         F2 p = f2(p0, p1);
         f2_get(f2(l[r], l[r + 1]) + p, l[r], l[r + 1]);
-        F2 y = p * f2(v_mul, v_mul);
+        F2 y = p * f2(v_mul[r / C::RR], v_mul[r / C::RR]);
 #pragma unroll
         for (int term = 0; term < C::T; ++term) {
           f2_get(y, p0, p1);
@@ -989,7 +1111,8 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < kKvTile / 32; ++ks)
-            mma_f8_ss(tm_o, va + ks * (32 * D / 16), pa + ks * (512 / 16), idesc_f8(N, true), ks > 0 ? 1u : add);
+            mma_f8_ss(tm_o, va + ks * (32 * D / 16), pa + ks * (512 / 16), idesc_f8(N, true, C::kFour),
+                      ks > 0 ? 1u : add);
           mma_commit(&s.empty[st]);
         }
         __syncwarp();
@@ -1028,17 +1151,21 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     // Then the common reference, and each warpgroup's weight against it. (At least
     // the largest score: sums are large where a reference went below it.)
     if (t < RT) {
-      float mx = s.moved[0][t];
+      float mx = kNegInf;
 #pragma unroll
-      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s.moved[w][t]);
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int c = 0; c < RT; c += C::RR) mx = fmaxf(mx, s.moved[w][c + t % C::RR]);
       s.ml[1][wg][t] = exp2_approx(s.ml[0][wg][t] - mx);
-      if (wg == 0) {
+      if (wg == 0 && t < C::RR) {
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(s.red[w][t]);
-          sum += ((v.x + v.y) + (v.z + v.w)) * exp2_approx(s.ml[0][w][t] - mx);
-        }
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int c = 0; c < RT; c += C::RR) {
+            const float4 v = *reinterpret_cast<const float4*>(s.red[w][c + t]);
+            sum += ((v.x + v.y) + (v.z + v.w)) * exp2_approx(s.ml[0][w][c + t] - mx);
+          }
         s.mx[t] = mx;
         s.sum[t] = sum;
         s.inv[t] = __fdividef(1.0f, sum);
@@ -1048,24 +1175,32 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     float* const join = reinterpret_cast<float*>(p_smem);
     const int rows = info.rows, part = info.slot;
 #pragma unroll
-    for (int r0 = 0; r0 < RT; r0 += C::kJoinRows) {
+    for (int r0 = 0; r0 < C::RR; r0 += C::kJoinRows) {
       if (r0 > 0) bar_sync(8, kAll);
       if (t < D) {
+        // Of two tokens in an operand row, each half of the lanes has one's dimensions.
+        const bool second = C::PAR == 2 && t >= C::HD;
 #pragma unroll
-        for (int r = 0; r < C::kJoinRows; ++r)
-          join[(wg * C::kJoinRows + r) * D + t] = o[r0 + r] * s.ml[1][wg][r0 + r] * (vref * (1.0f / kProbScale));
+        for (int r = 0; r < C::kJoinRows; ++r) {
+          const float x = second ? o[RT - C::RR + r0 + r] : o[r0 + r];
+          join[(wg * C::kJoinRows + r) * D + t] =
+              x * s.ml[1][wg][r0 + r + (second ? C::RR : 0)] * (vref * (1.0f / kProbScale));
+        }
       }
       bar_sync(8, kAll);
       // Four dimensions of a row a thread.
-      for (int c = threadIdx.x; c < C::kJoinRows * (D / 4); c += kAll) {
-        const int row = c / (D / 4), r = r0 + row, d = c % (D / 4) * 4;
+      for (int c = threadIdx.x; c < C::kJoinRows * (C::HD / 4); c += kAll) {
+        const int row = c / (C::HD / 4), r = r0 + row, d = c % (C::HD / 4) * 4;
         if (r >= rows) break;
         float4 v = *reinterpret_cast<const float4*>(&join[row * D + d]);
 #pragma unroll
-        for (int w = 1; w < W; ++w) {
-          const float4 u = *reinterpret_cast<const float4*>(&join[(w * C::kJoinRows + row) * D + d]);
-          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int half = 0; half < D; half += C::HD) {
+            if (w == 0 && half == 0) continue;
+            const float4 u = *reinterpret_cast<const float4*>(&join[(w * C::kJoinRows + row) * D + half + d]);
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+          }
         const int4 bad_from = *reinterpret_cast<const int4*>(&s.poison[d]);
         const int row_pos = info.row_pos[r];
         const int64_t at = info.row_at[r];
@@ -1078,7 +1213,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
           float* const to = part_row(a, part, rows, r);
           *reinterpret_cast<float2*>(to + d) = make_float2(v.x, v.y);
           *reinterpret_cast<float2*>(to + d + 2) = make_float2(v.z, v.w);
-          if (d == 0) *reinterpret_cast<float2*>(to + D) = row_pos < 0 ? make_float2(kUnset, 0.0f) : make_float2(mx, sum);
+          if (d == 0) *reinterpret_cast<float2*>(to + C::HD) = row_pos < 0 ? make_float2(kUnset, 0.0f) : make_float2(mx, sum);
         } else if (at >= 0) {
           const bool none = row_pos < 0 || sum == 0.0f;
           v = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
@@ -1090,7 +1225,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
             const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
             packed = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
           }
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + d) = packed;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * C::HD + d) = packed;
           if (a.lse && d == 0) a.lse[at] = none ? kNegInf : mx * 0.6931471805599453f + logf(sum);
         }
       }
@@ -1275,10 +1410,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 }
 
 // Launch with the given tensor maps on the current device; grid CTAs.
-template <int D, int RT, int T>
+template <int D, int RT, int T, bool FOUR = false>
 cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid, int device,
                         cudaStream_t stream) {
-  using C = AttendCfg<D, RT, T>;
+  using C = AttendCfg<D, RT, T, FOUR>;
   constexpr int smem = 1024 + C::kStages * C::kStageBytes + 2 * C::kQBytes + C::kPRegion +
                        static_cast<int>(sizeof(AttendShared<C>));
   static_assert(smem <= 227 * 1024, "shared memory");
@@ -1294,15 +1429,20 @@ cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const Atte
   return launch_pdl(kv_attend_kernel<C>, dim3(grid), dim3(C::kThreads), smem, stream, tk, tv, a);
 }
 
+// The tensor map of the 4-bit cache's keys or values (kv_attend.cu).
+bool encode_cache_map4(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c);
+
 // All row counts of one head size and term count (kv_attend_d*_t*.cu).
-template <int D, int T>
+template <int D, int T, bool FOUR = false>
 cudaError_t attend_rows(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a, int grid,
                         int device, cudaStream_t stream) {
   switch (rt) {
-    case 4: return attend_form<D, 4, T>(tk, tv, a, grid, device, stream);
-    case 8: return attend_form<D, 8, T>(tk, tv, a, grid, device, stream);
-    case 16: return attend_form<D, 16, T>(tk, tv, a, grid, device, stream);
-    default: return attend_form<D, 32, T>(tk, tv, a, grid, device, stream);
+    case 4:
+      // (Of the 4-bit cache's 64 dimensions a row has two columns.)
+      if constexpr (!FOUR || D == 128) return attend_form<D, 4, T, FOUR>(tk, tv, a, grid, device, stream);
+    case 8: return attend_form<D, 8, T, FOUR>(tk, tv, a, grid, device, stream);
+    case 16: return attend_form<D, 16, T, FOUR>(tk, tv, a, grid, device, stream);
+    default: return attend_form<D, 32, T, FOUR>(tk, tv, a, grid, device, stream);
   }
 }
 using AttendLaunch = cudaError_t (*)(int rt, const CUtensorMap& tk, const CUtensorMap& tv, const AttendArgs& a,
@@ -1311,5 +1451,9 @@ cudaError_t attend_d64_t2(int, const CUtensorMap&, const CUtensorMap&, const Att
 cudaError_t attend_d64_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
 cudaError_t attend_d128_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
 cudaError_t attend_d128_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend4_d64_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend4_d64_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend4_d128_t2(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
+cudaError_t attend4_d128_t3(int, const CUtensorMap&, const CUtensorMap&, const AttendArgs&, int, int, cudaStream_t);
 
 }  // namespace qsa

@@ -42,6 +42,7 @@
 // 585 TFLOP/s, bf16 749 us.
 #pragma once
 
+#include "kv4_codes.cuh"
 #include "kv_attend_kernel.cuh"
 
 namespace qsa {
@@ -60,7 +61,19 @@ constexpr float kManyScale = 64.0f;  // of a probability 1 at the largest value 
 // its warpgroup has done with the last one's.
 __host__ __device__ constexpr int many_buffers(int D) { return (512 - 2 * D) / 128; }
 
-struct ManyMeta {
+// Of the 4-bit cache the scales of 16 tokens are a power of two common to them
+// (ks, vs; their largest scale is 2^12 to 2^13 of it) times one for each token in
+// fp16 (kt, vt), with which the converted codes are multiplied: exact, as a scale
+// has 8 bits and a code 2, but for scales below 2^-20 of the largest of the 16.
+template <bool FOUR>
+struct TokenScales {};
+template <>
+struct TokenScales<true> {
+  alignas(16) uint16_t kt[kKvTile], vt[kKvTile];
+};
+
+template <bool FOUR>
+struct ManyMeta : TokenScales<FOUR> {
   alignas(16) float ks[8], vs[8];  // key and value scales of 16 tokens each
   alignas(16) float lv[8];         // log2 of the value scales against vmax, -kRange at least
   alignas(16) int32_t page[8];     // -1: no block
@@ -69,9 +82,9 @@ struct ManyMeta {
                                    // scale is below 2^-kManyNear of vmax
 };
 
-template <int D>
+template <int D, bool FOUR>
 struct ManyShared {
-  ManyMeta meta[kManyRing];
+  ManyMeta<FOUR> meta[kManyRing];
   alignas(16) int32_t poison[kManyRing][D];  // of item i in i % kManyRing: first position with a NaN value code
   int32_t poisoned[kManyRing];
   float row_mul[2][kManyRows];
@@ -171,9 +184,22 @@ __device__ __forceinline__ bool many_active(const AttendArgs& a, const Entry& en
 }
 
 // ------------------------------------------------------------ pages, scales
+// The common power of two of 16 bf16 scales, which become fp16 multiples of it
+// (NaN stays NaN). 0: there is none, all are 0.
+__device__ __forceinline__ float share_scale(uint4 (&v)[2]) {
+  const float top = fmaxf(largest_scale(v[0]), largest_scale(v[1]));
+  const float common = __uint_as_float(max(static_cast<int>(__float_as_uint(top) & 0x7F800000u) - (12 << 23), 1 << 23));
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(common));
+  uint32_t* const w = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = half2_of(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
+  return top == 0.0f ? 0.0f : common;
+}
+
 // One warp; lane i (of 8) looks up tokens 16 i .. of a tile.
-template <int D>
-__device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& start) {
+template <int D, bool FOUR>
+__device__ void many_lookup(const AttendArgs& a, ManyShared<D, FOUR>& s, const Start& start) {
   const int lane = threadIdx.x % 32, i = lane % 8;
   uint32_t g = 0;
   bool bad = false;
@@ -193,9 +219,31 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
         }
       }
       float ks = 0.0f, vs = 0.0f;
-      if (page >= 0) {
-        ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
-        vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+      uint4 kt[2] = {}, vt[2] = {};
+      if constexpr (FOUR) {
+        if (page >= 0) {
+          const int pos = ((w.t + t) * 8 + i) * 16;
+          const int64_t row = (static_cast<int64_t>(page) * a.c.Hkv + w.h) * a.c.block + (pos & (a.c.block - 1));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            kt[x] = load_global(reinterpret_cast<const uint4*>(a.c.k_scale4 + row) + x);
+            vt[x] = load_global(reinterpret_cast<const uint4*>(a.c.v_scale4 + row) + x);
+          }
+          const int over = pos + 15 - en.last_pos;  // tokens that no row sees
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (over > 8 - 8 * x) {
+              drop_last(kt[x], over - (8 - 8 * x));
+              drop_last(vt[x], over - (8 - 8 * x));
+            }
+          ks = share_scale(kt);
+          vs = share_scale(vt);
+        }
+      } else {
+        if (page >= 0) {
+          ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+          vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+        }
       }
       const float vnow = fmaxf(vmax, warp_max(vs)), lnow = log2_approx(vnow);
       const float lv = fmaxf(log2_approx(vs) - lnow, -kRange);
@@ -207,8 +255,15 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D>& s, const Start& 
       const uint32_t at = g % kManyRing;
       if (g >= kManyRing) wait_or_stop(&s.meta_empty[at], (g / kManyRing + 1) & 1, &s.stop, a.status);
       __syncwarp();
-      ManyMeta& m = s.meta[at];
+      ManyMeta<FOUR>& m = s.meta[at];
       if (lane < 8) {
+        if constexpr (FOUR) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            reinterpret_cast<uint4*>(m.kt)[2 * i + x] = kt[x];
+            reinterpret_cast<uint4*>(m.vt)[2 * i + x] = vt[x];
+          }
+        }
         m.ks[i] = ks;
         m.vs[i] = vs;
         m.lv[i] = lv;
@@ -253,11 +308,27 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
+// 16 4-bit codes times their token's scale (two halves of it) to 16 halves.
+__device__ __forceinline__ void convert16(uint8_t* tile, uint32_t off, const uint2& codes, uint32_t scale) {
+  const __half2 s = *reinterpret_cast<const __half2*>(&scale);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[4];
+    e2m1x8_to_half2(i == 0 ? codes.x : codes.y, h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), s);
+      h[e] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    *reinterpret_cast<uint4*>(tile + swizzled<128>(off + 16 * i)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
 // Four warps. A thread takes the same 16 dimensions of kPasses tokens: loads of
 // a tile's values go out before its keys are converted, and of the next tile's
 // keys before its values are.
-template <int D, bool BF16>
-__device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16, uint8_t* v16, const Start& start) {
+template <int D, bool BF16, bool FOUR>
+__device__ void many_convert(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* k16, uint8_t* v16, const Start& start) {
   constexpr int kPer = D / 16;                 // threads of a token
   constexpr int kPasses = kKvTile * kPer / 128;
   constexpr int kBytes = kKvTile * D * 2;
@@ -267,16 +338,17 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
   const int row0 = D == 128 ? warp * 4 + ((lane >> 2) & 3) : warp * 8 + (lane >> 2);
   const uint32_t off0 = (c / 4) * (kKvTile * 128) + row0 * 128 + (c % 4) * 32;
   uint32_t g = 0, it = 0;
-  uint4 key[kPasses], val[kPasses];
+  using Codes = typename std::conditional<FOUR, uint2, uint4>::type;  // of 16 elements
+  Codes key[kPasses], val[kPasses];
   // Unconditional, so that all of a tile's loads are in flight together: where
   // there is no block, page 0 (its scores are masked, its values made zero).
-  auto load = [&](const uint8_t* base, const ManyMeta& m, int h, uint4 (&to)[kPasses]) {
+  auto load = [&](const uint8_t* base, const ManyMeta<FOUR>& m, int h, Codes (&to)[kPasses]) {
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       const int row = row0 + p * (kKvTile / kPasses);
-      to[p] = load_global(reinterpret_cast<const uint4*>(
+      to[p] = load_global(reinterpret_cast<const Codes*>(
           base + max(m.page[row / 16], 0) * a.c.page_stride +
-          (static_cast<int64_t>(h) * a.c.block + (row & (a.c.block - 1))) * D + c * 16));
+          (static_cast<int64_t>(h) * a.c.block + (row & (a.c.block - 1))) * (FOUR ? D / 2 : D) + c * sizeof(Codes)));
     }
   };
   auto published = [&](uint64_t* bar) {
@@ -290,7 +362,7 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
     int32_t* const poison = s.poison[it % kManyRing];
     for (int i = 0; i < part; ++i, ++g) {
       const uint32_t at = g % kManyRing, buf = g & 1;
-      const ManyMeta& m = s.meta[at];
+      const ManyMeta<FOUR>& m = s.meta[at];
       if (i == 0) {  // the keys of an item's first tile were not asked for ahead
         wait_or_stop(&s.meta_full[at], (g / kManyRing) & 1, &s.stop, a.status);
         // The lookup of this tile waited for the item that had this poison before.
@@ -302,8 +374,15 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
       load(a.c.v, m, w.h, val);
       if (g >= 2) wait_or_stop(&s.k_empty[buf], ((g >> 1) + 1) & 1, &s.stop, a.status);
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p)
-        convert16<BF16>(k16 + buf * kBytes, off0 + p * (kKvTile / kPasses) * 128, key[p]);
+      for (int p = 0; p < kPasses; ++p) {
+        const uint32_t off = off0 + p * (kKvTile / kPasses) * 128;
+        if constexpr (FOUR) {
+          const uint32_t scale = m.kt[row0 + p * (kKvTile / kPasses)];
+          convert16(k16 + buf * kBytes, off, key[p], scale | scale << 16);
+        } else {
+          convert16<BF16>(k16 + buf * kBytes, off, key[p]);
+        }
+      }
       published(&s.k_full[buf]);
       if (i + 1 < part) {
         const uint32_t next = (g + 1) % kManyRing;
@@ -313,13 +392,27 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
       // Values that no row sees are zeros, so that 0 times them is 0; NaN codes
       // that some rows see are zeros too, and noted for the rows that do.
       const int pos0 = (w.t + i) * kKvTile;
-      if (pos0 + kKvTile - 1 > lo_pos || m.holes != 0) {
+      uint32_t scale[FOUR ? kPasses : 1] = {};
+      if constexpr (FOUR) {
+        // A NaN scale that some rows do not see is made 0, and noted for those
+        // that do. (Where no row sees a token its scale is 0 already.)
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+          const int row = row0 + p * (kKvTile / kPasses);
+          scale[p] = m.vt[row];
+          if ((scale[p] & 0x7FFFu) > 0x7C00u && pos0 + row > lo_pos) {
+            scale[p] = 0;
+            s.poisoned[it % kManyRing] = 1;
+            for (int e = 0; e < 16; ++e) atomicMin(&poison[c * 16 + e], pos0 + row);
+          }
+        }
+      } else if (pos0 + kKvTile - 1 > lo_pos || m.holes != 0) {
         uint32_t hits = 0;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
           const int pos = pos0 + row0 + p * (kKvTile / kPasses);
-          uint4& u = val[p];
-          if (pos > hi_pos || m.page[(pos - pos0) / 16] < 0) u = make_uint4(0, 0, 0, 0);
+          Codes& u = val[p];
+          if (pos > hi_pos || m.page[(pos - pos0) / 16] < 0) u = Codes{};
           if (pos > lo_pos && (nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w))) hits |= 1u << p;
         }
         if (hits) s.poisoned[it % kManyRing] = 1;
@@ -343,8 +436,11 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
       }
       if (g >= 2) wait_or_stop(&s.v_empty[buf], ((g >> 1) + 1) & 1, &s.stop, a.status);
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p)
-        convert16<false>(v16 + buf * kBytes, off0 + p * (kKvTile / kPasses) * 128, val[p]);
+      for (int p = 0; p < kPasses; ++p) {
+        const uint32_t off = off0 + p * (kKvTile / kPasses) * 128;
+        if constexpr (FOUR) convert16(v16 + buf * kBytes, off, val[p], scale[p] | scale[p] << 16);
+        else convert16<false>(v16 + buf * kBytes, off, val[p]);
+      }
       published(&s.v_full[buf]);
       if (lane == 0) mbar_arrive(&s.meta_empty[at]);
     }
@@ -358,8 +454,8 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D>& s, uint8_t* k16
 // Whatever the two warpgroups begin with, one then has its products while the
 // other has the exponentials. (With a warp for each row tile both
 // fell into step: 8,600 cycles a tile instead of 7,700, at that time.)
-template <int D, bool BF16>
-__device__ void many_products(const AttendArgs& a, ManyShared<D>& s, uint32_t q_addr, uint32_t k_addr, uint32_t v_addr,
+template <int D, bool BF16, bool FOUR>
+__device__ void many_products(const AttendArgs& a, ManyShared<D, FOUR>& s, uint32_t q_addr, uint32_t k_addr, uint32_t v_addr,
                               const Start& start) {
   constexpr uint32_t kBytes = kKvTile * D * 2, kPanel = kKvTile * 128, kBuffers = many_buffers(D);
   const uint32_t tmem = uniform(s.tmem), tm_out = tmem + kBuffers * 128;
@@ -384,7 +480,7 @@ __device__ void many_products(const AttendArgs& a, ManyShared<D>& s, uint32_t q_
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t step = ((ks / 4) * kPanel + (ks % 4) * 32) >> 4;
-            mma_f16_ss(tmem + at * 128, q_desc + step, k_desc + step, idesc_many(kKvTile, BF16, false), ks > 0);
+            mma_f16_ss(tmem + at * 128, q_desc + step, k_desc + step, idesc_many(kKvTile, BF16 && !FOUR, false), ks > 0);
           }
           mma_commit(&s.s_full[at]);
           mma_commit(&s.k_empty[buf]);
@@ -441,8 +537,8 @@ __device__ void many_products(const AttendArgs& a, ManyShared<D>& s, uint32_t q_
 //
 // Short code counts here and at an item's end: it runs once an item, and its
 // instructions come from a far cache, about 15 cycles each.
-template <int D, bool BF16>
-__device__ __forceinline__ void many_queries(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem, const Entry& en,
+template <int D, bool BF16, bool FOUR>
+__device__ __forceinline__ void many_queries(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* q_smem, const Entry& en,
                                              int h, int w, int j, int head) {
   constexpr int kLanes = D / 8, kEach = 32 / kLanes, kBatch = 8;  // lanes of a row, rows at a time, loads in flight
   const int lane = threadIdx.x % 32, c = lane % kLanes;
@@ -480,7 +576,7 @@ __device__ __forceinline__ void many_queries(const AttendArgs& a, ManyShared<D>&
           float lo = __uint_as_float(x[e] << 16) * inv, hi = __uint_as_float(x[e] & 0xFFFF0000u) * inv;
           lo = fmaf(lo, 0.0f, lo);
           hi = fmaf(hi, 0.0f, hi);
-          x[e] = bf162_of(lo, hi);
+          x[e] = FOUR ? half2_of(lo, hi) : bf162_of(lo, hi);
         }
         if (c == 0) s.row_mul[w][row0 + r] = t;
       } else {
@@ -552,8 +648,8 @@ __device__ __forceinline__ void many_probabilities(uint32_t taddr, float f0, flo
   if (!BF16) tmem_st16(taddr + 16, rest);
 }
 
-template <int D, bool BF16>
-__device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem, int w) {
+template <int D, bool BF16, bool FOUR>
+__device__ void many_rows(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* q_smem, int w) {
   const int warp = uniform(static_cast<int>(threadIdx.x / 32 % 4)), t = threadIdx.x % 128, lane = t % 32;
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
   constexpr uint32_t kBuffers = many_buffers(D);
@@ -587,7 +683,7 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
     asm volatile("" : "+f"(zero));
     __syncwarp();
     if (active) {
-      many_queries<D, BF16>(a, s, q_smem + w * (kKvTile * D * 2), en, wk.h, w, j, t < qt * a.R ? t - jt * a.R : -1);
+      many_queries<D, BF16, FOUR>(a, s, q_smem + w * (kKvTile * D * 2), en, wk.h, w, j, t < qt * a.R ? t - jt * a.R : -1);
       mul = fabsf(a.scale_log2) * (BF16 ? s.row_mul[w][t] : 1.0f);
     }
     for (int i = 0; i < part; ++i, ++g) {
@@ -599,7 +695,7 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[buf]);
       } else {
-        const ManyMeta& meta = s.meta[at];
+        const ManyMeta<FOUR>& meta = s.meta[at];
         const int pos0 = (wk.t + i) * kKvTile;
         const uint32_t holes = meta.holes;
         const bool masked = holes != 0 || pos0 + kKvTile - 1 > lo_pos;
@@ -790,14 +886,14 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D>& s, uint8_t* q_smem
 }
 
 // -------------------------------------------------------------- the kernel
-template <int D, bool BF16>
+template <int D, bool BF16, bool FOUR>
 __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ uint8_t raw[];
   constexpr int kBytes = kKvTile * D * 2;  // a tile of 16-bit rows
   uint8_t* const q_smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* const v16 = q_smem + 2 * kBytes;
   uint8_t* const k16 = v16 + 2 * kBytes;
-  ManyShared<D>& s = *reinterpret_cast<ManyShared<D>*>(k16 + 2 * kBytes);
+  ManyShared<D, FOUR>& s = *reinterpret_cast<ManyShared<D, FOUR>*>(k16 + 2 * kBytes);
   const int warp = threadIdx.x / 32;
 
   if (threadIdx.x == 0) {
@@ -824,7 +920,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
   // tensor memory (after the wait, and before later kernels may start: see
   // kv_attend_kernel), and the others enter their code.
   if (warp < 8) {
-    many_rows<D, BF16>(a, s, q_smem, warp / 4);
+    many_rows<D, BF16, FOUR>(a, s, q_smem, warp / 4);
   } else {
     if (warp < 12) {
       pdl_wait();
@@ -844,9 +940,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
     many_begin(s);
     const Start start = s.share.start;
     if (s.share.hi > s.share.lo) {
-      if (warp < 12) many_convert<D, BF16>(a, s, k16, v16, start);
-      else if (warp == 12) many_products<D, BF16>(a, s, smem_u32(q_smem), smem_u32(k16), smem_u32(v16), start);
-      else many_lookup<D>(a, s, start);
+      if (warp < 12) many_convert<D, BF16, FOUR>(a, s, k16, v16, start);
+      else if (warp == 12) many_products<D, BF16, FOUR>(a, s, smem_u32(q_smem), smem_u32(k16), smem_u32(v16), start);
+      else many_lookup<D, FOUR>(a, s, start);
     }
   }
   tc_fence_before_sync();

@@ -1,4 +1,4 @@
-// kv_internal.h - declarations shared by the paged 8-bit cache's kernels and
+// kv_internal.h - declarations shared by the paged caches' kernels and
 // the C-ABI layer, and the device helpers of its e4m3 codes and scales.
 #pragma once
 
@@ -20,6 +20,9 @@ struct KvCacheArgs {
   const int32_t* n_new;
   int64_t page_stride;
   int32_t n_pages, max_blocks, B, Hkv, block, D;
+  // The 4-bit cache's scales, one a token (k_scale and v_scale are null then).
+  uint16_t* k_scale4 = nullptr;
+  uint16_t* v_scale4 = nullptr;
 };
 
 // Rows [B, n, heads, D] of 16-bit floats, strides in elements.
@@ -37,10 +40,16 @@ struct KvAppendProblem {
   const float* sin;
   void* q_out;
   uint16_t* kb;
+  const int32_t* offset = nullptr;  // 4-bit cache only
 };
 // CTAs of the append, of which *units each own a (block, head, K or V).
 int64_t kv_append_grid(const KvAppendProblem& p, int64_t* units, int32_t* blocks_per_seq);
 cudaError_t launch_kv_append(const KvAppendProblem& p, const DeviceInfo& dev, cudaStream_t stream);
+int64_t kv4_append_grid(const KvAppendProblem& p, int64_t* units, int32_t* blocks_per_seq);
+cudaError_t launch_kv4_append(const KvAppendProblem& p, const DeviceInfo& dev, cudaStream_t stream);
+int64_t kv4_read_grid(const KvCacheArgs& c, int32_t n);
+cudaError_t launch_kv4_read(const KvCacheArgs& c, int32_t n, bool bf16, void* k, void* v, const DeviceInfo& dev,
+                            cudaStream_t stream);
 
 struct KvAttendProblem {
   KvCacheArgs cache;
@@ -57,6 +66,30 @@ struct KvAttendProblem {
 // 0 for sizes the attention does not take.
 size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream);
+size_t kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
+cudaError_t launch_kv4_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream);
+
+struct Kv4WeightsProblem {
+  KvCacheArgs cache;
+  KvRows q;
+  int32_t n, Hq;
+  bool bf16;
+  float scale, decay;
+  const float* lse;
+  float* weights;
+};
+cudaError_t launch_kv4_weights(const Kv4WeightsProblem& p, const DeviceInfo& dev, cudaStream_t stream);
+
+struct Kv4EvictProblem {
+  KvCacheArgs cache;
+  float* weights;
+  int32_t budget, sink, recent;
+  int32_t* lens_out;
+  int32_t* offset;
+  int32_t* list;  // [B, Hkv, budget]: where the tokens of an item's slots come from
+};
+size_t kv4_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t budget);
+cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cudaStream_t stream);
 
 constexpr int kKvMaxGroup = 32;             // query heads per KV head
 constexpr uint32_t kKvIndexBit = 1u << 5;   // kErrCacheIndex (qsa_device.cuh) for host code

@@ -163,6 +163,153 @@ void plan_add(const char* kernel) {
 }
 }  // namespace qsa
 
+// -------------------------------------------------------- the paged caches
+// Sizes of a cache and the batch; nothing is dereferenced but *c. `bits` of an
+// element, pages and their stride in units of `unit` bytes.
+template <class Cache>
+static qsa_status check_cache_sizes(const Cache* c, int32_t n, int bits, int unit) {
+  if (!c) return QSA_ERR_INVALID_ARG;
+  if (c->B < 0 || n < 0 || c->n_pages < 0 || c->max_blocks < 0 || c->Hkv < 1 || c->block < 1 || c->D < 1)
+    return QSA_ERR_INVALID_ARG;
+  if ((c->D != 64 && c->D != 128) ||
+      (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) || c->Hkv > 65535)
+    return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (static_cast<int64_t>(c->max_blocks) * c->block > (1 << 30) ||
+      static_cast<int64_t>(c->B) * n > 0x7FFFFFFFLL)
+    return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (c->page_stride < static_cast<int64_t>(c->Hkv) * c->block * c->D * bits / 8) return QSA_ERR_INVALID_ARG;
+  if (c->page_stride >= (1LL << 40)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (c->page_stride % unit != 0) return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+static qsa_status check_cache_sizes(const qsa_kv_cache* c, int32_t n) { return check_cache_sizes(c, n, 8, 16); }
+static qsa_status check_cache_sizes(const qsa_kv4_cache* c, int32_t n) { return check_cache_sizes(c, n, 4, 32); }
+
+// Codes on `unit` bytes, scales on `scale_unit`; values and their scales need
+// not be there where `values` is false.
+template <class Cache>
+static qsa_status check_cache_pointers(const Cache* c, uintptr_t unit, uintptr_t scale_unit, bool values) {
+  if (!c->lens || (c->max_blocks > 0 && !c->page_table)) return QSA_ERR_INVALID_ARG;
+  if (c->n_pages > 0 && (!c->k || !c->k_scale || (values && (!c->v || !c->v_scale)))) return QSA_ERR_INVALID_ARG;
+  if (!aligned(c->k, unit) || !aligned(c->v, unit) || !aligned(c->k_scale, scale_unit) ||
+      !aligned(c->v_scale, scale_unit) || !aligned(c->page_table, 4) || !aligned(c->lens, 4) || !aligned(c->n_new, 4))
+    return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+static qsa_status check_cache_pointers(const qsa_kv_cache* c) { return check_cache_pointers(c, 16, 4, true); }
+static qsa_status check_cache_pointers(const qsa_kv4_cache* c, bool values = true) {
+  return check_cache_pointers(c, 32, 16, values);
+}
+
+// Rows of 16-bit floats read by 16-byte loads.
+static qsa_status check_rows(const qsa_rows* r) {
+  if (!r || !r->data) return QSA_ERR_INVALID_ARG;
+  if (r->stride_b < 0 || r->stride_n < 0 || r->stride_h < 0) return QSA_ERR_INVALID_ARG;
+  if (!aligned(r->data, 16) || r->stride_b % 8 != 0 || r->stride_n % 8 != 0 || r->stride_h % 8 != 0)
+    return QSA_ERR_MISALIGNED;
+  return QSA_OK;
+}
+
+static qsa::KvCacheArgs cache_args(const qsa_kv_cache* c) {
+  return qsa::KvCacheArgs{c->k,     c->v,       c->k_scale,    c->v_scale, c->page_table, c->lens,
+                          c->n_new, c->page_stride, c->n_pages, c->max_blocks, c->B, c->Hkv,
+                          c->block, c->D};
+}
+static qsa::KvCacheArgs cache_args(const qsa_kv4_cache* c) {
+  return qsa::KvCacheArgs{c->k,     c->v,       nullptr,    nullptr, c->page_table, c->lens,
+                          c->n_new, c->page_stride, c->n_pages, c->max_blocks, c->B, c->Hkv,
+                          c->block, c->D,       c->k_scale, c->v_scale};
+}
+
+static qsa::KvRows row_args(const qsa_rows* r) {
+  return r ? qsa::KvRows{r->data, r->stride_b, r->stride_n, r->stride_h} : qsa::KvRows{nullptr, 0, 0, 0};
+}
+
+// Both appends: `grid` and `launch` are the cache's own.
+template <class Cache, class Grid, class Launch>
+static qsa_status run_append(const Cache* cache, const qsa_rows* k, const qsa_rows* v, const qsa_rows* q, int32_t n,
+                             int32_t Hq, qsa_dtype dtype, const float* cos, const float* sin, int32_t rot,
+                             int32_t max_pos, int32_t interleaved, const int32_t* offset, void* q_out, uint16_t* kb,
+                             qsa_stream_t stream, Grid grid, Launch launch) {
+  qsa_status st = check_cache_sizes(cache, n);
+  if (st != QSA_OK) return st;
+  if (rot < 0 || max_pos < 0 || (q && Hq < 1)) return QSA_ERR_INVALID_ARG;
+  if (dtype != QSA_F16 && dtype != QSA_BF16) return QSA_ERR_INVALID_ARG;
+  if (rot % 16 != 0 || rot > cache->D) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  qsa::KvAppendProblem p{};
+  p.cache = cache_args(cache);
+  p.q = row_args(q);
+  p.n = n;
+  p.Hq = q ? Hq : 0;
+  if (cache->B == 0 || n == 0) return QSA_OK;
+  int64_t units = 0;
+  int32_t per_seq = 0;
+  if (grid(p, &units, &per_seq) > 0x7FFFFFFFLL) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if ((st = check_rows(k)) != QSA_OK || (st = check_rows(v)) != QSA_OK) return st;
+  if (q && ((st = check_rows(q)) != QSA_OK)) return st;
+  if ((q != nullptr) != (q_out != nullptr)) return QSA_ERR_INVALID_ARG;
+  if (rot > 0 && (!cos || !sin)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(kb, 2) || !aligned(cos, 16) || !aligned(sin, 16) || !aligned(offset, 4))
+    return QSA_ERR_MISALIGNED;
+  p.k = row_args(k);
+  p.v = row_args(v);
+  p.rot = rot;
+  p.max_pos = max_pos;
+  p.bf16 = dtype == QSA_BF16;
+  p.interleaved = interleaved != 0;
+  p.cos = cos;
+  p.sin = sin;
+  p.q_out = q_out;
+  p.kb = kb;
+  p.offset = offset;
+  const DeviceInfo* dev = nullptr;
+  if ((st = device_or_error(&dev)) != QSA_OK) return st;
+  return from_cuda(launch(p, *dev, as_cuda(stream)));
+}
+
+// Both attentions; at most `group` query heads on a KV head.
+template <class Cache, class Bytes, class Launch>
+static qsa_status run_attend(const Cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                             float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, qsa_stream_t stream, int group, Bytes bytes,
+                             Launch launch) {
+  qsa_status st = check_cache_sizes(cache, n);
+  if (st != QSA_OK) return st;
+  if (Hq < 1 || (dtype != QSA_F16 && dtype != QSA_BF16)) return QSA_ERR_INVALID_ARG;
+  if (Hq % cache->Hkv != 0) return QSA_ERR_INVALID_ARG;
+  if (ids && (k < 1 || (n_lists != 1 && n_lists != cache->Hkv))) return QSA_ERR_INVALID_ARG;
+  if (Hq / cache->Hkv > group || (ids && k > (1 << 20))) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (cache->B == 0 || n == 0) return QSA_OK;
+  if (!(scale - scale == 0.0f)) return QSA_ERR_INVALID_ARG;
+  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
+  if ((st = check_rows(q)) != QSA_OK) return st;
+  if (!out || !workspace || workspace_bytes < bytes(cache->B, n, Hq, cache->Hkv, cache->D)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ids, 4) || !aligned(workspace, 16))
+    return QSA_ERR_MISALIGNED;
+  qsa::KvAttendProblem p{};
+  p.cache = cache_args(cache);
+  p.q = row_args(q);
+  p.n = n;
+  p.Hq = Hq;
+  p.bf16 = dtype == QSA_BF16;
+  p.scale = scale;
+  p.ids = ids;
+  p.n_lists = ids ? n_lists : 1;
+  p.k = ids ? k : 0;
+  p.out = out;
+  p.lse = lse;
+  p.workspace = workspace;
+  const DeviceInfo* dev = nullptr;
+  if ((st = device_or_error(&dev)) != QSA_OK) return st;
+  return from_cuda(launch(p, *dev, as_cuda(stream)));
+}
+
+// Query heads on a KV head of the 4-bit cache: two tokens of 64 dimensions share
+// a row of the operand, which doubles a tile's columns.
+static int kv4_group(const qsa_kv4_cache* c) { return c && c->D == 64 ? qsa::kKvMaxGroup / 2 : qsa::kKvMaxGroup; }
+
 extern "C" {
 
 int qsa_abi_version(void) { return QSA_ABI_VERSION; }
@@ -501,130 +648,104 @@ qsa_status qsa_split_reduce_static(const float* partial_max, const float* partia
   return from_cuda(qsa::launch_split_reduce(p, *dev, s));
 }
 
-// ------------------------------------------------- the paged 8-bit cache
-// Sizes of the cache and the batch; nothing is dereferenced but *c.
-static qsa_status check_cache_sizes(const qsa_kv_cache* c, int32_t n) {
-  if (!c) return QSA_ERR_INVALID_ARG;
-  if (c->B < 0 || n < 0 || c->n_pages < 0 || c->max_blocks < 0 || c->Hkv < 1 || c->block < 1 || c->D < 1)
-    return QSA_ERR_INVALID_ARG;
-  if ((c->D != 64 && c->D != 128) ||
-      (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) || c->Hkv > 65535)
-    return QSA_ERR_UNSUPPORTED_GEOMETRY;
-  if (static_cast<int64_t>(c->max_blocks) * c->block > (1 << 30) ||
-      static_cast<int64_t>(c->B) * n > 0x7FFFFFFFLL)
-    return QSA_ERR_UNSUPPORTED_GEOMETRY;
-  if (c->page_stride < static_cast<int64_t>(c->Hkv) * c->block * c->D) return QSA_ERR_INVALID_ARG;
-  if (c->page_stride >= (1LL << 40)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
-  if (c->page_stride % 16 != 0) return QSA_ERR_MISALIGNED;
-  return QSA_OK;
-}
-
-static qsa_status check_cache_pointers(const qsa_kv_cache* c) {
-  if (!c->lens || (c->max_blocks > 0 && !c->page_table)) return QSA_ERR_INVALID_ARG;
-  if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return QSA_ERR_INVALID_ARG;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
-      !aligned(c->page_table, 4) || !aligned(c->lens, 4) || !aligned(c->n_new, 4))
-    return QSA_ERR_MISALIGNED;
-  return QSA_OK;
-}
-
-// Rows of 16-bit floats read by 16-byte loads.
-static qsa_status check_rows(const qsa_rows* r) {
-  if (!r || !r->data) return QSA_ERR_INVALID_ARG;
-  if (r->stride_b < 0 || r->stride_n < 0 || r->stride_h < 0) return QSA_ERR_INVALID_ARG;
-  if (!aligned(r->data, 16) || r->stride_b % 8 != 0 || r->stride_n % 8 != 0 || r->stride_h % 8 != 0)
-    return QSA_ERR_MISALIGNED;
-  return QSA_OK;
-}
-
-static qsa::KvCacheArgs cache_args(const qsa_kv_cache* c) {
-  return qsa::KvCacheArgs{c->k,     c->v,       c->k_scale,    c->v_scale, c->page_table, c->lens,
-                          c->n_new, c->page_stride, c->n_pages, c->max_blocks, c->B, c->Hkv,
-                          c->block, c->D};
-}
-
-static qsa::KvRows row_args(const qsa_rows* r) {
-  return r ? qsa::KvRows{r->data, r->stride_b, r->stride_n, r->stride_h} : qsa::KvRows{nullptr, 0, 0, 0};
-}
-
+// -------------------------------------------------------- the paged caches
 qsa_status qsa_kv_append(const qsa_kv_cache* cache, const qsa_rows* k, const qsa_rows* v, const qsa_rows* q,
                          int32_t n, int32_t Hq, qsa_dtype dtype, const float* cos, const float* sin,
                          int32_t rot, int32_t max_pos, int32_t interleaved, void* q_out, uint16_t* kb,
                          qsa_stream_t stream) {
+  return run_append(cache, k, v, q, n, Hq, dtype, cos, sin, rot, max_pos, interleaved, nullptr, q_out, kb, stream,
+                    qsa::kv_append_grid, qsa::launch_kv_append);
+}
+
+qsa_status qsa_kv4_append(const qsa_kv4_cache* cache, const qsa_rows* k, const qsa_rows* v, const qsa_rows* q,
+                          int32_t n, int32_t Hq, qsa_dtype dtype, const float* cos, const float* sin,
+                          int32_t rot, int32_t max_pos, int32_t interleaved, const int32_t* offset, void* q_out,
+                          uint16_t* kb, qsa_stream_t stream) {
+  return run_append(cache, k, v, q, n, Hq, dtype, cos, sin, rot, max_pos, interleaved, offset, q_out, kb, stream,
+                    qsa::kv4_append_grid, qsa::launch_kv4_append);
+}
+
+qsa_status qsa_kv4_read(const qsa_kv4_cache* cache, int32_t n, qsa_dtype dtype, void* k_out, void* v_out,
+                        qsa_stream_t stream) {
   qsa_status st = check_cache_sizes(cache, n);
   if (st != QSA_OK) return st;
-  if (rot < 0 || max_pos < 0 || (q && Hq < 1)) return QSA_ERR_INVALID_ARG;
   if (dtype != QSA_F16 && dtype != QSA_BF16) return QSA_ERR_INVALID_ARG;
-  if (rot % 16 != 0 || rot > cache->D) return QSA_ERR_UNSUPPORTED_GEOMETRY;
-  qsa::KvAppendProblem p{};
-  p.cache = cache_args(cache);
-  p.q = row_args(q);
-  p.n = n;
-  p.Hq = q ? Hq : 0;
   if (cache->B == 0 || n == 0) return QSA_OK;
-  int64_t units = 0;
-  int32_t per_seq = 0;
-  if (qsa::kv_append_grid(p, &units, &per_seq) > 0x7FFFFFFFLL) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  const qsa::KvCacheArgs c = cache_args(cache);
+  if (qsa::kv4_read_grid(c, n) > 0x7FFFFFFFLL) return QSA_ERR_UNSUPPORTED_GEOMETRY;
   if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
-  if ((st = check_rows(k)) != QSA_OK || (st = check_rows(v)) != QSA_OK) return st;
-  if (q && ((st = check_rows(q)) != QSA_OK)) return st;
-  if ((q != nullptr) != (q_out != nullptr)) return QSA_ERR_INVALID_ARG;
-  if (rot > 0 && (!cos || !sin)) return QSA_ERR_INVALID_ARG;
-  if (!aligned(q_out, 16) || !aligned(kb, 2) || !aligned(cos, 16) || !aligned(sin, 16)) return QSA_ERR_MISALIGNED;
-  p.k = row_args(k);
-  p.v = row_args(v);
-  p.rot = rot;
-  p.max_pos = max_pos;
-  p.bf16 = dtype == QSA_BF16;
-  p.interleaved = interleaved != 0;
-  p.cos = cos;
-  p.sin = sin;
-  p.q_out = q_out;
-  p.kb = kb;
+  if (!k_out || !v_out) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return QSA_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   if ((st = device_or_error(&dev)) != QSA_OK) return st;
-  return from_cuda(qsa::launch_kv_append(p, *dev, as_cuda(stream)));
+  return from_cuda(qsa::launch_kv4_read(c, n, dtype == QSA_BF16, k_out, v_out, *dev, as_cuda(stream)));
 }
 
 size_t qsa_kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
   return qsa::kv_attend_workspace_bytes(B, n, Hq, Hkv, D);
 }
+size_t qsa_kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  return qsa::kv4_attend_workspace_bytes(B, n, Hq, Hkv, D);
+}
 
 qsa_status qsa_kv_attend(const qsa_kv_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
                          float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, qsa_stream_t stream) {
+  return run_attend(cache, q, n, Hq, dtype, scale, ids, n_lists, k, out, lse, workspace, workspace_bytes, stream,
+                    qsa::kKvMaxGroup, qsa::kv_attend_workspace_bytes, qsa::launch_kv_attend);
+}
+
+qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                          float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, qsa_stream_t stream) {
+  return run_attend(cache, q, n, Hq, dtype, scale, ids, n_lists, k, out, lse, workspace, workspace_bytes, stream,
+                    kv4_group(cache), qsa::kv4_attend_workspace_bytes, qsa::launch_kv4_attend);
+}
+
+qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
+                           float scale, const float* lse, float decay, float* weights, qsa_stream_t stream) {
   qsa_status st = check_cache_sizes(cache, n);
   if (st != QSA_OK) return st;
   if (Hq < 1 || (dtype != QSA_F16 && dtype != QSA_BF16)) return QSA_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0) return QSA_ERR_INVALID_ARG;
-  if (ids && (k < 1 || (n_lists != 1 && n_lists != cache->Hkv))) return QSA_ERR_INVALID_ARG;
-  if (Hq / cache->Hkv > qsa::kKvMaxGroup || (ids && k > (1 << 20))) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (Hq / cache->Hkv > kv4_group(cache)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
   if (cache->B == 0 || n == 0) return QSA_OK;
-  if (!(scale - scale == 0.0f)) return QSA_ERR_INVALID_ARG;
-  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f) || decay < 0.0f) return QSA_ERR_INVALID_ARG;
+  if ((st = check_cache_pointers(cache, false)) != QSA_OK) return st;
   if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
   if ((st = check_rows(q)) != QSA_OK) return st;
-  if (!out || !workspace ||
-      workspace_bytes < qsa::kv_attend_workspace_bytes(cache->B, n, Hq, cache->Hkv, cache->D))
-    return QSA_ERR_INVALID_ARG;
-  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ids, 4) || !aligned(workspace, 16))
-    return QSA_ERR_MISALIGNED;
-  qsa::KvAttendProblem p{};
-  p.cache = cache_args(cache);
-  p.q = row_args(q);
-  p.n = n;
-  p.Hq = Hq;
-  p.bf16 = dtype == QSA_BF16;
-  p.scale = scale;
-  p.ids = ids;
-  p.n_lists = ids ? n_lists : 1;
-  p.k = ids ? k : 0;
-  p.out = out;
-  p.lse = lse;
-  p.workspace = workspace;
+  if (!lse || !weights) return QSA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(weights, 4)) return QSA_ERR_MISALIGNED;
+  const qsa::Kv4WeightsProblem p{cache_args(cache), row_args(q), n, Hq, dtype == QSA_BF16, scale, decay, lse, weights};
   const DeviceInfo* dev = nullptr;
   if ((st = device_or_error(&dev)) != QSA_OK) return st;
-  return from_cuda(qsa::launch_kv_attend(p, *dev, as_cuda(stream)));
+  return from_cuda(qsa::launch_kv4_weights(p, *dev, as_cuda(stream)));
+}
+
+size_t qsa_kv4_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t budget) {
+  return qsa::kv4_evict_workspace_bytes(B, Hkv, budget);
+}
+
+qsa_status qsa_kv4_evict(const qsa_kv4_cache* cache, float* weights, int32_t budget, int32_t sink, int32_t recent,
+                         int32_t* lens_out, int32_t* offset, void* workspace, size_t workspace_bytes,
+                         qsa_stream_t stream) {
+  qsa_status st = check_cache_sizes(cache, 1);
+  if (st != QSA_OK) return st;
+  if (budget < 1 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > budget) return QSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(cache->B) * cache->Hkv > (1 << 27)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (cache->B == 0) return QSA_OK;
+  if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
+  if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
+  if (!weights || !lens_out || lens_out == cache->lens || lens_out == offset || !workspace ||
+      workspace_bytes < qsa::kv4_evict_workspace_bytes(cache->B, cache->Hkv, budget))
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned(weights, 4) || !aligned(lens_out, 4) || !aligned(offset, 4) || !aligned(workspace, 16))
+    return QSA_ERR_MISALIGNED;
+  const qsa::Kv4EvictProblem p{cache_args(cache), weights,  budget, sink,
+                               recent,            lens_out, offset, static_cast<int32_t*>(workspace)};
+  const DeviceInfo* dev = nullptr;
+  if ((st = device_or_error(&dev)) != QSA_OK) return st;
+  return from_cuda(qsa::launch_kv4_evict(p, *dev, as_cuda(stream)));
 }
 
 qsa_status qsa_selftest_bounded_wait(uint64_t timeout_ns, qsa_stream_t stream) {
