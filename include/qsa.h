@@ -561,7 +561,7 @@ qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t
  *   lse    f32 [B, n, Hq], as qsa_kv4_attend wrote it for the same rows; a row
  *          with -inf gives no token any weight.
  *   decay  finite, not negative.
- *   weights  f32 [n_pages, Hkv, block], 4-byte aligned. The tokens of the
+ *   weights  f32 [n_pages, Hkv, block], 16-byte aligned. The tokens of the
  *          call's sequences are updated, every other slot keeps its value.
  * A page may appear once in the table rows of the call's sequences. Scores and
  * sums are fp32, a query's elements held as by qsa_kv4_attend. Results do not

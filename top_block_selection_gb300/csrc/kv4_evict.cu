@@ -7,7 +7,7 @@
 // bits, ordered) by three histograms of 11, 11 and 10 bits, and of the keys equal
 // to it the lowest slots. Kept tokens move together in their order.
 //
-// One cluster of 1 to 8 CTAs an item: a CTA holds its part of the keys in shared
+// One cluster of 1 to 16 CTAs an item: a CTA holds its part of the keys in shared
 // memory, so that the weights are read once; histograms are added over
 // distributed shared memory. The move is in place: a token never moves up, so a
 // chunk's stores touch no later chunk's sources; within a chunk all CTAs load
@@ -25,7 +25,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kMaxKeys = 40960;  // of a CTA's part, in shared memory; those past it are read again in each pass
-constexpr int kPieces = 8;       // of 16 bytes, a thread's share of a chunk
+constexpr int kBatch = 8;        // keys of a thread whose loads are in flight together
+constexpr int kPieces = 4;       // of 32 bytes, a thread's share of a chunk of the move
 
 struct EvictArgs {
   KvCacheArgs c;
@@ -58,6 +59,23 @@ __device__ __forceinline__ uint2 load_remote2(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
+}
+
+// 32 bytes, loaded and stored by one instruction.
+struct Piece {
+  uint64_t v[4];
+};
+__device__ __forceinline__ Piece load_piece(const void* p) {
+  Piece x;
+  asm volatile("ld.global.v4.u64 {%0, %1, %2, %3}, [%4];"
+               : "=l"(x.v[0]), "=l"(x.v[1]), "=l"(x.v[2]), "=l"(x.v[3])
+               : "l"(p)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ void store_piece(void* p, const Piece& x) {
+  asm volatile("st.global.v4.u64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(x.v[0]), "l"(x.v[1]), "l"(x.v[2]), "l"(x.v[3])
+               : "memory");
 }
 
 struct EvictShared {
@@ -98,7 +116,7 @@ __device__ __forceinline__ void find_bin(EvictShared& s, int pass, int ctas, uin
   above = s.above;
 }
 
-__global__ void __launch_bounds__(kThreads) kv4_evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint8_t raw[];
   EvictShared& s = *reinterpret_cast<EvictShared*>(raw);
   uint32_t* const keys = reinterpret_cast<uint32_t*>(raw + sizeof(EvictShared));
@@ -122,35 +140,51 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_kernel(const __grid_consta
     return;
   }
   const int32_t* const table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks;
-  // Row of (page, head, slot) in the scales and weights; -1: no such page.
-  auto row_of = [&](int slot) -> int64_t {
+  // The page of a slot, -1: no such page; and the slot's row in scales and weights.
+  // (Without branches, so that the loads of several go out together.)
+  auto page_of = [&](int slot) -> int {
     const int page = load_global(table + (slot >> a.block_log2));
-    if (page < 0 || page >= a.c.n_pages) {
-      bad = true;
-      return -1;
-    }
+    const bool there = page >= 0 && page < a.c.n_pages;
+    bad = bad || !there;
+    return there ? page : -1;
+  };
+  auto row_in = [&](int page, int slot) {
     return ((static_cast<int64_t>(page) * a.c.Hkv + h) << a.block_log2) + (slot & mask);
+  };
+  auto row_of = [&](int slot) -> int64_t {
+    const int page = page_of(slot);
+    return page < 0 ? -1 : row_in(page, slot);
   };
 
   const int keep = a.budget - a.sink - a.recent;
   const int middle = len - a.recent - a.sink;
   const int part = (middle + a.ctas - 1) / a.ctas;
   const int first = a.sink + min(rank * part, middle), count = a.sink + min((rank + 1) * part, middle) - first;
+  auto key_of = [](float w) { return isnan(w) ? 0xFFFFFFFFu : score_key(w); };
   auto fresh_key = [&](int i) -> uint32_t {
     const int64_t row = row_of(first + i);
-    const float w = row >= 0 ? load_global(a.weights + row) : 0.0f;
-    return isnan(w) ? 0xFFFFFFFFu : score_key(w);
+    return key_of(row >= 0 ? load_global(a.weights + row) : 0.0f);
   };
   auto key = [&](int i) -> uint32_t { return i < a.cap ? keys[i] : fresh_key(i); };
 
   int32_t* const list = a.list + static_cast<int64_t>(item) * a.budget;
   if (keep > 0) {
     __syncthreads();  // the histograms are clear
-#pragma unroll 4
-    for (int i = tid; i < count; i += kThreads) {
-      const uint32_t k = fresh_key(i);
-      if (i < a.cap) keys[i] = k;
-      atomicAdd(&s.hist[0][k >> 21], 1u);
+    for (int i0 = tid; i0 < count; i0 += kBatch * kThreads) {
+      int64_t row[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) row[x] = i0 + x * kThreads < count ? row_of(first + i0 + x * kThreads) : -1;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) w[x] = row[x] >= 0 ? load_global(a.weights + row[x]) : 0.0f;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int i = i0 + x * kThreads;
+        if (i >= count) break;
+        const uint32_t k = key_of(w[x]);
+        if (i < a.cap) keys[i] = k;
+        atomicAdd(&s.hist[0][k >> 21], 1u);
+      }
     }
     uint32_t need = keep, prefix = 0, bin, above;
     cluster_sync();
@@ -216,65 +250,54 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_kernel(const __grid_consta
     cluster_sync();
   }
 
-  // The move.
-  const int half = a.c.D / 32;  // pieces of a token's key
-  const int tokens = kThreads * kPieces / (2 * half);
+  // The move. A token's codes are `lanes` pieces, one to a lane: its key's first.
+  const int lanes = a.c.D / 32, piece = tid % lanes, tokens = kThreads * kPieces / lanes;
   const int newest = a.budget - a.recent, shift = len - a.budget;
-  auto source = [&](int slot) { return slot >= newest ? slot + shift : __ldcg(list + slot); };
+  uint8_t* const codes = (piece < lanes / 2 ? a.c.k : a.c.v) + piece % (lanes / 2) * 32;
+  auto codes_at = [&](int page, int slot) {
+    return codes + page * a.c.page_stride + ((h << a.block_log2) + (slot & mask)) * static_cast<int64_t>(a.c.D / 2);
+  };
+  // Beside its codes a lane moves the key's scale (the first lane), the value's
+  // (the second) and the weight (the last).
+  uint16_t* const scales = piece == 0 ? a.c.k_scale4 : a.c.v_scale4;
   for (int base = a.sink; base < a.budget; base += a.ctas * tokens) {
-    const int mine = base + rank * tokens;
-    uint4 data[kPieces];
-    uint32_t moves = 0;
-    // A token's pieces are one to a lane: `half` of its key, `half` of its value.
-    auto piece_at = [&](int i, int64_t row) -> uint4* {
-      const int p = i % (2 * half);
-      uint8_t* const base_at = p < half ? a.c.k : a.c.v;
-      const int64_t page = (row >> a.block_log2) / a.c.Hkv, rest = row - ((page * a.c.Hkv) << a.block_log2);
-      return reinterpret_cast<uint4*>(base_at + page * a.c.page_stride + rest * (a.c.D / 2) + (p % half) * 16);
-    };
+    const int mine = base + rank * tokens + tid / lanes;
+    int src[kPieces], from[kPieces], to[kPieces];
+    Piece data[kPieces];
+    uint16_t scale[kPieces];
+    float weight[kPieces];
 #pragma unroll
     for (int r = 0; r < kPieces; ++r) {
-      const int i = r * kThreads + tid, slot = mine + i / (2 * half);
-      if (slot >= a.budget) continue;
-      const int src = source(slot);
-      if (src == slot) continue;
-      const int64_t row = row_of(src);
-      if (row < 0) continue;
-      data[r] = load_global(piece_at(i, row));
-      moves |= 1u << r;
+      const int slot = mine + r * (kThreads / lanes);
+      src[r] = slot >= a.budget ? slot : slot >= newest ? slot + shift : __ldcg(list + slot);
     }
-    uint16_t ks[2], vs[2];
-    float w[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = r * kThreads + tid, slot = mine + i;
-      if (i >= tokens || slot >= a.budget) continue;
-      const int src = source(slot);
-      if (src == slot) continue;
-      const int64_t row = row_of(src);
-      if (row < 0) continue;
-      ks[r] = a.c.k_scale4[row];
-      vs[r] = a.c.v_scale4[row];
-      w[r] = load_global(a.weights + row);
-      moves |= 256u << r;
+    for (int r = 0; r < kPieces; ++r) {
+      const int slot = mine + r * (kThreads / lanes);
+      from[r] = to[r] = -1;
+      if (src[r] != slot) {
+        from[r] = page_of(src[r]);
+        to[r] = page_of(slot);
+      }
     }
+#pragma unroll
+    for (int r = 0; r < kPieces; ++r)
+      if (from[r] >= 0 && to[r] >= 0) {
+        data[r] = load_piece(codes_at(from[r], src[r]));
+        const int64_t row = row_in(from[r], src[r]);
+        if (piece < 2) scale[r] = scales[row];
+        if (piece == lanes - 1) weight[r] = load_global(a.weights + row);
+      }
     cluster_sync();
 #pragma unroll
-    for (int r = 0; r < kPieces; ++r) {
-      const int i = r * kThreads + tid;
-      if (!(moves >> r & 1)) continue;
-      const int64_t row = row_of(mine + i / (2 * half));
-      if (row >= 0) *piece_at(i, row) = data[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (!(moves >> (8 + r) & 1)) continue;
-      const int64_t row = row_of(mine + r * kThreads + tid);
-      if (row < 0) continue;
-      a.c.k_scale4[row] = ks[r];
-      a.c.v_scale4[row] = vs[r];
-      a.weights[row] = w[r];
-    }
+    for (int r = 0; r < kPieces; ++r)
+      if (from[r] >= 0 && to[r] >= 0) {
+        const int slot = mine + r * (kThreads / lanes);
+        store_piece(codes_at(to[r], slot), data[r]);
+        const int64_t row = row_in(to[r], slot);
+        if (piece < 2) scales[row] = scale[r];
+        if (piece == lanes - 1) a.weights[row] = weight[r];
+      }
   }
   if (bad) atomicOr(a.status, kErrCacheIndex);
   // An attention next on the stream may start early and reads codes by bulk copies.
@@ -304,7 +327,7 @@ cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cu
   // more of the longest sequence there can be.
   const int64_t items = static_cast<int64_t>(p.cache.B) * p.cache.Hkv;
   const int64_t longest = static_cast<int64_t>(p.cache.max_blocks) * p.cache.block;
-  a.ctas = 8;
+  a.ctas = 16;
   while (a.ctas > 1 && (items * a.ctas > 2 * dev.sm_count || longest < 1024 * a.ctas)) a.ctas /= 2;
   a.cap = static_cast<int32_t>(std::min<int64_t>((longest + a.ctas - 1) / a.ctas, kMaxKeys));
   const size_t smem = sizeof(EvictShared) + sizeof(uint32_t) * a.cap;
@@ -314,6 +337,8 @@ cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cu
     const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(sizeof(EvictShared) + sizeof(uint32_t) * kMaxKeys));
     if (e != cudaSuccess) return e;
+    const cudaError_t e2 = cudaFuncSetAttribute(kv4_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e2 != cudaSuccess) return e2;
     ready.fetch_or(bit, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};

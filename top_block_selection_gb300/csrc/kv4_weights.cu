@@ -11,10 +11,10 @@
 // the exponent's absolute one, and one float of c would be the largest part of it.
 //
 // One CTA an SM. The tiles of all (sequence, KV head) items are dealt to the
-// CTAs in equal contiguous shares. A warp loads keys (TMA) and scales ahead, four
-// make the e4m3 terms of up to kGroups x RT rows, one issues the products, and
-// two warpgroups take the tiles in turn, each with two places for scores in
-// tensor memory. More rows than that go over the share's tiles of the item again
+// CTAs in equal contiguous shares. A warp loads keys, scales and weights ahead by
+// bulk copies, four make the e4m3 terms of up to kGroups x RT rows, one issues the
+// products, and two warpgroups take the tiles in turn, each with two places for
+// scores in tensor memory. More rows than that go over the share's tiles of the item again
 // (from L2), adding to what the pass before left.
 //
 // What bounds it: for a decode step the keys and weights from HBM; for many rows
@@ -26,11 +26,15 @@
 namespace qsa {
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kGroups = 4;       // of rows, in one pass
 constexpr int kQueryWarps = 4;
 constexpr int kThreads = 2 * 128 + 64 + 32 * kQueryWarps;
 constexpr int kPlace = 128;      // columns of a place for scores
+
+template <int D_, int RT_, int T_>
+struct WeightsCfg : AttendCfg<D_, RT_, T_, true> {
+  static constexpr int kStages = RT_ < 32 ? 10 : 6;  // even: a stage serves one warpgroup
+  static constexpr int kGroups = RT_ < 32 ? 1 : 4;   // of rows, in one pass (fewer rows than 32 are one group)
+};
 
 struct WeightsArgs {
   AttendArgs a;      // out, lse, ids, parts, jobs unused; scale_log2 = 1
@@ -61,10 +65,11 @@ struct GroupRows {
 
 template <class C>
 struct WeightsShared {
-  GroupRows<C> rows[2][kGroups];
-  alignas(16) uint16_t ks[kStages][C::kTokens];
-  alignas(16) int64_t row0[kStages][C::kSlots];  // of a slot's first token among the weights; -1: no block
-  uint64_t k_full[kStages], k_empty[kStages];
+  GroupRows<C> rows[2][C::kGroups];
+  alignas(16) uint16_t ks[C::kStages][C::kTokens];
+  alignas(16) float old[C::kStages][C::kTokens];    // weights before the call
+  alignas(16) int64_t row0[C::kStages][C::kSlots];  // of a slot's first token among the weights; -1: no block
+  uint64_t k_full[C::kStages], k_empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], s_empty[2][2];
   int64_t scan[kThreads / 32];
@@ -94,7 +99,7 @@ __device__ __forceinline__ void each_item(const AttendArgs& a, const WeightsShar
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     kv4_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightsArgs w) {
-  constexpr int PAR = C::PAR, RT = C::RT, N = C::N;
+  constexpr int PAR = C::PAR, RT = C::RT, N = C::N, kStages = C::kStages, kGroups = C::kGroups;
   constexpr int kTile = kKvTile * 128;  // bytes of a key tile
   extern __shared__ uint8_t raw[];
   uint8_t* const ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -201,16 +206,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < PAR; ++i)
             k_mul[i] = __uint_as_float(static_cast<uint32_t>(s.ks[st][t * PAR + i]) << 16);
           const int64_t row0 = s.row0[st][slot];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.k_empty[st]);
           float* const at = w.weights + row0 + off;
           bool there[PAR];
           float old[PAR], acc[PAR];
 #pragma unroll
           for (int i = 0; i < PAR; ++i) {
             there[i] = row0 >= 0 && pos + i < q.len;
-            old[i] = acc[i] = 0.0f;
-            if (there[i] && (pass > 0 || (w.decay != 0.0f && pos + i < q.first))) old[i] = load_global(at + i);
+            acc[i] = 0.0f;
+            old[i] = pass == 0 && w.decay != 0.0f && pos + i < q.first ? s.old[st][t * PAR + i] * w.decay : 0.0f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.k_empty[st]);
+          if (pass > 0) {  // what this thread left in the pass before
+#pragma unroll
+            for (int i = 0; i < PAR; ++i)
+              if (there[i]) old[i] = load_global(at + i);
           }
           for (int gr = 0; gr < groups; ++gr, ++unit) {
             const GroupRows<C>& rows = s.rows[buf][gr];
@@ -250,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < PAR; ++i)
-            if (there[i]) at[i] = (pass > 0 ? old[i] : old[i] * w.decay) + acc[i];
+            if (there[i]) at[i] = old[i] + acc[i];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_empty[buf]);
@@ -278,34 +288,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               page = -1;
             }
           }
-          using Scales = typename std::conditional<PAR == 2, uint4, uint2>::type;
-          Scales next{};
-          auto scales = [&](int i) {
-            const int t = lane * 4 * PAR, from = i * spt + t / a.c.block;
-            const int of = __shfl_sync(0xFFFFFFFFu, page, from & 31);
-            next = Scales{};
-            if (i < tiles && of >= 0)
-              next = load_global(reinterpret_cast<const Scales*>(
-                  a.c.k_scale4 + (static_cast<int64_t>(of) * a.c.Hkv + h) * a.c.block + (t & (a.c.block - 1))));
-          };
-          scales(0);
           for (int i = 0; i < tiles; ++i, ++g) {
             const uint32_t st = g % kStages;
             if (ok && g >= kStages) ok = wait_or_stop(&s.k_empty[st], ((g / kStages) & 1) ^ 1, &s.stop, a.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) continue;
             const uint32_t there = __ballot_sync(0xFFFFFFFFu, my_k == i && page >= 0);
-            // Bytes count as they are packed, half of a slab's.
-            if (elect_one()) mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2));
-            for (int j = 0; j < spt; ++j) {
-              const int z = __shfl_sync(0xFFFFFFFFu, page, i * spt + j);
-              if (z >= 0 && elect_one()) tma_load_3d(ring + st * kTile + j * slab, &tm_k, 0, y, z, &s.k_full[st]);
-              __syncwarp();
+            // Codes count as they are packed, half of a slab's bytes.
+            const bool with_old = pass == 0 && w.decay != 0.0f;
+            if (elect_one())
+              mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2 + a.c.block * (with_old ? 6 : 2)));
+            __syncwarp();
+            // Each lane of the tile brings its own block.
+            if (my_k == i) {
+              const int64_t row0 = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
+              s.row0[st][my_slot] = row0;
+              if (page >= 0) {
+                const int first = my_slot * a.c.block;
+                tma_load_3d(ring + st * kTile + my_slot * slab, &tm_k, 0, y, page, &s.k_full[st]);
+                bulk_load(&s.ks[st][first], a.c.k_scale4 + row0, a.c.block * 2, &s.k_full[st]);
+                if (with_old) bulk_load(&s.old[st][first], w.weights + row0, a.c.block * 4, &s.k_full[st]);
+              }
             }
-            *reinterpret_cast<Scales*>(&s.ks[st][lane * 4 * PAR]) = next;
-            if (my_k == i)
-              s.row0[st][my_slot] = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
-            scales(i + 1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.k_full[st]);
           }
@@ -368,23 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           en.j0 = (pass * kGroups + gr) * a.qt;
           en.nq = min(en.j0 + a.qt, q.n_new) - en.j0;
           en.first_pos = q.first + en.j0;
-          for (int r0 = (warp - 10) * 4; r0 < RT; r0 += 4 * kQueryWarps) {
-            query_rows<C, 4>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, h, r0, 1);
-            __syncwarp();
-            const int r = r0 + lane;
-            if (lane < 4 && r < RT) {
-              const int pos = rows.info.row_pos[r];
-              const bool there = pos >= 0 && pos != kKvNoToken;
-              const float lse = there ? load_global(w.lse + rows.info.row_at[r]) : -INFINITY;
-              const bool gives = there && lse != -INFINITY;
-              const float t = rows.info.row_mul[r];
-              rows.hi[r] = gives ? t * w.c_hi : 0.0f;
-              rows.lo[r] = gives ? t * w.c_lo : 0.0f;
-              rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
-              if (!there) rows.info.row_pos[r] = -1;
-            }
-            __syncwarp();
+          // A warp's rows of a group are loaded together.
+          constexpr int kRows = RT / kQueryWarps;
+          const int r0 = (warp - 10) * kRows, r = r0 + lane;
+          query_rows<C, kRows>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, h, r0, 1);
+          __syncwarp();
+          if (lane < kRows) {
+            const int pos = rows.info.row_pos[r];
+            const bool there = pos >= 0 && pos != kKvNoToken;
+            const float lse = there ? load_global(w.lse + rows.info.row_at[r]) : -INFINITY;
+            const bool gives = there && lse != -INFINITY;
+            const float t = rows.info.row_mul[r];
+            rows.hi[r] = gives ? t * w.c_hi : 0.0f;
+            rows.lo[r] = gives ? t * w.c_lo : 0.0f;
+            rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
+            if (!there) rows.info.row_pos[r] = -1;
           }
+          __syncwarp();
         }
         // The first position that not all of the pass's rows see.
         if (warp == 10 && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups * a.qt, 0) : -1;
@@ -401,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int RT, int T>
 cudaError_t weights_form(const CUtensorMap& tk, const WeightsArgs& w, int grid, int device, cudaStream_t stream) {
-  using C = AttendCfg<D, RT, T, true>;
-  constexpr int smem = 1024 + kStages * kKvTile * 128 + 2 * kGroups * C::kQBytes + static_cast<int>(sizeof(WeightsShared<C>));
+  using C = WeightsCfg<D, RT, T>;
+  constexpr int smem = 1024 + C::kStages * kKvTile * 128 + 2 * C::kGroups * C::kQBytes + static_cast<int>(sizeof(WeightsShared<C>));
   static_assert(smem <= 227 * 1024, "shared memory");
   static_assert(C::N <= kPlace, "tensor memory");
   static std::atomic<uint64_t> ready{0};

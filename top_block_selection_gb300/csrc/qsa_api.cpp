@@ -715,7 +715,7 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
   if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
   if ((st = check_rows(q)) != QSA_OK) return st;
   if (!lse || !weights) return QSA_ERR_INVALID_ARG;
-  if (!aligned(lse, 4) || !aligned(weights, 4)) return QSA_ERR_MISALIGNED;
+  if (!aligned(lse, 4) || !aligned(weights, 16)) return QSA_ERR_MISALIGNED;
   const qsa::Kv4WeightsProblem p{cache_args(cache), row_args(q), n, Hq, dtype == QSA_BF16, scale, decay, lse, weights};
   const DeviceInfo* dev = nullptr;
   if ((st = device_or_error(&dev)) != QSA_OK) return st;
