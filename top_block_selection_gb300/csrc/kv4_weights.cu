@@ -12,7 +12,7 @@
 //
 // One CTA an SM. The tiles of all (sequence, KV head) items are dealt to the
 // CTAs in equal contiguous shares. A warp loads keys, scales and weights ahead by
-// bulk copies, four make the e4m3 terms of up to kGroups x RT rows, one issues the
+// asynchronous copies, eight make the e4m3 terms of up to kGroups x RT rows, one issues the
 // products, and two warpgroups take the tiles in turn, each with two places for
 // scores in tensor memory. More rows than that go over the share's tiles of the item again
 // (from L2), adding to what the pass before left.
@@ -26,13 +26,18 @@
 namespace qsa {
 namespace {
 
-constexpr int kQueryWarps = 4;
-constexpr int kThreads = 2 * 128 + 64 + 32 * kQueryWarps;
+constexpr int kQueryWarps = 8;
+constexpr int kFirstProducer = 9;  // warps: 8 of weights, products, producers, queries
 constexpr int kPlace = 128;      // columns of a place for scores
 
 template <int D_, int RT_, int T_>
 struct WeightsCfg : AttendCfg<D_, RT_, T_, true> {
-  static constexpr int kStages = RT_ < 32 ? 10 : 6;  // even: a stage serves one warpgroup
+  static constexpr int kProducers = RT_ < 32 ? 4 : 2;  // warps that load, a tile each in turn
+  // A stage serves one warpgroup and one producer.
+  static constexpr int kStages = RT_ < 32 ? 8 : 6;
+  static constexpr int kFirstQuery = kFirstProducer + kProducers;
+  static constexpr int kThreads = 32 * (kFirstQuery + kQueryWarps);
+  static_assert(kStages % 2 == 0 && kStages % kProducers == 0, "stages");
   static constexpr int kGroups = RT_ < 32 ? 1 : 4;   // of rows, in one pass (fewer rows than 32 are one group)
 };
 
@@ -43,6 +48,15 @@ struct WeightsArgs {
   float c_hi, c_lo;  // scale * log2(e)
   float decay;
 };
+
+// 16 bytes to shared memory, behind the thread's back.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+// Arrives on `bar` when the thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 struct Sequence {
   int32_t len, first, n_new, tiles;  // tokens, slot of the first new one, new ones
@@ -72,7 +86,7 @@ struct WeightsShared {
   uint64_t k_full[C::kStages], k_empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], s_empty[2][2];
-  int64_t scan[kThreads / 32];
+  int64_t scan[C::kThreads / 32];
   int64_t lo, hi, total;
   int32_t b, h, t;  // where the share begins
   uint32_t tmem, stop;
@@ -96,10 +110,27 @@ __device__ __forceinline__ void each_item(const AttendArgs& a, const WeightsShar
   }
 }
 
+// K columns of scores: their terms added, each 1/16 of the one before.
+template <class C, int K>
+__device__ __forceinline__ void score_part(uint32_t taddr, float (&x)[K]) {
+  float t1[K], t2[K];
+  tmem_ld_cols<K>(taddr, x);
+  tmem_ld_cols<K>(taddr + C::RT, t1);
+  if (C::T == 3) tmem_ld_cols<K>(taddr + 2 * C::RT, t2);
+  tmem_ld_wait();
+#pragma unroll
+  for (int r = 0; r < K; r += 2) {
+    F2 sum = f2(t1[r], t1[r + 1]);
+    if (C::T == 3) sum = fma2(f2(t2[r], t2[r + 1]), f2(0.0625f, 0.0625f), sum);
+    f2_get(fma2(sum, f2(0.0625f, 0.0625f), f2(x[r], x[r + 1])), x[r], x[r + 1]);
+  }
+}
+
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
     kv4_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightsArgs w) {
   constexpr int PAR = C::PAR, RT = C::RT, N = C::N, kStages = C::kStages, kGroups = C::kGroups;
+  constexpr int kThreads = C::kThreads, kProducers = C::kProducers;
   constexpr int kTile = kKvTile * 128;  // bytes of a key tile
   extern __shared__ uint8_t raw[];
   uint8_t* const ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -110,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.k_full[i], 2);
+      mbar_init(&s.k_full[i], 33);
       mbar_init(&s.k_empty[i], 5);
     }
     for (int i = 0; i < 2; ++i) {
@@ -129,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_proxy_async_global();  // earlier plain stores, before this kernel's bulk loads
   // Tensor memory is asked for only now, and later kernels of the stream may start
   // only once every CTA has it (see kv_attend_kernel).
-  if (warp == 9) {
+  if (warp == 8) {
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
@@ -228,34 +259,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_or_stop(&s.s_full[wg][place], (unit >> 1) & 1, &s.stop, a.status);
             __syncwarp();
             tc_fence_after_sync();
-            float e[RT];
-            tmem_rows<C, false>(tm + place * kPlace, e);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.s_empty[wg][place]);
+            const bool masks = pos + PAR - 1 > lo_pos;
+            // A part of the rows at a time, each of one token's columns.
+            constexpr int kPart = C::RR < 16 ? C::RR : 16;
 #pragma unroll
-            for (int r = 0; r < RT; r += 2) {
-              const float k = k_mul[r / C::RR];
-              const F2 y = f2(e[r], e[r + 1]) * f2(k, k);
-              const F2 x = fma2(y, f2(rows.hi[r], rows.hi[r + 1]),
-                                fma2(y, f2(rows.lo[r], rows.lo[r + 1]), f2(rows.nl[r], rows.nl[r + 1])));
-              f2_get(x, e[r], e[r + 1]);
-              e[r] = exp2_approx(e[r]);
-              e[r + 1] = exp2_approx(e[r + 1]);
-            }
-            if (pos + PAR - 1 > lo_pos) {
+            for (int r0 = 0; r0 < RT; r0 += kPart) {
+              float e[kPart];
+              score_part<C, kPart>(tm + place * kPlace + r0, e);
+              if (r0 + kPart == RT) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.s_empty[wg][place]);
+              }
+              const float k = k_mul[r0 / C::RR];
 #pragma unroll
-              for (int r = 0; r < RT; ++r)
-                if (pos + r / C::RR > rows.info.row_pos[r]) e[r] = 0.0f;
-            }
+              for (int r = 0; r < kPart; r += 2) {
+                const F2 y = f2(e[r], e[r + 1]) * f2(k, k);
+                const F2 x = fma2(y, f2(rows.hi[r0 + r], rows.hi[r0 + r + 1]),
+                                  fma2(y, f2(rows.lo[r0 + r], rows.lo[r0 + r + 1]), f2(rows.nl[r0 + r], rows.nl[r0 + r + 1])));
+                f2_get(x, e[r], e[r + 1]);
+                e[r] = exp2_approx(e[r]);
+                e[r + 1] = exp2_approx(e[r + 1]);
+              }
+              if (masks) {
 #pragma unroll
-            for (int i = 0; i < PAR; ++i) {
-              F2 sum = f2(0.0f, 0.0f);
+                for (int r = 0; r < kPart; ++r)
+                  if (pos + r0 / C::RR > rows.info.row_pos[r0 + r]) e[r] = 0.0f;
+              }
+              F2 sum = f2(e[0], e[1]);
 #pragma unroll
-              for (int r = 0; r < C::RR; r += 2) sum = sum + f2(e[i * C::RR + r], e[i * C::RR + r + 1]);
+              for (int r = 2; r < kPart; r += 2) sum = sum + f2(e[r], e[r + 1]);
               float s0, s1;
               f2_get(sum, s0, s1);
-              acc[i] += s0 + s1;
+              acc[r0 / C::RR] += s0 + s1;
             }
           }
 #pragma unroll
@@ -267,19 +303,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         g0 += part;
       }
     });
-  } else if (warp == 8) {
+  } else if (warp >= kFirstProducer && warp < C::kFirstQuery) {
     // ------------------------------------------------------- keys, scales
+    // Tiles p, p + kProducers, ... of the CTA: one warp's chain of instructions for
+    // a tile takes longer (about 800 cycles) than the tile may.
+    const int p = warp - kFirstProducer;
     const int spt = a.spt, per_batch = 32 / spt, my_k = lane / spt, my_slot = lane % spt;
-    uint32_t g = 0;
+    uint32_t g0 = 0;
     bool bad = false, ok = true;
     each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
       if (load_global(a.c.lens + b) > q.len) bad = true;  // longer than its page table
       const int32_t* const table = a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks;
       const int y = h * a.c.block / PAR, slab = a.c.block * C::HD;
-      for (int pass = 0; pass < passes; ++pass)
-        for (int k0 = 0; k0 < part; k0 += per_batch) {
-          const int tiles = min(per_batch, part - k0);
-          const int blk = (t0 + k0 + my_k) * spt + my_slot;
+      for (int pass = 0; pass < passes; ++pass, g0 += part) {
+        const int own0 = static_cast<int>((p + kProducers - g0 % kProducers) % kProducers);
+        const int own = part > own0 ? (part - own0 + kProducers - 1) / kProducers : 0;
+        for (int k0 = 0; k0 < own; k0 += per_batch) {
+          const int tiles = min(per_batch, own - k0);
+          const int blk = (t0 + own0 + (k0 + my_k) * kProducers) * spt + my_slot;
           int page = -1;
           if (my_k < tiles && static_cast<int64_t>(blk) * a.c.block < q.len) {
             page = load_global(table + blk);
@@ -288,37 +329,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               page = -1;
             }
           }
-          for (int i = 0; i < tiles; ++i, ++g) {
-            const uint32_t st = g % kStages;
+          for (int i = 0; i < tiles; ++i) {
+            const uint32_t g = g0 + own0 + (k0 + i) * kProducers, st = g % kStages;
             if (ok && g >= kStages) ok = wait_or_stop(&s.k_empty[st], ((g / kStages) & 1) ^ 1, &s.stop, a.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) continue;
             const uint32_t there = __ballot_sync(0xFFFFFFFFu, my_k == i && page >= 0);
             // Codes count as they are packed, half of a slab's bytes.
-            const bool with_old = pass == 0 && w.decay != 0.0f;
-            if (elect_one())
-              mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2 + a.c.block * (with_old ? 6 : 2)));
+            if (elect_one()) mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2));
             __syncwarp();
-            // Each lane of the tile brings its own block.
-            if (my_k == i) {
-              const int64_t row0 = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
+            const int64_t row0 = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
+            if (my_k == i) {  // each lane of the tile brings its own block's keys
               s.row0[st][my_slot] = row0;
-              if (page >= 0) {
-                const int first = my_slot * a.c.block;
-                tma_load_3d(ring + st * kTile + my_slot * slab, &tm_k, 0, y, page, &s.k_full[st]);
-                bulk_load(&s.ks[st][first], a.c.k_scale4 + row0, a.c.block * 2, &s.k_full[st]);
-                if (with_old) bulk_load(&s.old[st][first], w.weights + row0, a.c.block * 4, &s.k_full[st]);
+              if (page >= 0) tma_load_3d(ring + st * kTile + my_slot * slab, &tm_k, 0, y, page, &s.k_full[st]);
+            }
+            // Scales and weights by 16-byte copies of all lanes: bulk copies of a
+            // block's few bytes took 700 cycles a tile to issue.
+            {
+              const int t = lane * 8;
+              const int64_t from = __shfl_sync(0xFFFFFFFFu, row0, (i * spt + t / a.c.block) & 31);
+              if (from >= 0 && t < C::kTokens) copy16(&s.ks[st][t], a.c.k_scale4 + from + (t & (a.c.block - 1)));
+            }
+            if (pass == 0 && w.decay != 0.0f) {
+#pragma unroll
+              for (int x = 0; x < PAR; ++x) {
+                const int t = x * 128 + lane * 4;
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, row0, (i * spt + t / a.c.block) & 31);
+                if (from >= 0) copy16(&s.old[st][t], w.weights + from + (t & (a.c.block - 1)));
               }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.k_full[st]);
+            copies_arrive(&s.k_full[st]);
           }
         }
+      }
     });
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, kErrCacheIndex);
     if (!ok)  // let the copies in flight land before the CTA gives its memory back
-      for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s.k_full[i], 0, 10000000ull), mbar_wait_bounded(&s.k_full[i], 1, 10000000ull);
-  } else if (warp == 9) {
+      for (int i = p; i < kStages; i += kProducers)
+        for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait_bounded(&s.k_full[i], parity, 10000000ull);
+  } else if (warp == 8) {
     // ----------------------------------------------------------- products
     const uint32_t tmem = uniform(s.tmem), ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem);
     const bool leader = elect_one();
@@ -365,22 +414,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = pc & 1;
         if (pc >= 2) wait_or_stop(&s.q_empty[buf], ((pc >> 1) & 1) ^ 1, &s.stop, a.status);
         const int groups = min(per_pass, n_groups - pass * kGroups);
-        for (int gr = 0; gr < groups; ++gr) {
+        // A warp's rows are of one group, and loaded together.
+        constexpr int kRows = kGroups * RT / kQueryWarps, kWarps = RT / kRows;
+        const int gr = (warp - C::kFirstQuery) / kWarps, r0 = (warp - C::kFirstQuery) % kWarps * kRows, r = r0 + lane;
+        if (gr < groups) {
           GroupRows<C>& rows = s.rows[buf][gr];
           Entry en{};
           en.b = b;
           en.j0 = (pass * kGroups + gr) * a.qt;
           en.nq = min(en.j0 + a.qt, q.n_new) - en.j0;
           en.first_pos = q.first + en.j0;
-          // A warp's rows of a group are loaded together.
-          constexpr int kRows = RT / kQueryWarps;
-          const int r0 = (warp - 10) * kRows, r = r0 + lane;
+          // (A lane's row as query_rows has it.)
+          const int row = r % C::RR, j = row / a.R;
+          const bool there = lane < kRows && row < a.qt * a.R && j < en.nq && en.first_pos + j >= 0;
+          float lse = -INFINITY;
+          if (there)
+            lse = load_global(w.lse + (static_cast<int64_t>(b) * a.n + en.j0 + j) * a.Hq + h * a.R + (row - j * a.R));
           query_rows<C, kRows>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, h, r0, 1);
           __syncwarp();
           if (lane < kRows) {
-            const int pos = rows.info.row_pos[r];
-            const bool there = pos >= 0 && pos != kKvNoToken;
-            const float lse = there ? load_global(w.lse + rows.info.row_at[r]) : -INFINITY;
             const bool gives = there && lse != -INFINITY;
             const float t = rows.info.row_mul[r];
             rows.hi[r] = gives ? t * w.c_hi : 0.0f;
@@ -391,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         // The first position that not all of the pass's rows see.
-        if (warp == 10 && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups * a.qt, 0) : -1;
+        if (warp == C::kFirstQuery && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups * a.qt, 0) : -1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_full[buf]);
@@ -400,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) tmem_dealloc(s.tmem, 512);
+  if (warp == 8) tmem_dealloc(s.tmem, 512);
 }
 
 template <int D, int RT, int T>
@@ -416,7 +468,7 @@ cudaError_t weights_form(const CUtensorMap& tk, const WeightsArgs& w, int grid, 
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  const cudaError_t e = launch_pdl(kv4_weights_kernel<C>, dim3(grid), dim3(kThreads), smem, stream, tk, w);
+  const cudaError_t e = launch_pdl(kv4_weights_kernel<C>, dim3(grid), dim3(C::kThreads), smem, stream, tk, w);
   if (e == cudaSuccess) plan_add("kv4_weights_kernel");
   return e;
 }
