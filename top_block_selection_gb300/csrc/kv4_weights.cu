@@ -12,9 +12,10 @@
 //
 // One CTA an SM. The tiles of all (sequence, KV head) items are dealt to the
 // CTAs in equal contiguous shares. A warp loads keys, scales and weights ahead by
-// asynchronous copies, eight make the e4m3 terms of up to kGroups x RT rows, one issues the
-// products, and two warpgroups take the tiles in turn, each with two places for
-// scores in tensor memory. More rows than that go over the share's tiles of the item again
+// asynchronous copies, eight make the e4m3 terms of up to kGroups x RT rows, and two
+// warpgroups take the tiles in turn, each with a warp that issues its products and
+// two places for scores in tensor memory. (One warp for all products took 360
+// cycles a tile beside its waits.) More rows than that go over the share's tiles of the item again
 // (from L2), adding to what the pass before left.
 //
 // What bounds it: for a decode step the keys and weights from HBM; for many rows
@@ -27,7 +28,7 @@ namespace qsa {
 namespace {
 
 constexpr int kQueryWarps = 8;
-constexpr int kFirstProducer = 9;  // warps: 8 of weights, products, producers, queries
+constexpr int kFirstProducer = 10;  // warps: 8 of weights, 2 of products, producers, queries
 constexpr int kPlace = 128;      // columns of a place for scores
 
 template <int D_, int RT_, int T_>
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], kQueryWarps);
-      mbar_init(&s.q_empty[i], 9);
+      mbar_init(&s.q_empty[i], 10);
       for (int j = 0; j < 2; ++j) {
         mbar_init(&s.s_full[i][j], 1);
         mbar_init(&s.s_empty[i][j], 4);
@@ -367,40 +368,37 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (!ok)  // let the copies in flight land before the CTA gives its memory back
       for (int i = p; i < kStages; i += kProducers)
         for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait_bounded(&s.k_full[i], parity, 10000000ull);
-  } else if (warp == 8) {
+  } else if (warp < kFirstProducer) {
     // ----------------------------------------------------------- products
-    const uint32_t tmem = uniform(s.tmem), ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem);
+    const int wg = warp - 8;
+    const uint32_t tm = uniform(s.tmem) + wg * 2 * kPlace, ring_addr = smem_u32(ring), q_addr = smem_u32(q_smem);
     const bool leader = elect_one();
-    uint32_t g0 = 0, pc = 0, unit[2] = {0, 0};
+    uint32_t g0 = 0, pc = 0, unit = 0;
     each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
       for (int pass = 0; pass < passes; ++pass, ++pc) {
         const uint32_t buf = pc & 1;
         const int groups = min(per_pass, n_groups - pass * kGroups);
         wait_or_stop(&s.q_full[buf], (pc >> 1) & 1, &s.stop, a.status);
-        // The two warpgroups' tiles side by side, so that both have scores to work on.
-        for (uint32_t pair = g0 & ~1u; pair < g0 + part; pair += 2)
-          for (int gr = 0; gr < groups; ++gr)
+        for (uint32_t g = g0 + ((g0 ^ wg) & 1); g < g0 + part; g += 2) {
+          const uint32_t st = g % kStages;
+          wait_or_stop(&s.k_full[st], (g / kStages) & 1, &s.stop, a.status);
+          for (int gr = 0; gr < groups; ++gr, ++unit) {
+            const uint32_t place = unit & 1;
+            if (unit >= 2) wait_or_stop(&s.s_empty[wg][place], ((unit >> 1) & 1) ^ 1, &s.stop, a.status);
+            __syncwarp();
+            tc_fence_after_sync();
+            if (leader) {
+              const uint64_t ka = smem_desc_rows<128>(ring_addr + st * kTile);
+              const uint64_t qa = smem_desc_rows<128>(q_addr + (buf * kGroups + gr) * C::kQBytes);
 #pragma unroll
-            for (int wg = 0; wg < 2; ++wg) {
-              const uint32_t g = pair + wg, st = g % kStages;
-              if (g < g0 || g >= g0 + part) continue;
-              if (gr == 0) wait_or_stop(&s.k_full[st], (g / kStages) & 1, &s.stop, a.status);
-              const uint32_t place = unit[wg] & 1;
-              if (unit[wg] >= 2) wait_or_stop(&s.s_empty[wg][place], ((unit[wg] >> 1) & 1) ^ 1, &s.stop, a.status);
-              ++unit[wg];
-              __syncwarp();
-              tc_fence_after_sync();
-              if (leader) {
-                const uint64_t ka = smem_desc_rows<128>(ring_addr + st * kTile);
-                const uint64_t qa = smem_desc_rows<128>(q_addr + (buf * kGroups + gr) * C::kQBytes);
-                const uint32_t to = tmem + (wg * 2 + place) * kPlace;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_f8_ss(to, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, true), ks > 0);
-                mma_commit(&s.s_full[wg][place]);
-                if (gr == groups - 1) mma_commit(&s.k_empty[st]);
-              }
-              __syncwarp();
+              for (int ks = 0; ks < 4; ++ks)
+                mma_f8_ss(tm + place * kPlace, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, true), ks > 0);
+              mma_commit(&s.s_full[wg][place]);
+              if (gr == groups - 1) mma_commit(&s.k_empty[st]);
             }
+            __syncwarp();
+          }
+        }
         if (leader) mma_commit(&s.q_empty[buf]);
         __syncwarp();
         g0 += part;
