@@ -7,7 +7,7 @@
 // bits, ordered) by three histograms of 11, 11 and 10 bits, and of the keys equal
 // to it the lowest slots. Kept tokens move together in their order.
 //
-// One cluster of 1 to 16 CTAs an item: a CTA holds its part of the keys in shared
+// One cluster of 1 to 8 CTAs an item: a CTA holds its part of the keys in shared
 // memory, so that the weights are read once; histograms are added over
 // distributed shared memory. The move is in place: a token never moves up, so a
 // chunk's stores touch no later chunk's sources; within a chunk all CTAs load
@@ -22,11 +22,12 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
+// CTAs of an item at most. (16 are a cluster that few GPCs take beside another: 8
+// heads of 131,072 tokens 84 us instead of 71.)
+constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 40960;  // of a CTA's part, in shared memory; those past it are read again in each pass
 constexpr int kBatch = 8;        // keys of a thread whose loads are in flight together
-constexpr int kPieces = 4;       // of 32 bytes, a thread's share of a chunk of the move
 
 struct EvictArgs {
   KvCacheArgs c;
@@ -39,20 +40,19 @@ struct EvictArgs {
   int32_t ctas, cap, block_log2;
 };
 
+template <int CLUSTER>
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (CLUSTER == 1) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ uint4 load_remote4(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at)
-               : "memory");
+__device__ __forceinline__ uint32_t load_remote(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
 __device__ __forceinline__ uint2 load_remote2(uint32_t at) {
@@ -80,48 +80,96 @@ __device__ __forceinline__ void store_piece(void* p, const Piece& x) {
 
 struct EvictShared {
   alignas(16) uint32_t hist[3][kBins];
-  uint32_t warp[kThreads / 32];
-  alignas(8) uint2 counts[kThreads / 32];  // above, equal
+  alignas(8) uint32_t coarse[3][kCoarse];  // sums of kBins / kCoarse bins
+  alignas(8) uint2 counts[32];  // above, equal
   alignas(8) uint2 total;
   uint32_t bin, above;
 };
 
-// The bin that holds the `need`-th largest key, and how many keys lie above it.
-__device__ __forceinline__ void find_bin(EvictShared& s, int pass, int ctas, uint32_t need, uint32_t& bin, uint32_t& above) {
-  const int tid = threadIdx.x, lane = tid % 32;
-  uint32_t n[4] = {0, 0, 0, 0};
-  for (int r = 0; r < ctas; ++r) {
-    const uint4 v = load_remote4(remote(&s.hist[pass][kBins - 4 - 4 * tid], r));
-    n[0] += v.w, n[1] += v.z, n[2] += v.y, n[3] += v.x;  // from the highest bin down
+// The sums of runs of bins, once a CTA's histogram is there; then the cluster's barrier.
+template <int THREADS, int CLUSTER>
+__device__ __forceinline__ void publish(EvictShared& s, int pass) {
+  constexpr int kPer = kBins / THREADS;
+  static_assert(kPer % 4 == 0 && kFine % kPer == 0, "bins of a thread");
+  __syncthreads();
+  uint32_t n = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(&s.hist[pass][kPer * threadIdx.x + i]);
+    n += (v.x + v.y) + (v.z + v.w);
   }
-  const uint32_t sum = n[0] + n[1] + n[2] + n[3];
-  uint32_t before = sum;
+#pragma unroll
+  for (int d = 1; d < kFine / kPer; d *= 2) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
+  if (threadIdx.x % (kFine / kPer) == 0) s.coarse[pass][threadIdx.x / (kFine / kPer)] = n;
+  cluster_sync<CLUSTER>();
+}
+
+// Of counts n held by the lanes, the higher lanes' first: the lane where the
+// `need`-th is, and how many come before it.
+__device__ __forceinline__ int lane_of_rank(uint32_t n, uint32_t need, uint32_t& before) {
+  const int lane = threadIdx.x % 32;
+  uint32_t sum = n;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, d);
-    if (lane >= d) before += v;
+    const uint32_t v = __shfl_down_sync(0xFFFFFFFFu, sum, d);
+    if (lane + d < 32) sum += v;
   }
-  if (lane == 31) s.warp[tid / 32] = before;
-  __syncthreads();
-  before -= sum;
-  for (int w = 0; w < tid / 32; ++w) before += s.warp[w];
-  if (before < need && need <= before + sum) {
-    int i = 0;
-    while (need > before + n[i]) before += n[i++];
-    s.bin = kBins - 1 - 4 * tid - i;
-    s.above = before;
+  const uint32_t at = __ballot_sync(0xFFFFFFFFu, sum >= need);  // the lanes up to the one sought
+  const int found = 31 - __clz(at);
+  before = __shfl_sync(0xFFFFFFFFu, sum - n, found);
+  return found;
+}
+
+// The bin that holds the `need`-th largest key, and how many keys lie above it:
+// a warp adds up the CTAs' sums of runs, then the bins of one run. (All bins of 16
+// CTAs were 128 KB to read for each of them, 8,000 cycles.)
+template <int CLUSTER>
+__device__ __forceinline__ void find_bin(EvictShared& s, int pass, int ctas, uint32_t need, uint32_t& bin, uint32_t& above) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    uint2 v[CLUSTER];
+    uint32_t u[CLUSTER];
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r)
+      v[r] = r < ctas ? load_remote2(remote(&s.coarse[pass][2 * lane], r)) : make_uint2(0, 0);
+    uint2 n = make_uint2(0, 0);
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) {
+      n.x += v[r].x;
+      n.y += v[r].y;
+    }
+    uint32_t before;
+    const int at = lane_of_rank(n.x + n.y, need, before);
+    const uint32_t high = __shfl_sync(0xFFFFFFFFu, n.y, at);
+    const bool low = need > before + high;
+    if (low) before += high;
+    const int run = 2 * at + (low ? 0 : 1);
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r)
+      u[r] = r < ctas ? load_remote(remote(&s.hist[pass][run * kFine + lane], r)) : 0;
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) m += u[r];
+    uint32_t more;
+    const int in_run = lane_of_rank(m, need - before, more);
+    if (lane == 0) {
+      s.bin = run * kFine + in_run;
+      s.above = before + more;
+    }
   }
   __syncthreads();
   bin = s.bin;
   above = s.above;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const __grid_constant__ EvictArgs a) {
+// PIECES of 32 bytes are a thread's share of a chunk of the move.
+template <int THREADS, int PIECES, int CTAS_PER_SM, int CLUSTER>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kv4_evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint8_t raw[];
   EvictShared& s = *reinterpret_cast<EvictShared*>(raw);
   uint32_t* const keys = reinterpret_cast<uint32_t*>(raw + sizeof(EvictShared));
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  for (int i = tid; i < 3 * kBins; i += kThreads) s.hist[0][i] = 0;
+  for (int i = tid; i < 3 * kBins; i += THREADS) s.hist[0][i] = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int item = blockIdx.x / a.ctas, rank = blockIdx.x % a.ctas;
@@ -165,63 +213,92 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const __grid_con
     const int64_t row = row_of(first + i);
     return key_of(row >= 0 ? load_global(a.weights + row) : 0.0f);
   };
-  auto key = [&](int i) -> uint32_t { return i < a.cap ? keys[i] : fresh_key(i); };
+  const bool resident = count <= a.cap;
+  // Keys i, i + step, .. of n (0 past the CTA's), from shared memory or, of a part
+  // too long for it, from global memory again.
+  auto keys_at = [&](int i, int step, auto& k) {
+    constexpr int n = sizeof(k) / sizeof(k[0]);
+    if (resident) {
+#pragma unroll
+      for (int x = 0; x < n; ++x) k[x] = i + x * step < count ? keys[i + x * step] : 0;
+    } else {
+#pragma unroll 1
+      for (int x = 0; x < n; ++x) {
+        const int j = i + x * step;
+        const uint32_t v = j >= count ? 0 : j < a.cap ? keys[j] : fresh_key(j);
+#pragma unroll
+        for (int y = 0; y < n; ++y)
+          if (y == x) k[y] = v;
+      }
+    }
+  };
+  // Counts the keys whose bits above `shift + bits` are `prefix` by the next `bits`.
+  auto count_bins = [&](uint32_t* hist, int shift, int bits, uint32_t prefix) {
+    for (int i = tid; i < count; i += kBatch * THREADS) {
+      uint32_t k[kBatch];
+      keys_at(i, THREADS, k);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        if (i + x * THREADS < count && k[x] >> (shift + bits) == prefix)
+          atomicAdd(&hist[(k[x] >> shift) & ((1u << bits) - 1)], 1u);
+    }
+  };
 
   int32_t* const list = a.list + static_cast<int64_t>(item) * a.budget;
   if (keep > 0) {
     __syncthreads();  // the histograms are clear
-    for (int i0 = tid; i0 < count; i0 += kBatch * kThreads) {
+    for (int i0 = tid; i0 < count; i0 += kBatch * THREADS) {
       int64_t row[kBatch];
       float w[kBatch];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) row[x] = i0 + x * kThreads < count ? row_of(first + i0 + x * kThreads) : -1;
+      for (int x = 0; x < kBatch; ++x) row[x] = i0 + x * THREADS < count ? row_of(first + i0 + x * THREADS) : -1;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) w[x] = row[x] >= 0 ? load_global(a.weights + row[x]) : 0.0f;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        const int i = i0 + x * kThreads;
+        const int i = i0 + x * THREADS;
         if (i >= count) break;
         const uint32_t k = key_of(w[x]);
         if (i < a.cap) keys[i] = k;
         atomicAdd(&s.hist[0][k >> 21], 1u);
       }
     }
-    uint32_t need = keep, prefix = 0, bin, above;
-    cluster_sync();
-    find_bin(s, 0, a.ctas, need, bin, above);
+    uint32_t need = keep, prefix, bin, above;
+    publish<THREADS, CLUSTER>(s, 0);
+    find_bin<CLUSTER>(s, 0, a.ctas, need, bin, above);
     need -= above;
     prefix = bin;
-    for (int i = tid; i < count; i += kThreads) {
-      const uint32_t k = key(i);
-      if (k >> 21 == prefix) atomicAdd(&s.hist[1][(k >> 10) & 2047], 1u);
-    }
-    cluster_sync();
-    find_bin(s, 1, a.ctas, need, bin, above);
+    count_bins(s.hist[1], 10, 11, prefix);
+    publish<THREADS, CLUSTER>(s, 1);
+    find_bin<CLUSTER>(s, 1, a.ctas, need, bin, above);
     need -= above;
     prefix = prefix << 11 | bin;
-    for (int i = tid; i < count; i += kThreads) {
-      const uint32_t k = key(i);
-      if (k >> 10 == prefix) atomicAdd(&s.hist[2][k & 1023], 1u);
-    }
-    cluster_sync();
-    find_bin(s, 2, a.ctas, need, bin, above);
+    count_bins(s.hist[2], 0, 10, prefix);
+    publish<THREADS, CLUSTER>(s, 2);
+    find_bin<CLUSTER>(s, 2, a.ctas, need, bin, above);
     need -= above;  // of the keys equal to the least one kept, so many stay
     const uint32_t least = prefix << 10 | bin;
 
     // Their places: each warp counts a contiguous run, then numbers it.
-    const int run = ((count + kThreads - 1) / kThreads) * 32;
+    constexpr int kSteps = 4;  // of 32 keys, side by side
+    const int run = ((count + THREADS * kSteps - 1) / (THREADS * kSteps)) * 32 * kSteps;
     const int from = min(warp * run, count), to = min(from + run, count);
     uint2 n = make_uint2(0, 0);
-    for (int i = from; i < to; i += 32) {
-      const uint32_t k = i + lane < to ? key(i + lane) : 0;
-      n.x += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < to && k > least));
-      n.y += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < to && k == least));
+    for (int i = from; i < to; i += 32 * kSteps) {
+      uint32_t k[kSteps];
+      keys_at(i + lane, 32, k);
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        const bool in = i + 32 * x + lane < to;
+        n.x += __popc(__ballot_sync(0xFFFFFFFFu, in && k[x] > least));
+        n.y += __popc(__ballot_sync(0xFFFFFFFFu, in && k[x] == least));
+      }
     }
     if (lane == 0) s.counts[warp] = n;
     __syncthreads();
     if (tid == 0) {
       uint2 t = make_uint2(0, 0);
-      for (int w = 0; w < kThreads / 32; ++w) {
+      for (int w = 0; w < THREADS / 32; ++w) {
         const uint2 v = s.counts[w];
         s.counts[w] = t;
         t.x += v.x;
@@ -229,29 +306,32 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const __grid_con
       }
       s.total = t;
     }
-    cluster_sync();
-    n = s.counts[warp];
-    for (int r = 0; r < rank; ++r) {
-      const uint2 v = load_remote2(remote(&s.total, r));
-      n.x += v.x;
-      n.y += v.y;
-    }
+    cluster_sync<CLUSTER>();
+    // What the CTAs before this one have: a lane each.
+    n = lane < rank ? load_remote2(remote(&s.total, lane)) : make_uint2(0, 0);
+    n.x = __reduce_add_sync(0xFFFFFFFFu, n.x) + s.counts[warp].x;
+    n.y = __reduce_add_sync(0xFFFFFFFFu, n.y) + s.counts[warp].y;
     const uint32_t below = (1u << lane) - 1;
-    for (int i = from; i < to; i += 32) {
-      const uint32_t k = i + lane < to ? key(i + lane) : 0;
-      const uint32_t more = __ballot_sync(0xFFFFFFFFu, i + lane < to && k > least);
-      const uint32_t same = __ballot_sync(0xFFFFFFFFu, i + lane < to && k == least);
-      const uint32_t equal = n.y + __popc(same & below);
-      const uint32_t place = n.x + __popc(more & below) + min(equal, need);
-      if ((more >> lane & 1) || ((same >> lane & 1) && equal < need)) list[a.sink + place] = first + i + lane;
-      n.x += __popc(more);
-      n.y += __popc(same);
+    for (int i = from; i < to; i += 32 * kSteps) {
+      uint32_t k[kSteps];
+      keys_at(i + lane, 32, k);
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        const int at = i + 32 * x + lane;
+        const uint32_t more = __ballot_sync(0xFFFFFFFFu, at < to && k[x] > least);
+        const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < to && k[x] == least);
+        const uint32_t equal = n.y + __popc(same & below);
+        const uint32_t place = n.x + __popc(more & below) + min(equal, need);
+        if ((more >> lane & 1) || ((same >> lane & 1) && equal < need)) list[a.sink + place] = first + at;
+        n.x += __popc(more);
+        n.y += __popc(same);
+      }
     }
-    cluster_sync();
+    cluster_sync<CLUSTER>();
   }
 
   // The move. A token's codes are `lanes` pieces, one to a lane: its key's first.
-  const int lanes = a.c.D / 32, piece = tid % lanes, tokens = kThreads * kPieces / lanes;
+  const int lanes = a.c.D / 32, piece = tid % lanes, tokens = THREADS * PIECES / lanes;
   const int newest = a.budget - a.recent, shift = len - a.budget;
   uint8_t* const codes = (piece < lanes / 2 ? a.c.k : a.c.v) + piece % (lanes / 2) * 32;
   auto codes_at = [&](int page, int slot) {
@@ -260,44 +340,46 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const __grid_con
   // Beside its codes a lane moves the key's scale (the first lane), the value's
   // (the second) and the weight (the last).
   uint16_t* const scales = piece == 0 ? a.c.k_scale4 : a.c.v_scale4;
-  for (int base = a.sink; base < a.budget; base += a.ctas * tokens) {
-    const int mine = base + rank * tokens + tid / lanes;
-    int src[kPieces], from[kPieces], to[kPieces];
-    Piece data[kPieces];
-    uint16_t scale[kPieces];
-    float weight[kPieces];
+  int src[PIECES], from[PIECES];
+  auto look_up = [&](int mine) {  // where the pieces of a chunk come from
 #pragma unroll
-    for (int r = 0; r < kPieces; ++r) {
-      const int slot = mine + r * (kThreads / lanes);
+    for (int r = 0; r < PIECES; ++r) {
+      const int slot = mine + r * (THREADS / lanes);
       src[r] = slot >= a.budget ? slot : slot >= newest ? slot + shift : __ldcg(list + slot);
     }
 #pragma unroll
-    for (int r = 0; r < kPieces; ++r) {
-      const int slot = mine + r * (kThreads / lanes);
-      from[r] = to[r] = -1;
-      if (src[r] != slot) {
-        from[r] = page_of(src[r]);
-        to[r] = page_of(slot);
-      }
+    for (int r = 0; r < PIECES; ++r) from[r] = src[r] != mine + r * (THREADS / lanes) ? page_of(src[r]) : -1;
+  };
+  int mine = a.sink + rank * tokens + tid / lanes;
+  look_up(mine);
+  for (int base = a.sink; base < a.budget; base += a.ctas * tokens) {
+    Piece data[PIECES];
+    uint16_t scale[PIECES];
+    float weight[PIECES];
+    uint32_t moves = 0;
+#pragma unroll
+    for (int r = 0; r < PIECES; ++r) {
+      if (from[r] < 0) continue;
+      moves |= 1u << r;
+      data[r] = load_piece(codes_at(from[r], src[r]));
+      const int64_t row = row_in(from[r], src[r]);
+      if (piece < 2) scale[r] = scales[row];
+      if (piece == lanes - 1) weight[r] = load_global(a.weights + row);
     }
+    const int now = mine;
+    mine += a.ctas * tokens;
+    if (base + a.ctas * tokens < a.budget) look_up(mine);
+    cluster_sync<CLUSTER>();
 #pragma unroll
-    for (int r = 0; r < kPieces; ++r)
-      if (from[r] >= 0 && to[r] >= 0) {
-        data[r] = load_piece(codes_at(from[r], src[r]));
-        const int64_t row = row_in(from[r], src[r]);
-        if (piece < 2) scale[r] = scales[row];
-        if (piece == lanes - 1) weight[r] = load_global(a.weights + row);
-      }
-    cluster_sync();
-#pragma unroll
-    for (int r = 0; r < kPieces; ++r)
-      if (from[r] >= 0 && to[r] >= 0) {
-        const int slot = mine + r * (kThreads / lanes);
-        store_piece(codes_at(to[r], slot), data[r]);
-        const int64_t row = row_in(to[r], slot);
-        if (piece < 2) scales[row] = scale[r];
-        if (piece == lanes - 1) a.weights[row] = weight[r];
-      }
+    for (int r = 0; r < PIECES; ++r) {
+      if (!(moves >> r & 1)) continue;
+      const int slot = now + r * (THREADS / lanes), to = page_of(slot);
+      if (to < 0) continue;
+      store_piece(codes_at(to, slot), data[r]);
+      const int64_t row = row_in(to, slot);
+      if (piece < 2) scales[row] = scale[r];
+      if (piece == lanes - 1) a.weights[row] = weight[r];
+    }
   }
   if (bad) atomicOr(a.status, kErrCacheIndex);
   // An attention next on the stream may start early and reads codes by bulk copies.
@@ -310,6 +392,38 @@ size_t kv4_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t budget) {
   if (B < 0 || Hkv < 1 || budget < 1) return 0;
   return sizeof(int32_t) * static_cast<size_t>(B) * Hkv * budget;
 }
+
+namespace {
+
+template <int THREADS, int PIECES, int CTAS_PER_SM, int CLUSTER>
+cudaError_t evict_form(const EvictArgs& a, int64_t items, int device, cudaStream_t stream) {
+  const auto kernel = kv4_evict_kernel<THREADS, PIECES, CTAS_PER_SM, CLUSTER>;
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << device;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(EvictShared) + sizeof(uint32_t) * kMaxKeys));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * a.ctas));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sizeof(EvictShared) + sizeof(uint32_t) * a.cap;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(a.ctas), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e == cudaSuccess) plan_add("kv4_evict_kernel");
+  return e;
+}
+
+}  // namespace
 
 cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cudaStream_t stream) {
   EvictArgs a{};
@@ -327,35 +441,14 @@ cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cu
   // more of the longest sequence there can be.
   const int64_t items = static_cast<int64_t>(p.cache.B) * p.cache.Hkv;
   const int64_t longest = static_cast<int64_t>(p.cache.max_blocks) * p.cache.block;
-  a.ctas = 16;
+  a.ctas = kMaxCluster;
   while (a.ctas > 1 && (items * a.ctas > 2 * dev.sm_count || longest < 1024 * a.ctas)) a.ctas /= 2;
   a.cap = static_cast<int32_t>(std::min<int64_t>((longest + a.ctas - 1) / a.ctas, kMaxKeys));
-  const size_t smem = sizeof(EvictShared) + sizeof(uint32_t) * a.cap;
-  static std::atomic<uint64_t> ready{0};
-  const uint64_t bit = 1ull << dev.id;
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sizeof(EvictShared) + sizeof(uint32_t) * kMaxKeys));
-    if (e != cudaSuccess) return e;
-    const cudaError_t e2 = cudaFuncSetAttribute(kv4_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e2 != cudaSuccess) return e2;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * a.ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(a.ctas), 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel, a);
-  if (e == cudaSuccess) plan_add("kv4_evict_kernel");
-  return e;
+  // Many items: small CTAs, two an SM, whose phases overlap (64 x 8 items of 4,160
+  // tokens 120 us; four an SM with half the pieces 159, one of 512 threads 138). Few:
+  // larger ones (8 items of 131,072 tokens 56 us, with 256 threads 80).
+  if (a.ctas == 1) return evict_form<256, 8, 2, 1>(a, items, dev.id, stream);
+  return evict_form<512, 8, 1, kMaxCluster>(a, items, dev.id, stream);
 }
 
 }  // namespace qsa
