@@ -540,8 +540,8 @@ qsa_status qsa_kv4_read(const qsa_kv4_cache* cache, int32_t n, qsa_dtype dtype, 
 /*
  * qsa_kv4_attend - attention of the n rows over the 4-bit cache, whole (ids
  * NULL) or over chosen blocks. Everything is as for qsa_kv_attend, with slots
- * for positions, but: at most 16 query heads on a KV head where D is 64; a NaN
- * scale makes every dimension of the rows that see its token NaN.
+ * for positions, but a NaN scale makes every dimension of the rows that see its
+ * token NaN.
  */
 size_t qsa_kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
 qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,

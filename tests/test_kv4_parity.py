@@ -206,10 +206,11 @@ def test_attend_heads(tbs, Hq, Hkv, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-def test_attend_32_heads_on_one(tbs, dtype):
-    check_attend(tbs, [300, 5], 2, 32, 1, 128, 64, dtype)
-    with pytest.raises(tbs.QsaError):
-        check_attend(tbs, [300, 5], 2, 32, 1, 64, 64, dtype)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("R", [9, 20, 24, 31, 32])
+def test_attend_many_heads_on_one(tbs, R, D, dtype):
+    check_attend(tbs, [300, 5], 2, R, 1, D, 64, dtype, seed=R)
+    check_attend(tbs, [300, 45], 1, 2 * R, 2, D, 32, dtype, ids=(2, 3), seed=R)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -321,6 +322,13 @@ def test_weights_rows_that_are_not_there(tbs):
     check_weights(tbs, [70, 41, 3, 0, 130], 9, 4, 1, 128, 64, "f16", 0.5, n_new=[0, 4, 9, 9, 1])
     check_weights(tbs, [70, 41, 3, 0, 130], 9, 4, 1, 64, 64, "bf16", 0.0, n_new=[0, 4, 9, 9, 1])
     check_weights(tbs, [300], 32, 32, 1, 128, 64, "f16", 0.0)
+
+
+@pytest.mark.parametrize("R", [11, 24, 31, 32])
+@pytest.mark.parametrize("n", [1, 5])
+def test_weights_many_heads_on_one(tbs, R, n):
+    check_weights(tbs, [300, 40], n, R, 1, 64, 64, "f16", 1.0, seed=R)
+    check_weights(tbs, [300, 40], n, 2 * R, 2, 128, 32, "bf16", 1.0, seed=R)
 
 
 # ------------------------------------------------------------------- evict

@@ -689,8 +689,7 @@ def qsa_kv4_attend_workspace_bytes(B: int, n: int, Hq: int, Hkv: int, D: int) ->
 
 def qsa_kv4_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids=None, scale=None, n_new=None,
                    out=None, lse=None, workspace=None):
-    """qsa_kv_attend over the 4-bit cache (at most 16 query heads on a KV head
-    where D is 64); workspace: a CUDA uint8 tensor of
+    """qsa_kv_attend over the 4-bit cache; workspace: a CUDA uint8 tensor of
     qsa_kv4_attend_workspace_bytes, allocated here when not given."""
     r = (_KV or _kv_binding()).attend4(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, ids, scale, n_new, out,
                                        lse, workspace)

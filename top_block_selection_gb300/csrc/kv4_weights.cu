@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_after_sync();
   pdl_launch_dependents();
 
-  const int n_groups = (a.n + a.qt - 1) / a.qt;  // of rows, a.qt queries each
+  const int n_groups = (a.n + a.qt - 1) / a.qt * a.split;  // of rows: a.qt queries, a.R heads
   const int passes = (n_groups + kGroups - 1) / kGroups;
   const int per_pass = min(n_groups, kGroups);
 
@@ -419,7 +419,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           GroupRows<C>& rows = s.rows[buf][gr];
           Entry en{};
           en.b = b;
-          en.j0 = (pass * kGroups + gr) * a.qt;
+          const int group = pass * kGroups + gr;
+          const int item = h * a.split + group % a.split;  // its heads are item * a.R ..
+          en.j0 = group / a.split * a.qt;
           en.nq = min(en.j0 + a.qt, q.n_new) - en.j0;
           en.first_pos = q.first + en.j0;
           // (A lane's row as query_rows has it.)
@@ -427,8 +429,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const bool there = lane < kRows && row < a.qt * a.R && j < en.nq && en.first_pos + j >= 0;
           float lse = -INFINITY;
           if (there)
-            lse = load_global(w.lse + (static_cast<int64_t>(b) * a.n + en.j0 + j) * a.Hq + h * a.R + (row - j * a.R));
-          query_rows<C, kRows>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, h, r0, 1);
+            lse = load_global(w.lse + (static_cast<int64_t>(b) * a.n + en.j0 + j) * a.Hq + item * a.R + (row - j * a.R));
+          query_rows<C, kRows>(a, rows.info, q_smem + (buf * kGroups + gr) * C::kQBytes, en, item, r0, 1);
           __syncwarp();
           if (lane < kRows) {
             const bool gives = there && lse != -INFINITY;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           __syncwarp();
         }
         // The first position that not all of the pass's rows see.
-        if (warp == C::kFirstQuery && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups * a.qt, 0) : -1;
+        if (warp == C::kFirstQuery && lane == 0) s.rows[buf][0].info.lo_pos = q.n_new > 0 ? max(q.first + pass * kGroups / a.split * a.qt, 0) : -1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_full[buf]);
@@ -494,7 +496,9 @@ cudaError_t launch_kv4_weights(const Kv4WeightsProblem& p, const DeviceInfo& dev
   const int columns = 128 / p.cache.D;  // of a row: one for each token of an operand row
   a.tile_log2 = columns == 2 ? 8 : 7;
   a.spt = (1 << a.tile_log2) / p.cache.block;
-  a.qt = std::min(p.n, std::max(1, 32 / (a.R * columns)));
+  a.split = head_split(a.R, columns, 32);
+  a.R /= a.split;
+  a.qt = std::min(p.n, 32 / (a.R * columns));
   w.lse = p.lse;
   w.weights = p.weights;
   w.decay = p.decay;
@@ -505,7 +509,7 @@ cudaError_t launch_kv4_weights(const Kv4WeightsProblem& p, const DeviceInfo& dev
   const int grid = static_cast<int>(std::min<int64_t>(dev.sm_count, most));
   CUtensorMap tk;
   if (!encode_cache_map4(&tk, p.cache.k, p.cache)) return cudaErrorInvalidValue;
-  const int rt = a.qt * a.R * columns;
+  const int rt = a.split > 1 ? 32 : a.qt * a.R * columns;
   if (p.cache.D == 64)
     return p.bf16 ? weights_rows<64, 2>(rt, tk, w, grid, dev.id, stream)
                   : weights_rows<64, 3>(rt, tk, w, grid, dev.id, stream);

@@ -96,8 +96,8 @@ bool encode_cache_map(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D, int group) {
-  if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > group || (D != 64 && D != 128)) return 0;
+size_t workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kKvMaxGroup || (D != 64 && D != 128)) return 0;
   const size_t rows = takes_many(B, n, Hq, Hkv) ? 2 * kManyRows : kKvMaxGroup;
   return sizeof(float) * 2 * kKvMaxCtas * rows * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
 }
@@ -115,6 +115,7 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   a.n = p.n;
   a.Hq = p.Hq;
   a.R = p.Hq / p.cache.Hkv;
+  a.split = 1;
   a.n_lists = p.n_lists;
   a.k = p.k;
   a.bf16 = p.bf16;
@@ -125,6 +126,15 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   // column for each of the two tokens in an operand row.
   const bool many = !p.ids && takes_many(p.cache.B, p.n, p.Hq, p.cache.Hkv);
   const int columns = four && !many ? 128 / p.cache.D : 1;
+  if (four && !many && a.R * columns > 16) {
+    // The form of 32 columns takes four times as long a tile as that of 16: the heads
+    // are split over two items (or more, where two equal parts do not do it or there
+    // are none), which read the same tiles at about the same time, from L2.
+    const int fine = head_split(a.R, columns, 16), least = head_split(a.R, columns, 32);
+    a.split = fine <= 2 * least ? fine : least;
+    a.R /= a.split;
+  }
+  a.heads = p.cache.Hkv * a.split;
   a.tile_log2 = columns == 2 ? 8 : 7;
   a.spt = (1 << a.tile_log2) / p.cache.block;
   a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / (a.R * columns)));
@@ -133,7 +143,7 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   const int rt = rows_form(a.qt * a.R * columns);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
   const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
-  const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * p.cache.Hkv * item_tiles;
+  const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * a.heads * item_tiles;
   const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sm_count, kKvMaxCtas), most));
   // (No item costs more than another where a CTA has a tile or two.)
   a.item_cost = many ? kManyItemCost : p.ids || most <= 2 * grid ? 0 : kItemCost;
@@ -175,11 +185,17 @@ bool encode_cache_map4(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int head_split(int R, int per_row, int columns) {
+  int s = 1;
+  while (R % s != 0 || R / s * per_row > columns) ++s;
+  return s;
+}
+
 size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
-  return workspace_bytes(B, n, Hq, Hkv, D, kKvMaxGroup);
+  return workspace_bytes(B, n, Hq, Hkv, D);
 }
 size_t kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
-  return workspace_bytes(B, n, Hq, Hkv, D, D == 64 ? kKvMaxGroup / 2 : kKvMaxGroup);
+  return workspace_bytes(B, n, Hq, Hkv, D);
 }
 
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {

@@ -84,7 +84,8 @@ struct AttendArgs {
   int32_t* jobs;     // [grid][4]: entry, head, last CTA of an item that this CTA begins and others end; or -1
   uint32_t* status;
   float scale_log2;
-  int32_t n, Hq, R;
+  int32_t n, Hq, R;  // R: query heads of an item
+  int32_t heads, split;  // items of a query tile: `split` of them on each KV head
   int32_t qt, n_qt;  // queries of a tile, query tiles of a sequence
   int32_t n_lists, k;
   int32_t spt;       // blocks of a tile
@@ -496,6 +497,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
       en_of = w.e;
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
+    const int kv = C::kFour && a.split > 1 ? w.h / a.split : w.h;  // the item's KV head
     const int first = (W - g0 % W + p) % W;  // this warpgroup's tiles: first, first + W, ...
     const int own = part > first ? (part - first + W - 1) / W : 0;
     const int cap = a.c.max_blocks * a.c.block;
@@ -503,7 +505,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
     const int keys = min(en.last_pos + 1, cap);
     const int32_t* list = nullptr;
     if (a.ids)
-      list = a.ids + ((static_cast<int64_t>(en.b) * a.n_lists + (a.n_lists > 1 ? w.h : 0)) * a.n + en.j0) * a.k;
+      list = a.ids + ((static_cast<int64_t>(en.b) * a.n_lists + (a.n_lists > 1 ? kv : 0)) * a.n + en.j0) * a.k;
     const int32_t* table = a.c.page_table + static_cast<int64_t>(en.b) * a.c.max_blocks;
     for (int k0 = 0; k0 < own && ok; k0 += per_batch) {
       const int slot = (w.t + first + (k0 + my_k) * W) * spt + my_slot;
@@ -522,13 +524,13 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
       }
       float ks = 0.0f, vs = 0.0f;
       if (!C::kFour && page >= 0) {
-        ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
-        vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + w.h);
+        ks = load_global(a.c.k_scale + static_cast<int64_t>(page) * a.c.Hkv + kv);
+        vs = load_global(a.c.v_scale + static_cast<int64_t>(page) * a.c.Hkv + kv);
       }
       const int z = page >= 0 ? page : a.c.n_pages;  // no block: reads past the last page give zeros
       const int base = page >= 0 ? blk * a.c.block : kKvNoToken;
       const int tiles = min(per_batch, own - k0);
-      const int y = uniform(w.h * a.c.block / C::PAR), slab = a.c.block * C::HD;
+      const int y = uniform(kv * a.c.block / C::PAR), slab = a.c.block * C::HD;
       // The scales of a lane's 4 (or 8) tokens of tile i, asked for a tile ahead.
       using Scales = typename std::conditional<C::PAR == 2, uint4, uint2>::type;
       Scales next_k{}, next_v{};
@@ -537,7 +539,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
         const int of = __shfl_sync(0xFFFFFFFFu, page, from & 31), at = __shfl_sync(0xFFFFFFFFu, base, from & 31);
         next_k = next_v = Scales{};
         if (i >= tiles || of < 0) return;
-        const int64_t row = (static_cast<int64_t>(of) * a.c.Hkv + w.h) * a.c.block + in_block;
+        const int64_t row = (static_cast<int64_t>(of) * a.c.Hkv + kv) * a.c.block + in_block;
         next_k = load_global(reinterpret_cast<const Scales*>(a.c.k_scale4 + row));
         next_v = load_global(reinterpret_cast<const Scales*>(a.c.v_scale4 + row));
         const int over = at + in_block + 4 * C::PAR - keys;  // tokens that no row sees
@@ -602,7 +604,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
     }
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, kErrCacheIndex);
     g0 += part;
-    step(w, part, en.tiles, a.c.Hkv, a.item_cost);
+    step(w, part, en.tiles, a.heads, a.item_cost);
   }
   if (!ok) {  // let the copies in flight land before the CTA gives its memory back
     const uint32_t n = min(last, static_cast<uint32_t>(C::kStages / W));
@@ -755,7 +757,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       if (lane == 0) mbar_arrive(&s.q_full[buf]);
     }
     at += w.t + part + a.item_cost;
-    step(w, part, en.tiles, a.c.Hkv, a.item_cost);
+    step(w, part, en.tiles, a.heads, a.item_cost);
   }
 }
 
@@ -1245,7 +1247,7 @@ template <int kThreads, int kFirst, int kBarrier>
 __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, Start& shared, Start& start,
                                            int64_t& total, int64_t& lo, int64_t& hi, int& grid) {
   const int tid = threadIdx.x - kFirst, warp = tid / 32, lane = tid % 32;
-  const int entries = a.c.B * a.n_qt, heads = a.c.Hkv;
+  const int entries = a.c.B * a.n_qt, heads = a.heads;
   auto share = [&](int64_t tiles) {
     total = tiles * heads;
     grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
@@ -1431,6 +1433,9 @@ cudaError_t attend_form(const CUtensorMap& tk, const CUtensorMap& tv, const Atte
 
 // The tensor map of the 4-bit cache's keys or values (kv_attend.cu).
 bool encode_cache_map4(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c);
+// Into how many items the R query heads of a KV head are split, for at most
+// `columns` columns an item: the smallest divisor of R that does it.
+int head_split(int R, int per_row, int columns);
 
 // All row counts of one head size and term count (kv_attend_d*_t*.cu).
 template <int D, int T, bool FOUR = false>

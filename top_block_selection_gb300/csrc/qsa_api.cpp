@@ -268,18 +268,18 @@ static qsa_status run_append(const Cache* cache, const qsa_rows* k, const qsa_ro
   return from_cuda(launch(p, *dev, as_cuda(stream)));
 }
 
-// Both attentions; at most `group` query heads on a KV head.
+// Both attentions.
 template <class Cache, class Bytes, class Launch>
 static qsa_status run_attend(const Cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
                              float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
-                             void* workspace, size_t workspace_bytes, qsa_stream_t stream, int group, Bytes bytes,
+                             void* workspace, size_t workspace_bytes, qsa_stream_t stream, Bytes bytes,
                              Launch launch) {
   qsa_status st = check_cache_sizes(cache, n);
   if (st != QSA_OK) return st;
   if (Hq < 1 || (dtype != QSA_F16 && dtype != QSA_BF16)) return QSA_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0) return QSA_ERR_INVALID_ARG;
   if (ids && (k < 1 || (n_lists != 1 && n_lists != cache->Hkv))) return QSA_ERR_INVALID_ARG;
-  if (Hq / cache->Hkv > group || (ids && k > (1 << 20))) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (Hq / cache->Hkv > qsa::kKvMaxGroup || (ids && k > (1 << 20))) return QSA_ERR_UNSUPPORTED_GEOMETRY;
   if (cache->B == 0 || n == 0) return QSA_OK;
   if (!(scale - scale == 0.0f)) return QSA_ERR_INVALID_ARG;
   if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
@@ -305,10 +305,6 @@ static qsa_status run_attend(const Cache* cache, const qsa_rows* q, int32_t n, i
   if ((st = device_or_error(&dev)) != QSA_OK) return st;
   return from_cuda(launch(p, *dev, as_cuda(stream)));
 }
-
-// Query heads on a KV head of the 4-bit cache: two tokens of 64 dimensions share
-// a row of the operand, which doubles a tile's columns.
-static int kv4_group(const qsa_kv4_cache* c) { return c && c->D == 64 ? qsa::kKvMaxGroup / 2 : qsa::kKvMaxGroup; }
 
 extern "C" {
 
@@ -692,14 +688,14 @@ qsa_status qsa_kv_attend(const qsa_kv_cache* cache, const qsa_rows* q, int32_t n
                          float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, qsa_stream_t stream) {
   return run_attend(cache, q, n, Hq, dtype, scale, ids, n_lists, k, out, lse, workspace, workspace_bytes, stream,
-                    qsa::kKvMaxGroup, qsa::kv_attend_workspace_bytes, qsa::launch_kv_attend);
+                    qsa::kv_attend_workspace_bytes, qsa::launch_kv_attend);
 }
 
 qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
                           float scale, const int32_t* ids, int32_t n_lists, int32_t k, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, qsa_stream_t stream) {
   return run_attend(cache, q, n, Hq, dtype, scale, ids, n_lists, k, out, lse, workspace, workspace_bytes, stream,
-                    kv4_group(cache), qsa::kv4_attend_workspace_bytes, qsa::launch_kv4_attend);
+                    qsa::kv4_attend_workspace_bytes, qsa::launch_kv4_attend);
 }
 
 qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq, qsa_dtype dtype,
@@ -708,7 +704,7 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
   if (st != QSA_OK) return st;
   if (Hq < 1 || (dtype != QSA_F16 && dtype != QSA_BF16)) return QSA_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0) return QSA_ERR_INVALID_ARG;
-  if (Hq / cache->Hkv > kv4_group(cache)) return QSA_ERR_UNSUPPORTED_GEOMETRY;
+  if (Hq / cache->Hkv > qsa::kKvMaxGroup) return QSA_ERR_UNSUPPORTED_GEOMETRY;
   if (cache->B == 0 || n == 0) return QSA_OK;
   if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f) || decay < 0.0f) return QSA_ERR_INVALID_ARG;
   if ((st = check_cache_pointers(cache, false)) != QSA_OK) return st;
