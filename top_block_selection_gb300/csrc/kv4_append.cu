@@ -3,9 +3,13 @@
 // Each new token's key (rotated as in kv_append.cu) and value have, for each KV
 // head, a scale of their own, the smallest bf16 s with max|x| <= 6 s, and the
 // codes e2m1(x / s), the quotient rounded to fp32 first. That changes no code:
-// a border between two codes is a number of at most three bits, and s times it
-// is an fp32 number, so that x / s is either the border itself, exactly, or off
-// by more than the quotient's rounding. A token's codes depend on that token
+// a border T between two codes is a number of at most three bits, and s T is an
+// fp32 number, so that x / s is T itself, exactly, or off by more than half an
+// fp32 step: x differs from s T by a step of its own, and the 8 bits of s keep its
+// mantissa below 2 - 2^-7. The quotient is x times the reciprocal of s, corrected
+// by its remainder (Markstein): within 2^-47 before its one rounding, at two
+// operations more than the product (a division each took 2 us more for 4,096
+// tokens). A token's codes depend on that token
 // alone: nothing that is in the cache is touched again.
 //
 // The block key is the mean of the block's stored keys. Products of a code and
@@ -23,17 +27,24 @@ namespace qsa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // tokens of a thread whose loads are in flight together
+// One token of a thread at a time and 8 CTAs an SM: 4,096 tokens 19.6 us, a token of
+// each of 64 requests 5.8 (two tokens in flight, which spills, 19.6 and 6.4, at 6
+// CTAs an SM 21.2 and 5.5; four and 6, with divisions, 23.8 and 7.9).
+constexpr int kCtasPerSm = 8;
 
-__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float s) {
+// inv is 1 / s, rounded.
+__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float s, float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  for (int i = 0; i < 8; ++i) {
+    const float q = x[i] * inv;
+    y[i] = copysignf(fmaf(fmaf(-q, s, x[i]), inv, q), x[i]);  // (the sign of a zero)
+  }
   return e2m1x8(y);
 }
 
 template <int TPT, bool BF16, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 6) kv4_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_wait();
   pdl_launch_dependents();  // after the wait: at most one kernel ahead of the one that runs
   if (static_cast<int64_t>(blockIdx.x) >= a.units) {
@@ -67,10 +78,6 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_append_kernel(const __grid_co
   }
   int page = -1;
   if (blk64 < a.c.max_blocks) page = load_global(a.c.page_table + static_cast<int64_t>(b) * a.c.max_blocks + blk64);
-  if (page < 0 || page >= a.c.n_pages) {
-    if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
-    return;
-  }
 
   const int start = static_cast<int>(start64), held = static_cast<int>(end64) - start;
   const int n_old = max(p0 - start, 0);
@@ -78,66 +85,70 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_append_kernel(const __grid_co
   const int64_t in = b * src.sb + h * src.sh + (static_cast<int64_t>(start) - sp.first) * src.sn;
   const int sub = threadIdx.x % TPT, tok = threadIdx.x / TPT;
   const Lane l = lane_of<TPT>(sub, is_v ? 0 : a.rot, PAIRS);
-  uint8_t* const codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * (D / 2);
-  uint16_t* const scales =
-      (is_v ? a.c.v_scale4 : a.c.k_scale4) + (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block;
   const bool want_kb = a.kb != nullptr && !is_v;
 
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
   // A pass of slots that hold only older tokens matters to the block key alone.
-  for (int s0 = want_kb ? 0 : n_old / kTokens * kTokens; s0 < held; s0 += kBatch * kTokens) {
-    uint4 raw[kBatch][2];
+  for (int slot = (want_kb ? 0 : n_old / kTokens * kTokens) + tok; slot - tok < held; slot += kTokens) {
+    const bool fresh = slot >= n_old && slot < held;
+    uint4 raw0, raw1;
+    if (fresh) {
+      const int64_t row = in + static_cast<int64_t>(slot) * src.sn;
+      raw0 = load8(src.data, row + l.off0);
+      raw1 = load8(src.data, row + l.off1);
+    }
+    // The page is waited for only now, with the new tokens on their way.
+    if (page < 0 || page >= a.c.n_pages) {
+      if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
+      return;
+    }
+    uint8_t* const codes =
+        (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + (static_cast<int64_t>(h) * a.c.block + slot) * (D / 2);
+    uint16_t* const scale =
+        (is_v ? a.c.v_scale4 : a.c.k_scale4) + (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block + slot;
+    uint32_t c0 = 0, c1 = 0, top = 0;
+    float s = 0.0f, x[8], y[8];
+    if (slot < n_old && want_kb) {
+      c0 = load_global(reinterpret_cast<const uint32_t*>(codes + l.off0 / 2));
+      c1 = load_global(reinterpret_cast<const uint32_t*>(codes + l.off1 / 2));
+      s = load_scale(scale);
+    }
+    if (fresh) {
+      unpack8<BF16>(raw0, x);
+      unpack8<BF16>(raw1, y);
+      if (l.turns) rotate<PAIRS>(a.cos, a.sin, (ahead + start + slot) * (a.rot / 2), l, x, y);
+      // Magnitudes order as their bits, NaN above all.
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int slot = s0 + t * kTokens + tok;
-      if (slot >= held) continue;
-      if (slot >= n_old) {
-        const int64_t row = in + static_cast<int64_t>(slot) * src.sn;
-        raw[t][0] = load8(src.data, row + l.off0);
-        raw[t][1] = load8(src.data, row + l.off1);
-      } else if (want_kb) {
-        raw[t][0].x = load_global(reinterpret_cast<const uint32_t*>(codes + slot * (D / 2) + l.off0 / 2));
-        raw[t][0].y = load_global(reinterpret_cast<const uint32_t*>(codes + slot * (D / 2) + l.off1 / 2));
-        raw[t][0].z = __float_as_uint(load_scale(scales + slot));
-      }
+      for (int e = 0; e < 8; ++e)
+        top = max(top, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
     }
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int slot = s0 + t * kTokens + tok;
-      const bool fresh = slot >= n_old && slot < held;
-      float x[8], y[8];
-      uint32_t top = 0;
-      if (fresh) {
-        unpack8<BF16>(raw[t][0], x);
-        unpack8<BF16>(raw[t][1], y);
-        if (l.turns) rotate<PAIRS>(a.cos, a.sin, (ahead + start + slot) * (a.rot / 2), l, x, y);
-        // Magnitudes order as their bits, NaN above all.
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          top = max(top, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
-      }
-#pragma unroll
-      for (int d = 1; d < TPT; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      uint32_t c0 = raw[t][0].x, c1 = raw[t][0].y;
-      float s = __uint_as_float(raw[t][0].z);
-      if (fresh) {
-        s = token_scale(top);
-        c0 = isnan(s) ? 0u : encode8(x, s);
-        c1 = isnan(s) ? 0u : encode8(y, s);
-        *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + l.off0 / 2) = c0;
-        *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + l.off1 / 2) = c1;
-        if (sub == 0) scales[slot] = static_cast<uint16_t>(__float_as_uint(s) >> 16);
-      }
-      if (want_kb && slot < held) {
-        e2m1x8_to_float(c0, x);
-        e2m1x8_to_float(c1, y);
+    for (int d = 1; d < TPT; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (fresh) {
+      s = token_scale(top);
+      if (top == 0x7F800000u) {  // infinities to the largest finite float: code 6
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          acc[e] = fmaf(x[e], s, acc[e]);
-          acc[8 + e] = fmaf(y[e], s, acc[8 + e]);
+          x[e] = fminf(fmaxf(x[e], -3.402823466e38f), 3.402823466e38f);
+          y[e] = fminf(fmaxf(y[e], -3.402823466e38f), 3.402823466e38f);
         }
+      }
+      const float inv = __frcp_rn(s);
+      c0 = isnan(s) ? 0u : encode8(x, s, inv);
+      c1 = isnan(s) ? 0u : encode8(y, s, inv);
+      *reinterpret_cast<uint32_t*>(codes + l.off0 / 2) = c0;
+      *reinterpret_cast<uint32_t*>(codes + l.off1 / 2) = c1;
+      if (sub == 0) *scale = static_cast<uint16_t>(__float_as_uint(s) >> 16);
+    }
+    if (want_kb && slot < held) {
+      e2m1x8_to_float(c0, x);
+      e2m1x8_to_float(c1, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[e] = fmaf(x[e], s, acc[e]);
+        acc[8 + e] = fmaf(y[e], s, acc[8 + e]);
       }
     }
   }
