@@ -74,8 +74,8 @@ __device__ __forceinline__ Sequence sequence_of(const AttendArgs& a, int b) {
 
 template <class C>
 struct GroupRows {
-  ItemInfo<C::RT> info;
-  alignas(16) float hi[C::RT], lo[C::RT], nl[C::RT];  // c of the row, its -lse log2(e)
+  ItemInfo<C::RR> info;
+  alignas(16) float hi[C::RR], lo[C::RR], nl[C::RR];  // c of the row, its -lse log2(e)
 };
 
 template <class C>
@@ -111,13 +111,13 @@ __device__ __forceinline__ void each_item(const AttendArgs& a, const WeightsShar
   }
 }
 
-// K columns of scores: their terms added, each 1/16 of the one before.
+// K columns of scores: their terms added, each 1/16 of the one before, RR columns on.
 template <class C, int K>
 __device__ __forceinline__ void score_part(uint32_t taddr, float (&x)[K]) {
   float t1[K], t2[K];
   tmem_ld_cols<K>(taddr, x);
-  tmem_ld_cols<K>(taddr + C::RT, t1);
-  if (C::T == 3) tmem_ld_cols<K>(taddr + 2 * C::RT, t2);
+  tmem_ld_cols<K>(taddr + C::RR, t1);
+  if (C::T == 3) tmem_ld_cols<K>(taddr + 2 * C::RR, t2);
   tmem_ld_wait();
 #pragma unroll
   for (int r = 0; r < K; r += 2) {
@@ -130,7 +130,7 @@ __device__ __forceinline__ void score_part(uint32_t taddr, float (&x)[K]) {
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1)
     kv4_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightsArgs w) {
-  constexpr int PAR = C::PAR, RT = C::RT, N = C::N, kStages = C::kStages, kGroups = C::kGroups;
+  constexpr int PAR = C::PAR, RT = C::RT, kStages = C::kStages, kGroups = C::kGroups;
   constexpr int kThreads = C::kThreads, kProducers = C::kProducers;
   constexpr int kTile = kKvTile * 128;  // bytes of a key tile
   extern __shared__ uint8_t raw[];
@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     each_item<C>(a, s, [&](int b, const Sequence& q, int h, int t0, int part) {
       for (int pass = 0; pass < passes; ++pass, ++pc) {
         const uint32_t buf = pc & 1;
+        // A tile may be the other warpgroup's in the next pass, which adds to what this
+        // one stored.
+        if (pass > 0) bar_sync(1, 256);
         wait_or_stop(&s.q_full[buf], (pc >> 1) & 1, &s.stop, a.status);
         const int groups = min(per_pass, n_groups - pass * kGroups);
         const int lo_pos = s.rows[buf][0].info.lo_pos;
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.k_empty[st]);
-          if (pass > 0) {  // what this thread left in the pass before
+          if (pass > 0) {  // what the pass before left
 #pragma unroll
             for (int i = 0; i < PAR; ++i)
               if (there[i]) old[i] = load_global(at + i);
@@ -266,7 +269,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
             for (int r0 = 0; r0 < RT; r0 += kPart) {
               float e[kPart];
-              score_part<C, kPart>(tm + place * kPlace + r0, e);
+              const int r1 = r0 % C::RR;
+              score_part<C, kPart>(tm + place * kPlace + r0 / C::RR * C::NQ + r1, e);
               if (r0 + kPart == RT) {
                 tc_fence_before_sync();
                 __syncwarp();
@@ -276,8 +280,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
               for (int r = 0; r < kPart; r += 2) {
                 const F2 y = f2(e[r], e[r + 1]) * f2(k, k);
-                const F2 x = fma2(y, f2(rows.hi[r0 + r], rows.hi[r0 + r + 1]),
-                                  fma2(y, f2(rows.lo[r0 + r], rows.lo[r0 + r + 1]), f2(rows.nl[r0 + r], rows.nl[r0 + r + 1])));
+                const F2 x = fma2(y, f2(rows.hi[r1 + r], rows.hi[r1 + r + 1]),
+                                  fma2(y, f2(rows.lo[r1 + r], rows.lo[r1 + r + 1]), f2(rows.nl[r1 + r], rows.nl[r1 + r + 1])));
                 f2_get(x, e[r], e[r + 1]);
                 e[r] = exp2_approx(e[r]);
                 e[r + 1] = exp2_approx(e[r + 1]);
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               if (masks) {
 #pragma unroll
                 for (int r = 0; r < kPart; ++r)
-                  if (pos + r0 / C::RR > rows.info.row_pos[r0 + r]) e[r] = 0.0f;
+                  if (pos + r0 / C::RR > rows.info.row_pos[r1 + r]) e[r] = 0.0f;
               }
               F2 sum = f2(e[0], e[1]);
 #pragma unroll
@@ -389,10 +393,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             tc_fence_after_sync();
             if (leader) {
               const uint64_t ka = smem_desc_rows<128>(ring_addr + st * kTile);
-              const uint64_t qa = smem_desc_rows<128>(q_addr + (buf * kGroups + gr) * C::kQBytes);
+              const uint64_t qa = smem_desc_rows<C::HD>(q_addr + (buf * kGroups + gr) * C::kQBytes);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_f8_ss(tm + place * kPlace, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, true), ks > 0);
+              for (int i = 0; i < 4; ++i) {
+                const int ks = i % (C::HD / 32), half = i / (C::HD / 32);
+                mma_f8_ss(tm + place * kPlace + half * C::NQ, ka + i * 2, qa + ks * 2, idesc_f8(C::NQ, false, true), ks > 0);
+              }
               mma_commit(&s.s_full[wg][place]);
               if (gr == groups - 1) mma_commit(&s.k_empty[st]);
             }
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (pc >= 2) wait_or_stop(&s.q_empty[buf], ((pc >> 1) & 1) ^ 1, &s.stop, a.status);
         const int groups = min(per_pass, n_groups - pass * kGroups);
         // A warp's rows are of one group, and loaded together.
-        constexpr int kRows = kGroups * RT / kQueryWarps, kWarps = RT / kRows;
+        constexpr int kRows = (kGroups * C::RR + kQueryWarps - 1) / kQueryWarps, kWarps = C::RR / kRows;
         const int gr = (warp - C::kFirstQuery) / kWarps, r0 = (warp - C::kFirstQuery) % kWarps * kRows, r = r0 + lane;
         if (gr < groups) {
           GroupRows<C>& rows = s.rows[buf][gr];
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           en.nq = min(en.j0 + a.qt, q.n_new) - en.j0;
           en.first_pos = q.first + en.j0;
           // (A lane's row as query_rows has it.)
-          const int row = r % C::RR, j = row / a.R;
+          const int row = r, j = row / a.R;
           const bool there = lane < kRows && row < a.qt * a.R && j < en.nq && en.first_pos + j >= 0;
           float lse = -INFINITY;
           if (there)
@@ -460,7 +466,7 @@ cudaError_t weights_form(const CUtensorMap& tk, const WeightsArgs& w, int grid, 
   using C = WeightsCfg<D, RT, T>;
   constexpr int smem = 1024 + C::kStages * kKvTile * 128 + 2 * C::kGroups * C::kQBytes + static_cast<int>(sizeof(WeightsShared<C>));
   static_assert(smem <= 227 * 1024, "shared memory");
-  static_assert(C::N <= kPlace, "tensor memory");
+  static_assert(C::NS <= kPlace, "tensor memory");
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = 1ull << device;
   if (!(ready.load(std::memory_order_acquire) & bit)) {

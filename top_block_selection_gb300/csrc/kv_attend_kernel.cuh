@@ -361,22 +361,28 @@ struct AttendCfg {
   static constexpr int kSlots = kKvMaxSlots * PAR;          // its blocks
   static constexpr int T = T_;                              // e4m3 terms of a value
   static constexpr int N = (T * RT + 15) / 16 * 16;         // columns: the terms of each row
-  // Warpgroups. (Beside the scales of its tokens, the 4-bit cache's form of 16
-  // columns in three terms has no room in shared memory for a third one's probabilities.)
-  static constexpr int W = RT >= 32 || (kFour && RT == 16 && T_ == 3) ? 2 : 3;
+  // Of scores: the terms of the queries, which have the scores of an operand row's
+  // two tokens one after the other (each half of the row a product of its own).
+  static constexpr int NQ = (T * RR + 15) / 16 * 16;
+  static constexpr int NS = PAR * NQ;
+  // Warpgroups. (Beside the scales of its tokens, the 4-bit cache's form of 16 rows of
+  // 128 dimensions in three terms has no room in shared memory for a third one's
+  // probabilities.)
+  static constexpr int W = RT >= 32 || (kFour && RR == 16 && T_ == 3) ? 2 : 3;
   static constexpr int kThreads = W * 128 + W * 32 + 32;    // they, a producer warp for each, the query warp
   static constexpr int kStageBytes = 2 * kKvTile * D;       // K then V
   // A stage serves one warpgroup only: a parity wait may not run two phases
   // ahead, and only a stage's own last user knows that its phase has passed.
   static constexpr int kStages = (RT >= 32 ? 4 : 6) * (128 / D);
   static_assert(kStages % W == 0, "a stage serves one warpgroup");
-  static constexpr int kQBytes = N * D;                     // one of two buffers
+  static constexpr int kQBytes = NQ * HD;                   // one of two buffers
   static constexpr int kPBytes = N * kKvTile;               // one of W
   static constexpr int kJoinRows = RT <= 8 ? RR : RR / 2;   // rows joined at a time, over the P buffers
   static constexpr int kJoinBytes = W * kJoinRows * D * 4;
   static constexpr int kPRegion = W * kPBytes > kJoinBytes ? W * kPBytes : kJoinBytes;
-  static constexpr int kTmemCols = 2 * N * W <= 128 ? 128 : (2 * N * W <= 256 ? 256 : 512);
-  static_assert(2 * N * W <= 512, "TMEM");
+  static constexpr int kColumns = (NS + N) * W;
+  static constexpr int kTmemCols = kColumns <= 128 ? 128 : (kColumns <= 256 ? 256 : 512);
+  static_assert(kColumns <= 512, "TMEM");
   // Tiles of a warpgroup after which it looks whether its references stand too
   // high for the tokens that come now.
   static constexpr int kRun = T == 3 ? 8 : 4;
@@ -412,7 +418,7 @@ struct ItemInfo {
 
 template <class C>
 struct AttendShared {
-  ItemInfo<C::RT> item[2];
+  ItemInfo<C::RR> item[2];
   StageMeta<C> meta[C::kStages];
   alignas(16) float red[C::W][C::RT][4];     // per-warp maxima, then sums
   alignas(16) float spread[C::W][4];         // per-warp: the largest value scale over its tokens' smallest (log2)
@@ -616,34 +622,30 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
 }
 
 // --------------------------------------------------------- the query's terms
-// Rows r0, r0 + step, ... (K of them, below RT) of the query tile `en` for KV
+// Rows r0, r0 + step, ... (K of them, below RR) of the query tile `en` for KV
 // head h, by one warp: all loaded, then each scaled by a power of two to the
 // range of e4m3 and split in terms. Rows that are not there are zero. `dst`
 // holds rows of D bytes, term after term.
 template <class C, int K>
-__device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>& info, uint8_t* dst, const Entry& en,
+__device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RR>& info, uint8_t* dst, const Entry& en,
                                            int h, int r0, int step) {
-  constexpr int kPer = C::D / 32;  // elements of a lane
+  constexpr int kPer = C::HD / 32;  // elements of a lane
   const int lane = threadIdx.x % 32, rows = a.qt * a.R;
   uint32_t u[K][kPer / 2];
   int row_pos[K];
   int64_t row_at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    // Of two tokens in an operand row, column r + RR has the row's elements for
-    // the second, and zeros for the first.
-    const int half = C::PAR == 2 && r0 + k * step >= C::RR ? 1 : 0;
-    const int r = r0 + k * step - half * C::RR, j = a.qt > 1 ? r / a.R : 0, head = h * a.R + (r - j * a.R);
+    const int r = r0 + k * step, j = a.qt > 1 ? r / a.R : 0, head = h * a.R + (r - j * a.R);
     const bool there = r < rows && j < en.nq && en.first_pos + j >= 0;
     row_pos[k] = r >= rows ? kKvNoToken : (there ? en.first_pos + j : -1);
     row_at[k] = r < rows && en.j0 + j < a.n ? (static_cast<int64_t>(en.b) * a.n + en.j0 + j) * a.Hq + head : -1;
-    const int element = lane * kPer - half * C::HD;
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) u[k][e] = 0;
-    if (there && (C::PAR == 1 || (element >= 0 && element < C::HD))) {
+    if (there) {
       const uint16_t* const src = static_cast<const uint16_t*>(a.q.data) + en.b * a.q.sb +
                                   static_cast<int64_t>(en.j0 + j) * a.q.sn + static_cast<int64_t>(head) * a.q.sh +
-                                  element;
+                                  lane * kPer;
       if (kPer == 4) {
         const uint2 v = load_global(reinterpret_cast<const uint2*>(src));
         u[k][0] = v.x;
@@ -656,7 +658,7 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int r = r0 + k * step;
-    if (r >= C::RT) break;
+    if (r >= C::RR) break;
     float x[kPer], m = 0.0f;
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) {
@@ -687,7 +689,7 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
         x[2 * e] = 16.0f * (x[2 * e] - back.x);  // at most half a step of the code: no more than 16
         x[2 * e + 1] = 16.0f * (x[2 * e + 1] - back.y);
       }
-      uint8_t* const to = dst + swizzled<C::D>((term * C::RT + r) * C::D + lane * kPer);
+      uint8_t* const to = dst + swizzled<C::HD>((term * C::RR + r) * C::HD + lane * kPer);
       if (kPer == 4) *reinterpret_cast<uint32_t*>(to) = code[0] | (code[kPer / 2 - 1] << 16);
       else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
     }
@@ -703,7 +705,7 @@ __device__ __forceinline__ void query_rows(const AttendArgs& a, ItemInfo<C::RT>&
 // this CTA begins an item that others end (one thread). `at`: the place of the
 // item's first tile among all tiles.
 template <class C>
-__device__ __forceinline__ void describe_item(const AttendArgs& a, ItemInfo<C::RT>& info, const Entry& en, const Walk& w,
+__device__ __forceinline__ void describe_item(const AttendArgs& a, ItemInfo<C::RR>& info, const Entry& en, const Walk& w,
                                               int part, int64_t at, int64_t total, int grid) {
   info.tiles = part;
   info.lo_pos = en.last_pos < 0 ? -1 : max(en.first_pos, 0);
@@ -735,7 +737,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     if (it >= 2) ok = wait_or_stop(&s.q_empty[buf], ((it >> 1) & 1) ^ 1, &s.stop, a.status);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (!ok) break;
-    ItemInfo<C::RT>& info = s.item[buf];
+    ItemInfo<C::RR>& info = s.item[buf];
     if (w.left <= 0) {
       if (lane == 0) {
         info.tiles = 0;
@@ -750,7 +752,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
     if (it > 0) {
 #pragma unroll 1
-      for (int r = 0; r < C::RT; r += 4) query_rows<C, 4>(a, info, q_smem + buf * C::kQBytes, en, w.h, r, 1);
+      for (int r = 0; r < C::RR; r += 4) query_rows<C, 4>(a, info, q_smem + buf * C::kQBytes, en, w.h, r, 1);
       if (lane == 0) describe_item<C>(a, info, en, w, part, at, total, grid);
       fence_proxy_async_smem();
       __syncwarp();
@@ -793,18 +795,21 @@ static __device__ __noinline__ void poison_all(int32_t* poison, int pos) {
   for (int d = 0; d < 128; ++d) atomicMin(&poison[d], pos);
 }
 
-// The columns of RT rows at `taddr`, their T terms added, each 1/16 of the one
-// before it (of three terms of a probability, the second 1/8), a few rows at a
-// time (the terms of all would not fit in registers beside the softmax state).
+// The RT columns of a term at `taddr`, the T terms added, each 1/16 of the one
+// before it (of three terms of a probability, the second 1/8), a few at a time (the
+// terms of all would not fit in registers beside the softmax state). Scores of an
+// operand row's second token stand NQ columns behind the first one's.
 template <class C, bool kProbs>
 __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[C::RT]) {
-  constexpr int kPart = C::RT <= 8 ? C::RT : C::RT / 2;
+  constexpr bool kPairs = !kProbs && C::PAR == 2;
+  constexpr int kPart = kPairs ? C::RR : C::RT <= 8 ? C::RT : C::RT / 2, kTerm = kPairs ? C::RR : C::RT;
 #pragma unroll
   for (int r0 = 0; r0 < C::RT; r0 += kPart) {
+    const uint32_t at = taddr + (kPairs ? r0 / C::RR * C::NQ : r0);
     float t0[kPart], t1[kPart], t2[kPart];
-    tmem_ld_cols<kPart>(taddr + r0, t0);
-    tmem_ld_cols<kPart>(taddr + C::RT + r0, t1);
-    if (C::T == 3) tmem_ld_cols<kPart>(taddr + 2 * C::RT + r0, t2);
+    tmem_ld_cols<kPart>(at, t0);
+    tmem_ld_cols<kPart>(at + kTerm, t1);
+    if (C::T == 3) tmem_ld_cols<kPart>(at + 2 * kTerm, t2);
     tmem_ld_wait();
 #pragma unroll
     for (int r = 0; r < kPart; r += 2) {
@@ -853,10 +858,13 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   auto issue_scores = [&](uint32_t st, int buf) {
     tc_fence_after_sync();
     const uint64_t ka = smem_desc_rows<D>(ring_addr + st * C::kStageBytes);
-    const uint64_t qa = smem_desc_rows<D>(q_addr + buf * C::kQBytes);
+    const uint64_t qa = smem_desc_rows<C::HD>(q_addr + buf * C::kQBytes);
     if (leader) {
 #pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(tm_s, ka + ks * 2, qa + ks * 2, idesc_f8(N, false, C::kFour), ks > 0);
+      for (int i = 0; i < D / 32; ++i) {
+        const int ks = i % (C::HD / 32), half = i / (C::HD / 32);
+        mma_f8_ss(tm_s + half * C::NQ, ka + i * 2, qa + ks * 2, idesc_f8(C::NQ, false, C::kFour), ks > 0);
+      }
       mma_commit(&s.s_bar[wg]);
     }
     __syncwarp();
@@ -870,14 +878,14 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
   const int64_t total = s.share.total;
   const int grid = s.share.grid;
   if (s.share.hi <= s.share.lo) return;
-  tm_s = uniform(s.tmem) + wg * 2 * N;
-  tm_o = tm_s + N;
+  tm_s = uniform(s.tmem) + wg * (C::NS + N);
+  tm_o = tm_s + C::NS;
   {
     const Walk walk = s.share.start.walk;
     const Entry en = s.share.start.entry;
     const int64_t at0 = s.share.lo - walk.t;
-    if (wg * 4 + warp < RT)
-      query_rows<C, (RT + W * 4 - 1) / (W * 4)>(a, s.item[0], q_smem, en, walk.h, wg * 4 + warp, W * 4);
+    if (wg * 4 + warp < C::RR)
+      query_rows<C, (C::RR + W * 4 - 1) / (W * 4)>(a, s.item[0], q_smem, en, walk.h, wg * 4 + warp, W * 4);
     if (threadIdx.x == W * 128 - 1)
       describe_item<C>(a, s.item[0], en, walk,
                        static_cast<int>(min(static_cast<int64_t>(en.tiles - walk.t), walk.left)), at0, total, grid);
@@ -889,7 +897,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
     if (it > 0 && !wait_or_stop(&s.q_full[buf], ((it - 1) >> 1) & 1, &s.stop, a.status)) bad = true;
     if (threadIdx.x < 128) s.poison[threadIdx.x] = kKvNoToken;
     if (bar_any(8, kAll, bad)) break;
-    const ItemInfo<RT>& info = s.item[buf];
+    const ItemInfo<C::RR>& info = s.item[buf];
     const int tiles = uniform(info.tiles);
     if (tiles == 0) break;
     const int lo_pos = info.lo_pos, hi_pos = info.hi_pos;
@@ -969,14 +977,14 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
           const float km = k_mul[r / C::RR];
-          const F2 f = f2(info.row_mul[r], info.row_mul[r + 1]) * f2(km, km);
+          const F2 f = f2(info.row_mul[r % C::RR], info.row_mul[r % C::RR + 1]) * f2(km, km);
           const F2 base = relative ? f2(-m[r], -m[r + 1]) : f2(0.0f, 0.0f);
           f2_get(fma2(f2(e[r], e[r + 1]), f, base), e[r], e[r + 1]);
         }
         if (masks) {
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            if (pos + r / C::RR > info.row_pos[r]) e[r] = kNegInf;
+            if (pos + r / C::RR > info.row_pos[r % C::RR]) e[r] = kNegInf;
         }
       };
       scores(true);
@@ -998,7 +1006,7 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
         // codes being below 2^17.7, of a 4-bit code 2^11.4: they have no steps below 1 then.)
         scores(false);
         const float vnow = fmaxf(vref, meta.vmax);
-        const float mul = warp_max(lane < RT ? fabsf(info.row_mul[lane]) : 0.0f);
+        const float mul = warp_max(lane < C::RR ? fabsf(info.row_mul[lane]) : 0.0f);
         float lv[C::PAR], far = 0.0f, top = kNegInf;
 #pragma unroll
         for (int i2 = 0; i2 < C::PAR; ++i2) {
