@@ -90,8 +90,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_append_kernel(const 
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-  // A pass of slots that hold only older tokens matters to the block key alone.
-  for (int slot = (want_kb ? 0 : n_old / kTokens * kTokens) + tok; slot - tok < held; slot += kTokens) {
+  auto add = [&](uint32_t c0, uint32_t c1, float s) {
+    float x[8], y[8];
+    e2m1x8_to_float(c0, x);
+    e2m1x8_to_float(c1, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      acc[e] = fmaf(x[e], s, acc[e]);
+      acc[8 + e] = fmaf(y[e], s, acc[8 + e]);
+    }
+  };
+  uint8_t* codes = nullptr;
+  uint16_t* scales = nullptr;
+  auto found = [&]() {
+    const bool there = page >= 0 && page < a.c.n_pages;
+    if (!there && threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
+    codes = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + static_cast<int64_t>(h) * a.c.block * (D / 2);
+    scales = (is_v ? a.c.v_scale4 : a.c.k_scale4) + (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block;
+    return there;
+  };
+  // The older tokens, for the block key: the loads of four go out together.
+  if (want_kb && n_old > 0) {
+    if (!found()) return;
+#pragma unroll 1
+    for (int s0 = tok; s0 < n_old; s0 += 4 * kTokens) {
+      uint32_t c0[4], c1[4];
+      float s[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int slot = min(s0 + t * kTokens, n_old - 1);
+        c0[t] = load_global(reinterpret_cast<const uint32_t*>(codes + slot * (D / 2) + l.off0 / 2));
+        c1[t] = load_global(reinterpret_cast<const uint32_t*>(codes + slot * (D / 2) + l.off1 / 2));
+        s[t] = load_scale(scales + slot);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (s0 + t * kTokens < n_old) add(c0[t], c1[t], s[t]);
+    }
+  }
+  for (int slot = n_old / kTokens * kTokens + tok; slot - tok < held; slot += kTokens) {
     const bool fresh = slot >= n_old && slot < held;
     uint4 raw0, raw1;
     if (fresh) {
@@ -100,21 +137,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_append_kernel(const 
       raw1 = load8(src.data, row + l.off1);
     }
     // The page is waited for only now, with the new tokens on their way.
-    if (page < 0 || page >= a.c.n_pages) {
-      if (threadIdx.x == 0) atomicOr(a.status, kErrCacheIndex);
-      return;
-    }
-    uint8_t* const codes =
-        (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + (static_cast<int64_t>(h) * a.c.block + slot) * (D / 2);
-    uint16_t* const scale =
-        (is_v ? a.c.v_scale4 : a.c.k_scale4) + (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block + slot;
+    if (!codes && !found()) return;
     uint32_t c0 = 0, c1 = 0, top = 0;
     float s = 0.0f, x[8], y[8];
-    if (slot < n_old && want_kb) {
-      c0 = load_global(reinterpret_cast<const uint32_t*>(codes + l.off0 / 2));
-      c1 = load_global(reinterpret_cast<const uint32_t*>(codes + l.off1 / 2));
-      s = load_scale(scale);
-    }
     if (fresh) {
       unpack8<BF16>(raw0, x);
       unpack8<BF16>(raw1, y);
@@ -138,18 +163,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_append_kernel(const 
       const float inv = __frcp_rn(s);
       c0 = isnan(s) ? 0u : encode8(x, s, inv);
       c1 = isnan(s) ? 0u : encode8(y, s, inv);
-      *reinterpret_cast<uint32_t*>(codes + l.off0 / 2) = c0;
-      *reinterpret_cast<uint32_t*>(codes + l.off1 / 2) = c1;
-      if (sub == 0) *scale = static_cast<uint16_t>(__float_as_uint(s) >> 16);
-    }
-    if (want_kb && slot < held) {
-      e2m1x8_to_float(c0, x);
-      e2m1x8_to_float(c1, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc[e] = fmaf(x[e], s, acc[e]);
-        acc[8 + e] = fmaf(y[e], s, acc[8 + e]);
-      }
+      *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + l.off0 / 2) = c0;
+      *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + l.off1 / 2) = c1;
+      if (sub == 0) scales[slot] = static_cast<uint16_t>(__float_as_uint(s) >> 16);
+      if (want_kb) add(c0, c1, s);
     }
   }
   // An attention next on the stream may start early and reads codes by bulk
