@@ -311,17 +311,14 @@ PyObject* read4(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const int bf16 = PyObject_IsTrue(a[7]);
     if (bf16 < 0) return nullptr;
     const ScalarType type = bf16 ? ScalarType::BFloat16 : ScalarType::Half;
-    const int64_t shape[5] = {2, c.B, n, c.Hkv, c.D};
-    Tensor rows[2], made;
+    const int64_t shape[4] = {c.B, n, c.Hkv, c.D};
+    Tensor rows[2];
     for (int i = 0; i < 2; ++i) {
       if (a[9 + i] != Py_None) {
         rows[i] = tensor(a[9 + i], i ? "v_out" : "k_out");
-        plain(rows[i], type, IntArrayRef(shape + 1, 4), dev, i ? "v_out" : "k_out");
+        plain(rows[i], type, IntArrayRef(shape, 4), dev, i ? "v_out" : "k_out");
       } else {
-        // Keys and values in one allocation: a second one takes 1.5 us.
-        at::AutoDispatchBelowADInplaceOrView plain_views;
-        if (!made.defined()) made = at::empty(IntArrayRef(shape, 5), tensor(a[0], "k_cache").options().dtype(type));
-        rows[i] = made.select(0, i);
+        rows[i] = at::empty(IntArrayRef(shape, 4), tensor(a[0], "k_cache").options().dtype(type));
       }
     }
     c10::cuda::OptionalCUDAGuard guard;
