@@ -580,7 +580,7 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
  * the lowest slot first; NaN counts as the largest), moved together in their
  * order: codes, scales and weights.
  *
- *   weights  f32 [n_pages, Hkv, block], 4-byte aligned.
+ *   weights  f32 [n_pages, Hkv, block], 16-byte aligned.
  *   budget   >= 1; sink, recent >= 0, sink + recent <= budget.
  *   lens_out int32 [B]: min(lens, budget). May not be lens itself.
  *   offset   optional int32 [B]: grows by the number of tokens that went, as

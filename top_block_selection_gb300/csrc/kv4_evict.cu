@@ -11,7 +11,7 @@
 // memory, so that the weights are read once; histograms are added over
 // distributed shared memory. The move is in place: a token never moves up, so a
 // chunk's stores touch no later chunk's sources; within a chunk all CTAs load
-// before any stores. What bounds it: bytes for many items; for few, the chain of
+// before any stores, until the chunks come from beyond the budget altogether. What bounds it: bytes for many items; for few, the chain of
 // a chunk's dependent loads (list, page, codes) and its cluster barrier.
 #include <algorithm>
 #include <atomic>
@@ -27,7 +27,8 @@ constexpr int kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
 // heads of 131,072 tokens 84 us instead of 71.)
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 40960;  // of a CTA's part, in shared memory; those past it are read again in each pass
-constexpr int kBatch = 8;        // keys of a thread whose loads are in flight together
+constexpr int kBatch = 8;        // keys of a thread side by side
+constexpr int kQuads = 4;        // loads of four weights of a thread in flight together
 
 struct EvictArgs {
   KvCacheArgs c;
@@ -247,20 +248,34 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kv4_evict_kernel(const _
   int32_t* const list = a.list + static_cast<int64_t>(item) * a.budget;
   if (keep > 0) {
     __syncthreads();  // the histograms are clear
-    for (int i0 = tid; i0 < count; i0 += kBatch * THREADS) {
-      int64_t row[kBatch];
-      float w[kBatch];
+    // Four slots a load, the first aligned; four such loads of a thread together.
+    const int lead = first & 3;
+    for (int j0 = tid; 4 * j0 < count + lead; j0 += kQuads * THREADS) {
+      int page[kQuads];
+      float4 w[kQuads];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) row[x] = i0 + x * THREADS < count ? row_of(first + i0 + x * THREADS) : -1;
+      for (int x = 0; x < kQuads; ++x) {
+        const int i = 4 * (j0 + x * THREADS) - lead;
+        page[x] = i < count ? page_of(first + i) : -1;
+      }
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) w[x] = row[x] >= 0 ? load_global(a.weights + row[x]) : 0.0f;
+      for (int x = 0; x < kQuads; ++x) {
+        w[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (page[x] >= 0)
+          w[x] = load_global(reinterpret_cast<const float4*>(
+              a.weights + row_in(page[x], first + 4 * (j0 + x * THREADS) - lead)));
+      }
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const int i = i0 + x * THREADS;
-        if (i >= count) break;
-        const uint32_t k = key_of(w[x]);
-        if (i < a.cap) keys[i] = k;
-        atomicAdd(&s.hist[0][k >> 21], 1u);
+      for (int x = 0; x < kQuads; ++x) {
+        const float each[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * (j0 + x * THREADS) - lead + e;
+          if (i < 0 || i >= count) continue;
+          const uint32_t k = key_of(each[e]);
+          if (i < a.cap) keys[i] = k;
+          atomicAdd(&s.hist[0][k >> 21], 1u);
+        }
       }
     }
     uint32_t need = keep, prefix, bin, above;
@@ -368,8 +383,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kv4_evict_kernel(const _
     }
     const int now = mine;
     mine += a.ctas * tokens;
+    // Tokens from beyond the budget lie where nothing is stored. Once a chunk begins
+    // with one (all later ones come from further up), what it overwrites has been
+    // loaded: the chunks before it waited for that.
+    const int begins_at = base >= newest ? base + shift : __ldcg(list + base);
     if (base + a.ctas * tokens < a.budget) look_up(mine);
-    cluster_sync<CLUSTER>();
+    if (begins_at < a.budget) cluster_sync<CLUSTER>();
 #pragma unroll
     for (int r = 0; r < PIECES; ++r) {
       if (!(moves >> r & 1)) continue;

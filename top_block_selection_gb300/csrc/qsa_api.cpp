@@ -735,7 +735,7 @@ qsa_status qsa_kv4_evict(const qsa_kv4_cache* cache, float* weights, int32_t bud
   if (!weights || !lens_out || lens_out == cache->lens || lens_out == offset || !workspace ||
       workspace_bytes < qsa::kv4_evict_workspace_bytes(cache->B, cache->Hkv, budget))
     return QSA_ERR_INVALID_ARG;
-  if (!aligned(weights, 4) || !aligned(lens_out, 4) || !aligned(offset, 4) || !aligned(workspace, 16))
+  if (!aligned(weights, 16) || !aligned(lens_out, 4) || !aligned(offset, 4) || !aligned(workspace, 16))
     return QSA_ERR_MISALIGNED;
   const qsa::Kv4EvictProblem p{cache_args(cache), weights,  budget, sink,
                                recent,            lens_out, offset, static_cast<int32_t*>(workspace)};
