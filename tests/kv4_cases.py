@@ -3,7 +3,7 @@ that hold no token have codes of every kind and NaN scales and weights, so that
 a stray read shows."""
 import numpy as np
 
-from kv_cases import angles, as_bf16, blocks_of, ROUND  # noqa: F401
+from kv_cases import angles, as_bf16, as_f16, blocks_of, ROUND  # noqa: F401
 from oracle import kv4_oracle as ko
 
 

@@ -64,7 +64,8 @@ __host__ __device__ constexpr int many_buffers(int D) { return (512 - 2 * D) / 1
 // Of the 4-bit cache the scales of 16 tokens are a power of two common to them
 // (ks, vs; their largest scale is 2^12 to 2^13 of it) times one for each token in
 // fp16 (kt, vt), with which the converted codes are multiplied: exact, as a scale
-// has 8 bits and a code 2, but for scales below 2^-20 of the largest of the 16.
+// has 8 bits and a code 2, but for scales below 2^-25 of the largest of the 16, whose
+// products fall below fp16's normal numbers.
 template <bool FOUR>
 struct TokenScales {};
 template <>
