@@ -108,15 +108,14 @@ def test_one_token_above_very_many(tbs, dtype, bits, D, n, R):  # noqa: F811
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("D,n,R,kernel", FORMS)
 def test_large_value_scale_without_weight(tbs, D, dtype, n, R, kernel, at):  # noqa: F811
-    """A token whose values are 2^14 (of many rows 2^24) times the others' and whose
-    score lies 60 (in log2) below them changes nothing, whether a row sees it or not.
-    (Of many rows the contract has scales exact down to 2^-25 of the largest of 16.)"""
+    """A token whose values are 2^14 (of many rows 2^26) times the others' and whose
+    score lies 60 (in log2) below them changes nothing, whether a row sees it or not."""
     rng = np.random.default_rng(D + n)
     k, v = rng.standard_normal((2000, D)), rng.standard_normal((2000, D)) * 2
     k[:, 0] = 0.0
     k[at, 0] = -6.0
     vs = 2.0 ** rng.uniform(-8, -7, 2000)
-    vs[at] = 2.0 ** ((14 if n == 1 else 24) - 8)
+    vs[at] = 2.0 ** ((14 if n == 1 else 26) - 8)
     c = one_head(1, k, v, np.ones(2000), vs, 64)
     q = rng.standard_normal((1, n, R, D)) * D ** -0.5
     q[..., 0] = 60 * np.log(2.0) / 6

@@ -61,16 +61,20 @@ constexpr float kManyScale = 64.0f;  // of a probability 1 at the largest value 
 // its warpgroup has done with the last one's.
 __host__ __device__ constexpr int many_buffers(int D) { return (512 - 2 * D) / 128; }
 
-// Of the 4-bit cache the scales of 16 tokens are a power of two common to them
-// (ks, vs; their largest scale is 2^12 to 2^13 of it) times one for each token in
-// fp16 (kt, vt), with which the converted codes are multiplied: exact, as a scale
-// has 8 bits and a code 2, but for scales below 2^-25 of the largest of the 16, whose
-// products fall below fp16's normal numbers.
+// Of the 4-bit cache. The key scales of 16 tokens are a power of two common to
+// them (ks; their largest scale is 2^12 to 2^13 of it) times one for each token in
+// fp16 (kt), with which the converted codes are multiplied: exact, as a scale has 8
+// bits and a code 2, but for scales below 2^-25 of the largest of the 16, whose
+// products fall below fp16's normal numbers. The value scales ride on the
+// probabilities, token by token (on the values, as the keys', one token of large
+// values without weight would push the probabilities of all others out of fp16).
 template <bool FOUR>
 struct TokenScales {};
 template <>
 struct TokenScales<true> {
-  alignas(16) uint16_t kt[kKvTile], vt[kKvTile];
+  alignas(16) uint16_t kt[kKvTile];
+  alignas(16) float vt[kKvTile];  // times kManyScale over vmax; 0 where there is none, or NaN
+  uint16_t nan[8];                // bit i: value scale i of 16 is NaN
 };
 
 template <bool FOUR>
@@ -238,7 +242,7 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D, FOUR>& s, const S
               drop_last(vt[x], over - (8 - 8 * x));
             }
           ks = share_scale(kt);
-          vs = share_scale(vt);
+          vs = fmaxf(largest_scale(vt[0]), largest_scale(vt[1]));
         }
       } else {
         if (page >= 0) {
@@ -251,7 +255,21 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D, FOUR>& s, const S
       const float shift = vmax > 0.0f ? fminf(lnow - log2_approx(vmax), room) : 0.0f;
       room -= shift;
       vmax = vnow;
-      const bool far = __any_sync(0xFFFFFFFFu, page >= 0 && lv < -kManyNear);
+      bool apart = page >= 0 && lv < -kManyNear;
+      float each[FOUR ? 16 : 1];
+      uint32_t nan = 0;
+      if constexpr (FOUR) {
+        const uint32_t* const bits = reinterpret_cast<const uint32_t*>(vt);
+        const float unit = vnow > 0.0f ? __fdividef(kManyScale, vnow) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float v = __uint_as_float(e % 2 ? bits[e / 2] & 0xFFFF0000u : bits[e / 2] << 16);
+          apart = apart || (v > 0.0f && v * unit < kManyScale / 64.0f);  // 2^-kManyNear
+          if (isnan(v)) nan |= 1u << e;
+          each[e] = isnan(v) ? 0.0f : v * unit;
+        }
+      }
+      const bool far = __any_sync(0xFFFFFFFFu, apart);
       const uint32_t holes = __ballot_sync(0xFFFFFFFFu, page < 0) & 0xFFu;
       const uint32_t at = g % kManyRing;
       if (g >= kManyRing) wait_or_stop(&s.meta_empty[at], (g / kManyRing + 1) & 1, &s.stop, a.status);
@@ -260,10 +278,12 @@ __device__ void many_lookup(const AttendArgs& a, ManyShared<D, FOUR>& s, const S
       if (lane < 8) {
         if constexpr (FOUR) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            reinterpret_cast<uint4*>(m.kt)[2 * i + x] = kt[x];
-            reinterpret_cast<uint4*>(m.vt)[2 * i + x] = vt[x];
-          }
+          for (int x = 0; x < 2; ++x) reinterpret_cast<uint4*>(m.kt)[2 * i + x] = kt[x];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<float4*>(m.vt)[4 * i + x] =
+                make_float4(each[4 * x], each[4 * x + 1], each[4 * x + 2], each[4 * x + 3]);
+          m.nan[i] = static_cast<uint16_t>(nan);
         }
         m.ks[i] = ks;
         m.vs[i] = vs;
@@ -309,7 +329,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// 16 4-bit codes times their token's scale (two halves of it) to 16 halves.
+// 16 4-bit codes, times their token's scale (two halves of it) or not, to 16 halves.
+template <bool SCALED>
 __device__ __forceinline__ void convert16(uint8_t* tile, uint32_t off, const uint2& codes, uint32_t scale) {
   const __half2 s = *reinterpret_cast<const __half2*>(&scale);
 #pragma unroll
@@ -319,7 +340,7 @@ __device__ __forceinline__ void convert16(uint8_t* tile, uint32_t off, const uin
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), s);
-      h[e] = *reinterpret_cast<const uint32_t*>(&x);
+      if (SCALED) h[e] = *reinterpret_cast<const uint32_t*>(&x);
     }
     *reinterpret_cast<uint4*>(tile + swizzled<128>(off + 16 * i)) = make_uint4(h[0], h[1], h[2], h[3]);
   }
@@ -379,7 +400,7 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_
         const uint32_t off = off0 + p * (kKvTile / kPasses) * 128;
         if constexpr (FOUR) {
           const uint32_t scale = m.kt[row0 + p * (kKvTile / kPasses)];
-          convert16(k16 + buf * kBytes, off, key[p], scale | scale << 16);
+          convert16<true>(k16 + buf * kBytes, off, key[p], scale | scale << 16);
         } else {
           convert16<BF16>(k16 + buf * kBytes, off, key[p]);
         }
@@ -393,16 +414,13 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_
       // Values that no row sees are zeros, so that 0 times them is 0; NaN codes
       // that some rows see are zeros too, and noted for the rows that do.
       const int pos0 = (w.t + i) * kKvTile;
-      uint32_t scale[FOUR ? kPasses : 1] = {};
       if constexpr (FOUR) {
-        // A NaN scale that some rows do not see is made 0, and noted for those
-        // that do. (Where no row sees a token its scale is 0 already.)
+        // A token whose value scale is NaN counts as 0 here, and is noted for the rows
+        // that see it. (Codes are finite, whatever stands where no row sees a token.)
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
           const int row = row0 + p * (kKvTile / kPasses);
-          scale[p] = m.vt[row];
-          if ((scale[p] & 0x7FFFu) > 0x7C00u && pos0 + row > lo_pos) {
-            scale[p] = 0;
+          if (m.nan[row / 16] >> (row % 16) & 1) {
             s.poisoned[it % kManyRing] = 1;
             for (int e = 0; e < 16; ++e) atomicMin(&poison[c * 16 + e], pos0 + row);
           }
@@ -439,7 +457,7 @@ __device__ void many_convert(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const uint32_t off = off0 + p * (kKvTile / kPasses) * 128;
-        if constexpr (FOUR) convert16(v16 + buf * kBytes, off, val[p], scale[p] | scale[p] << 16);
+        if constexpr (FOUR) convert16<false>(v16 + buf * kBytes, off, val[p], 0);
         else convert16<false>(v16 + buf * kBytes, off, val[p]);
       }
       published(&s.v_full[buf]);
@@ -609,9 +627,10 @@ __device__ __forceinline__ float max3(float x, float y, float z) {  // NaN count
 // scores are rounded before the reference is taken off, as they were for the
 // reference: where they are so large that this matters, a row's largest is 1.
 // (zero is 0, unknown to the compiler, which would join product and difference.)
-template <bool BF16, bool MASK>
-__device__ __forceinline__ void many_probabilities(uint32_t taddr, float f0, float f1, float v0, float v1, float m,
-                                                   int limit0, int limit1, float zero, F2& l) {
+// vt: the tokens' value scales, in place of v0 and v1 (4-bit cache).
+template <bool BF16, bool MASK, bool FOUR>
+__device__ __forceinline__ void many_probabilities(uint32_t taddr, float f0, float f1, float v0, float v1,
+                                                   const float* vt, float m, int limit0, int limit1, float zero, F2& l) {
   float x[32];
   tmem_ld_cols<32>(taddr, x);
   tmem_ld_wait();
@@ -632,7 +651,12 @@ __device__ __forceinline__ void many_probabilities(uint32_t taddr, float f0, flo
     }
     F2 p = f2(p0, p1);
     l = l + p;
-    p = p * f2(v, v);
+    if (FOUR) {
+      const float2 each = *reinterpret_cast<const float2*>(vt + e);
+      p = p * f2(each.x, each.y);
+    } else {
+      p = p * f2(v, v);
+    }
     f2_get(p, p0, p1);
     if (BF16) {
       first[e / 2] = half2_of(p0, p1);
@@ -747,8 +771,14 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* 
             float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (e <= limit) mx = fmaxf(mx, x[e]);
-            weight = fmaxf(weight, fmaf(mx, mul * meta.ks[c], meta.lv[c]));
+              if (e <= limit) {
+                if constexpr (FOUR)
+                  mx = fmaxf(mx, fmaf(x[e], mul * meta.ks[c],
+                                      fmaxf(log2_approx(meta.vt[c * 16 + e] * (1.0f / kManyScale)), -kRange)));
+                else
+                  mx = fmaxf(mx, x[e]);
+              }
+            weight = fmaxf(weight, FOUR ? mx : fmaf(mx, mul * meta.ks[c], meta.lv[c]));
           }
           if (fabsf(top) < kFine) top = weight;
         }
@@ -783,6 +813,8 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* 
         const bool huge = __any_sync(0xFFFFFFFFu, m > 1048576.0f || (m < -1048576.0f && m != kUnset));
         const float inv = vref > 0.0f ? __fdividef(kManyScale, vref) : 0.0f;
         float2 vs = *reinterpret_cast<const float2*>(&meta.vs[0]);
+        const float* vt = nullptr;
+        if constexpr (FOUR) vt = meta.vt;
         // A tile's sum apart: added one by one to a sum that one token above all
         // others made large, the small ones would lose bits each.
         F2 lt = f2(0.0f, 0.0f);
@@ -793,10 +825,11 @@ __device__ void many_rows(const AttendArgs& a, ManyShared<D, FOUR>& s, uint8_t* 
           vs = *reinterpret_cast<const float2*>(&meta.vs[(2 * c + 2) & 7]);
           if (masked || huge) {
             const int limit = row_pos - pos0 - c * 32;
-            many_probabilities<BF16, true>(tm_s + c * 32, f0, f1, v0, v1, m, (holes >> (2 * c)) & 1 ? -1 : limit,
-                                           (holes >> (2 * c + 1)) & 1 ? -1 : limit, zero, lt);
+            many_probabilities<BF16, true, FOUR>(tm_s + c * 32, f0, f1, v0, v1, vt + c * 32, m,
+                                                 (holes >> (2 * c)) & 1 ? -1 : limit,
+                                                 (holes >> (2 * c + 1)) & 1 ? -1 : limit, zero, lt);
           } else {
-            many_probabilities<BF16, false>(tm_s + c * 32, f0, f1, v0, v1, m, 0, 0, zero, lt);
+            many_probabilities<BF16, false, FOUR>(tm_s + c * 32, f0, f1, v0, v1, vt + c * 32, m, 0, 0, zero, lt);
           }
         }
         l = l + lt;
