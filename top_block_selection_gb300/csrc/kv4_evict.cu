@@ -465,9 +465,14 @@ cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cu
   a.cap = static_cast<int32_t>(std::min<int64_t>((longest + a.ctas - 1) / a.ctas, kMaxKeys));
   // Many items: small CTAs, two an SM, whose phases overlap (64 x 8 items of 4,160
   // tokens 120 us; four an SM with half the pieces 159, one of 512 threads 138). Few:
-  // larger ones (8 items of 131,072 tokens 56 us, with 256 threads 80).
+  // clusters, of large CTAs where half of the SMs stay idle all the same (8 items of
+  // 131,072 tokens 54 us, 72 with small ones; 16 items 107 and 97, 64 of 32,768 103
+  // and 87). (A second kernel on all SMs for the tokens from beyond the budget, about
+  // 5 us of work there, cost more than it saved: 46 us instead of 42 for 8 items in a
+  // stream of calls, 69 instead of 61 for 64.)
   if (a.ctas == 1) return evict_form<256, 8, 2, 1>(a, items, dev.id, stream);
-  return evict_form<512, 8, 1, kMaxCluster>(a, items, dev.id, stream);
+  if (items * a.ctas <= dev.sm_count / 2) return evict_form<512, 8, 1, kMaxCluster>(a, items, dev.id, stream);
+  return evict_form<256, 8, 2, kMaxCluster>(a, items, dev.id, stream);
 }
 
 }  // namespace qsa
