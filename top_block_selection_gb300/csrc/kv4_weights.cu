@@ -6,9 +6,10 @@
 // The tokens are the M = 128 operand of the score product, as in
 // kv_attend_kernel.cuh, so that a thread owns a token (of 64 dimensions, two) and
 // adds its weights up alone: no exchange, no atomics, and results that do not
-// depend on timing. The exponent is y (c + c') - lse log2(e), with y the scaled
-// product and c + c' = scale log2(e) in two floats: a weight's relative error is
-// the exponent's absolute one, and one float of c would be the largest part of it.
+// depend on timing. The exponent is y c - lse log2(e), with y the scaled product
+// and c = scale log2(e): a weight's relative error is the exponent's absolute one,
+// 2^-24 of its parts each (2.1e-7 and 3.2e-7 for the measured cases; c in two floats,
+// a tenth more time, made no difference that shows beside the others).
 //
 // One CTA an SM. The tiles of all (sequence, KV head) items are dealt to the
 // CTAs in equal contiguous shares. A warp loads keys, scales and weights ahead by
@@ -46,7 +47,7 @@ struct WeightsArgs {
   AttendArgs a;      // out, lse, ids, parts, jobs unused; scale_log2 = 1
   const float* lse;
   float* weights;
-  float c_hi, c_lo;  // scale * log2(e)
+  float c;           // scale * log2(e)
   float decay;
 };
 
@@ -75,7 +76,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttendArgs& a, int b) {
 template <class C>
 struct GroupRows {
   ItemInfo<C::RR> info;
-  alignas(16) float hi[C::RR], lo[C::RR], nl[C::RR];  // c of the row, its -lse log2(e)
+  alignas(16) float c[C::RR], nl[C::RR];  // scale log2(e) times the unit of the row's terms; -lse log2(e)
 };
 
 template <class C>
@@ -264,24 +265,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             __syncwarp();
             tc_fence_after_sync();
             const bool masks = pos + PAR - 1 > lo_pos;
-            // A part of the rows at a time, each of one token's columns.
-            constexpr int kPart = C::RR < 16 ? C::RR : 16;
-#pragma unroll
+            // A token's rows at a time, of three terms half of 32. (All the code of a
+            // unit for each token in turn: it has to stay in the instruction caches.)
+            constexpr int kPart = C::RR <= 16 || C::T == 2 ? C::RR : 16;
+#pragma unroll 1
             for (int r0 = 0; r0 < RT; r0 += kPart) {
               float e[kPart];
-              const int r1 = r0 % C::RR;
-              score_part<C, kPart>(tm + place * kPlace + r0 / C::RR * C::NQ + r1, e);
+              const int second = PAR == 2 && r0 >= C::RR, r1 = r0 - second * C::RR;  // of an operand row's tokens
+              score_part<C, kPart>(tm + place * kPlace + second * C::NQ + r1, e);
               if (r0 + kPart == RT) {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.s_empty[wg][place]);
               }
-              const float k = k_mul[r0 / C::RR];
+              const float k = second ? k_mul[PAR - 1] : k_mul[0];
 #pragma unroll
               for (int r = 0; r < kPart; r += 2) {
                 const F2 y = f2(e[r], e[r + 1]) * f2(k, k);
-                const F2 x = fma2(y, f2(rows.hi[r1 + r], rows.hi[r1 + r + 1]),
-                                  fma2(y, f2(rows.lo[r1 + r], rows.lo[r1 + r + 1]), f2(rows.nl[r1 + r], rows.nl[r1 + r + 1])));
+                const F2 x = fma2(y, f2(rows.c[r1 + r], rows.c[r1 + r + 1]), f2(rows.nl[r1 + r], rows.nl[r1 + r + 1]));
                 f2_get(x, e[r], e[r + 1]);
                 e[r] = exp2_approx(e[r]);
                 e[r + 1] = exp2_approx(e[r + 1]);
@@ -289,14 +290,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               if (masks) {
 #pragma unroll
                 for (int r = 0; r < kPart; ++r)
-                  if (pos + r0 / C::RR > rows.info.row_pos[r1 + r]) e[r] = 0.0f;
+                  if (pos + second > rows.info.row_pos[r1 + r]) e[r] = 0.0f;
               }
               F2 sum = f2(e[0], e[1]);
 #pragma unroll
               for (int r = 2; r < kPart; r += 2) sum = sum + f2(e[r], e[r + 1]);
               float s0, s1;
               f2_get(sum, s0, s1);
-              acc[r0 / C::RR] += s0 + s1;
+              if (second) acc[PAR - 1] += s0 + s1;
+              else acc[0] += s0 + s1;
             }
           }
 #pragma unroll
@@ -441,8 +443,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (lane < kRows) {
             const bool gives = there && lse != -INFINITY;
             const float t = rows.info.row_mul[r];
-            rows.hi[r] = gives ? t * w.c_hi : 0.0f;
-            rows.lo[r] = gives ? t * w.c_lo : 0.0f;
+            rows.c[r] = gives ? t * w.c : 0.0f;
             rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
             if (!there) rows.info.row_pos[r] = -1;
           }
@@ -508,9 +509,7 @@ cudaError_t launch_kv4_weights(const Kv4WeightsProblem& p, const DeviceInfo& dev
   w.lse = p.lse;
   w.weights = p.weights;
   w.decay = p.decay;
-  const double c = static_cast<double>(p.scale) * 1.4426950408889634;
-  w.c_hi = static_cast<float>(c);
-  w.c_lo = static_cast<float>(c - w.c_hi);
+  w.c = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
   const int64_t most = static_cast<int64_t>(p.cache.B) * p.cache.Hkv * ((p.cache.max_blocks - 1) / a.spt + 1);
   const int grid = static_cast<int>(std::min<int64_t>(dev.sm_count, most));
   CUtensorMap tk;
