@@ -7,7 +7,8 @@
 namespace qsa {
 namespace {
 
-constexpr int kCombineRows = 4;  // rows of a CTA, 128 threads each
+constexpr int kCombineRows = 4;   // rows of a CTA, a warp each
+constexpr int kCombineAhead = 4;  // parts whose values are asked for before their number is known
 // What an item costs beside its tiles, in tiles: a batch of 32 requests of 100
 // tokens and 32 of 16,384 takes 168 us instead of 484 at 0, 256 requests of 64 to
 // 829 tokens 50 us instead of 114, 64 requests of 1,000 to 16,384 tokens 175 at
@@ -17,54 +18,85 @@ constexpr int kItemCost = 5;
 
 // Joins the parts of the item that CTA blockIdx.x of the attention began and
 // others ended: that CTA's second slot and the first slots of the CTAs after
-// it, added in order. A CTA a row would be up to 4,900 CTAs, nearly all with
-// nothing to do, and their launch longer than the work: one token over 1,000
-// tokens took 10.8 us instead of 9.7. The sums are fp32 and the parts added in
-// the order of the tokens, so a call repeats its bits. It is bound by its
-// launch and two dependent loads: about 2 us.
-__global__ void __launch_bounds__(128 * kCombineRows) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float s_f[kCombineRows][kKvMaxCtas];
-  __shared__ float s_max[kCombineRows][4], s_sum[kCombineRows][4];
+// it, added in order. The sums are fp32 and the parts added in the order of the
+// tokens, so a call repeats its bits.
+//
+// It is bound by its launch and its loads' latency, which every call over a whole
+// context waits for: a warp has a row, so that nothing waits for a barrier; the first
+// parts are read (from the workspace, whatever stands there) together with the note
+// that says how many there are; and a CTA is small enough to lie beside one of the
+// attention's, waiting for its end. One token over 1,000 tokens took 8.6 us with CTAs
+// of 512 threads and three loads one after the other.
+__global__ void __launch_bounds__(32 * kCombineRows) kv_combine_kernel(const __grid_constant__ AttendArgs a) {
   pdl_wait();
   pdl_launch_dependents();  // after the wait: at most one kernel ahead of the one that runs
-  const int group = threadIdx.x / 128, tid = threadIdx.x % 128, rows = a.qt * a.R, D = a.c.D;
-  const int c0 = blockIdx.x, r = blockIdx.y * kCombineRows + group;
-  const int4 job = *reinterpret_cast<const int4*>(a.jobs + 4 * c0);
-  if (job.x < 0) return;
-  const int e = job.x, h = job.y, parts = job.z - c0 + 1;
-  const int b = e / a.n_qt, j = (e - b * a.n_qt) * a.qt + r / a.R;
-  const bool there = r < rows && j < a.n;
+  const int lane = threadIdx.x % 32, rows = a.qt * a.R, D = a.c.D, per = D / 64;
+  const int c0 = blockIdx.x, r = blockIdx.y * kCombineRows + threadIdx.x / 32;
+  if (r >= rows) return;
   auto part = [&](int i) { return part_row(a, i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), rows, r); };
-  float m = -INFINITY, l = 0.0f;
-  if (there)
-    for (int i = tid; i < parts; i += 128) m = fmaxf(m, part(i)[D]);
-  m = warp_max(m);
-  if (tid % 32 == 0) s_max[group][tid / 32] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_max[group][0], s_max[group][1]), fmaxf(s_max[group][2], s_max[group][3]));
-  if (there)
-    for (int i = tid; i < parts; i += 128) {
-      const float f = exp2_approx(part(i)[D] - m);
-      s_f[group][i] = f;
-      l += part(i)[D + 1] * f;
-    }
+  const int there = static_cast<int>(gridDim.x) - c0;  // parts that there can be
+  const uint4 job = load_global(reinterpret_cast<const uint4*>(a.jobs + 4 * c0));
+  float2 ml = make_float2(-INFINITY, 0.0f);  // reference and sum of part `lane`
+  if (lane < there) ml = *reinterpret_cast<const float2*>(part(lane) + D);
+  float2 v[kCombineAhead][2];
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-  if (tid % 32 == 0) s_sum[group][tid / 32] = l;
-  __syncthreads();
-  if (!there) return;
-  l = (s_sum[group][0] + s_sum[group][1]) + (s_sum[group][2] + s_sum[group][3]);
-  const int64_t at = (static_cast<int64_t>(b) * a.n + j) * a.Hq + h * a.R + r % a.R;
-  if (tid < D) {
-    float v = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) v += part(i)[tid] * s_f[group][i];
-    v = l == 0.0f ? 0.0f : v / l;
-    if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[at * D + tid] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(a.out)[at * D + tid] = __float2half_rn(v);
+  for (int i = 0; i < kCombineAhead; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (i < there && k < per) v[i][k] = *reinterpret_cast<const float2*>(part(i) + 64 * k + 2 * lane);
+  if (static_cast<int>(job.x) < 0) return;
+  const int e = job.x, h = job.y, parts = static_cast<int>(job.z) - c0 + 1;
+  const int b = e / a.n_qt, j = (e - b * a.n_qt) * a.qt + r / a.R;
+  if (j >= a.n) return;
+  float m = lane < parts ? ml.x : -INFINITY;
+  for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, part(i)[D]);
+  m = warp_max(m);
+  // The weights' sum in four trees, of parts 32 q .. 32 q + 31 (and 128 more) each.
+  float f = lane < parts ? exp2_approx(ml.x - m) : 0.0f, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (32 * q >= parts) break;
+    float l = 0.0f;
+    for (int i = 32 * q + lane; i < parts; i += 128)
+      l += i == lane ? ml.y * f : part(i)[D + 1] * exp2_approx(part(i)[D] - m);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    sums[q] = l;
   }
-  if (a.lse && tid == 0)
-    a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  const float l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const float2 (&x)[2], float w) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k < per) {
+        o[2 * k] += x[k].x * w;
+        o[2 * k + 1] += x[k].y * w;
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < kCombineAhead; ++i)
+    if (i < parts) add(v[i], __shfl_sync(0xFFFFFFFFu, f, i));
+  for (int i0 = kCombineAhead; i0 < parts; i0 += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (i0 + i < parts && k < per) v[i][k] = *reinterpret_cast<const float2*>(part(i0 + i) + 64 * k + 2 * lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= parts) break;
+      if ((i0 + i) % 32 == 0) f = i0 + i + lane < parts ? exp2_approx(part(i0 + i + lane)[D] - m) : 0.0f;
+      add(v[i], __shfl_sync(0xFFFFFFFFu, f, (i0 + i) % 32));
+    }
+  }
+  const int64_t at = (static_cast<int64_t>(b) * a.n + j) * a.Hq + h * a.R + r % a.R;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < per) {
+      const float x = l == 0.0f ? 0.0f : o[2 * k] / l, y = l == 0.0f ? 0.0f : o[2 * k + 1] / l;
+      static_cast<uint32_t*>(a.out)[(at * D + 64 * k) / 2 + lane] = a.bf16 ? bf162_of(x, y) : half2_of(x, y);
+    }
+  if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 // Whether kv_attend_many_kernel takes a call over the whole cache: where a tile
@@ -163,7 +195,7 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   // Items of one tile are never split.
   if (item_tiles == 1) return cudaSuccess;
   e = launch_pdl(kv_combine_kernel, dim3(grid, (a.qt * a.R + kCombineRows - 1) / kCombineRows),
-                 dim3(128 * kCombineRows), 0, stream, a);
+                 dim3(32 * kCombineRows), 0, stream, a);
   if (e == cudaSuccess) plan_add("kv_combine_kernel");
   return e;
 }
