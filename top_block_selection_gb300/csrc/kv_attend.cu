@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(32 * kCombineRows) kv_combine_kernel(const __g
   if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
+constexpr int kJoinTiles = 8;
+
 // Whether kv_attend_many_kernel takes a call over the whole cache: where a tile
 // of its rows is full, and there are so many rows in all that joining parts of
 // 256 rows does not outweigh its faster tiles. Both forms, 4 to 32 heads of 128
@@ -175,10 +177,17 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   const int rt = rows_form(a.qt * a.R * columns);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
   const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
-  const int64_t most = static_cast<int64_t>(p.cache.B) * a.n_qt * a.heads * item_tiles;
-  const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sm_count, kKvMaxCtas), most));
+  const int64_t items = static_cast<int64_t>(p.cache.B) * a.n_qt * a.heads, most = items * item_tiles;
+  const int ctas = std::min(dev.sm_count, kKvMaxCtas);
+  // The join is a launch of its own, about 4 us of a call in a stream and as long as
+  // kJoinTiles tiles of a CTA: where a CTA for each item is no more than that behind
+  // equal shares, nothing is split. (Lists are known here; of whole contexts only
+  // that none has more than item_tiles.)
+  a.per_item = four && !many && items <= ctas &&
+               (p.ids ? item_tiles * (ctas - items) <= kJoinTiles * ctas : item_tiles <= kJoinTiles);
+  const int grid = static_cast<int>(a.per_item ? items : std::min<int64_t>(ctas, most));
   // (No item costs more than another where a CTA has a tile or two.)
-  a.item_cost = many ? kManyItemCost : p.ids || most <= 2 * grid ? 0 : kItemCost;
+  a.item_cost = many ? kManyItemCost : p.ids || a.per_item || most <= 2 * grid ? 0 : kItemCost;
   a.jobs = static_cast<int32_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
 
@@ -193,7 +202,7 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   if (e != cudaSuccess) return e;
   plan_add(four ? "kv4_attend_kernel" : "kv_attend_kernel");
   // Items of one tile are never split.
-  if (item_tiles == 1) return cudaSuccess;
+  if (item_tiles == 1 || a.per_item) return cudaSuccess;
   e = launch_pdl(kv_combine_kernel, dim3(grid, (a.qt * a.R + kCombineRows - 1) / kCombineRows),
                  dim3(32 * kCombineRows), 0, stream, a);
   if (e == cudaSuccess) plan_add("kv_combine_kernel");

@@ -92,6 +92,7 @@ struct AttendArgs {
   int32_t fixed;     // tiles of every item over chosen blocks, else 0
   int32_t item_cost; // what an item costs beside its tiles, in tiles: counts where they are dealt out
   int32_t tile_log2; // log2 of a tile's tokens
+  bool per_item;     // a CTA for each item: none is split, and nothing is joined
   bool bf16;
 };
 
@@ -1276,7 +1277,16 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     start.walk.t = static_cast<int32_t>(lo - at - h * each) - a.item_cost;
     start.entry = en;
   };
-  if (a.fixed > 0) {
+  if (a.per_item) {
+    const int e = static_cast<int>(blockIdx.x) / heads;
+    start.walk.e = e;
+    start.walk.h = static_cast<int32_t>(blockIdx.x) - e * heads;
+    start.walk.t = 0;
+    start.entry = entry_of(a, e);
+    grid = static_cast<int>(gridDim.x);
+    lo = 0;
+    hi = total = start.walk.left = start.entry.tiles;
+  } else if (a.fixed > 0) {
     const int64_t each = static_cast<int64_t>(a.fixed) * heads;
     share(static_cast<int64_t>(entries) * a.fixed);
     const int64_t e = divide(lo, each);
