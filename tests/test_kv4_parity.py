@@ -219,6 +219,21 @@ def test_attend_rows_that_are_not_there(tbs, D):
     check_attend(tbs, [260, 4], 6, 2, 2, D, 32, "bf16")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,n,Hq,Hkv", [([2500, 70, 1300], 1, 8, 2), ([2300, 2200], 3, 12, 4), ([40000], 1, 2, 1)])
+def test_attend_split_items(tbs, D, dtype, lens, n, Hq, Hkv):
+    """Items of more tiles than a CTA takes, in two parts to one for nearly every CTA."""
+    check_attend(tbs, lens, n, Hq, Hkv, D, 64, dtype, plan="kv_combine_kernel", seed=n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,k,plan", [(1, 40, "kv_combine_kernel"), (20, 40, "kv_combine_kernel"), (75, 40, None), (1, 5, None)])
+def test_attend_chosen_items_split_or_not(tbs, D, B, k, plan):
+    check_attend(tbs, [3000] + [200] * (B - 1), 1, 4, 2, D, 64, "f16", ids=(2, k * 128 // D), seed=B, plan=plan or "kv4_attend_kernel")
+    assert ("combine" in tbs.qsa_arm()) == (plan is not None)
+
+
 @pytest.mark.parametrize("D,lists,dtype", [(64, 1, "f16"), (128, 2, "bf16"), (64, 2, "bf16"), (128, 1, "f16")])
 @pytest.mark.parametrize("block,k", [(16, 9), (64, 3), (128, 5)])
 def test_attend_chosen(tbs, D, lists, dtype, block, k):
