@@ -125,7 +125,7 @@ def test_attend_and_weights_reject_bad_arguments(lib):
 
 def test_evict_rejects_bad_arguments(lib):
     for kw in (dict(budget=0), dict(budget=-1), dict(sink=-1), dict(recent=-1), dict(sink=60, recent=5), dict(w=None),
-               dict(sink=(1 << 31) - 1, recent=(1 << 31) - 1), dict(lens=None), dict(lens=A), dict(offset=2 * A), dict(ws=None),
+               dict(sink=(1 << 31) - 1, recent=(1 << 31) - 1), dict(lens=None), dict(lens=A), dict(offset=2 * A), dict(offset=A), dict(ws=None),
                dict(size=2 * 8 * 64 * 4 - 1)):
         assert evict(lib, **kw) == INVALID, kw
     for kw in (dict(w=A + 8), dict(lens=A + 2), dict(offset=A + 1), dict(ws=A + 8)):
