@@ -565,10 +565,11 @@ qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t
  *   decay  finite, not negative.
  *   weights  f32 [n_pages, Hkv, block], 16-byte aligned. The tokens of the
  *          call's sequences are updated, every other slot keeps its value.
- * A page may appear once in the table rows of the call's sequences. Scores and
- * sums are fp32, a query's elements held as by qsa_kv4_attend. Results do not
- * depend on timing. cache->v and v_scale are not read and may be NULL. A token
- * with a NaN scale gets the weight NaN from rows that see it.
+ * A page may hold tokens of one sequence only, and appear once in its table row.
+ * Scores and sums are fp32, a query's elements held as by qsa_kv4_attend. Results
+ * do not depend on timing. cache->v and v_scale are not read and may be NULL. A
+ * key scale of NaN makes its token's weight NaN where a row with another lse than
+ * -inf sees it. With n = 0 nothing changes.
  * Errors as for qsa_kv4_attend (QSA_ERR_INVALID_ARG for a bad decay).
  */
 qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,
@@ -586,12 +587,13 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
  *   budget   >= 1; sink, recent >= 0, sink + recent <= budget.
  *   lens_out int32 [B]: min(lens, budget). May not be lens itself.
  *   offset   optional int32 [B]: grows by the number of tokens that went, as
- *            qsa_kv4_append takes it.
+ *            qsa_kv4_append takes it. May be neither lens nor lens_out.
  *   workspace  device, 16-byte aligned, at least
  *            qsa_kv4_evict_workspace_bytes bytes; needs no initialisation.
  *            Calls that may run at the same time need separate ones.
- * Slots from `budget` on keep what they held. A page of the call's sequences may
- * appear once in their table rows. Block keys are not made anew. A sequence
+ * Slots from `budget` on keep what they held. A page may hold tokens of one
+ * sequence only, and appear once in its table row. Block keys are not made anew
+ * (qsa_kv4_read gives the keys to make them of). A sequence
  * longer than its page table counts as that long; a page outside [0, n_pages)
  * is recorded, its tokens have weight 0, and nothing is moved from or to it.
  * n_new is not read. Errors as for qsa_kv4_append.

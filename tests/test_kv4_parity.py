@@ -339,6 +339,29 @@ def test_weights_rows_that_are_not_there(tbs):
     check_weights(tbs, [300], 32, 32, 1, 128, 64, "f16", 0.0)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16")])
+def test_weights_of_silent_rows(tbs, D, dtype, n):
+    """Rows with lse -inf, and a NaN key scale before the call's tokens: no weight
+    from these rows, and NaN only if another row of the KV head sees the token."""
+    c = kc.make_cache([300, 200], 2, 64, D, seed=n)
+    page = c["table"][0, 1]
+    c["k_scale"][page, :, 5] = np.nan
+    args, _ = on_gpu(c)
+    q = kc.ROUND[dtype](np.random.default_rng(n).standard_normal((2, n, 8, D)))
+    lse = np.full((2, n, 8), 3.0, np.float32)
+    lse[0, :, :4] = -np.inf       # all rows of head 0
+    lse[0, n // 2, 5] = -np.inf   # one of head 1
+    lse[1, :, 6] = -np.inf
+    want, bound = ko.weights(c, q, lse, c["w"], D ** -0.5, 0.5, terms=3 if dtype == "f16" else 2)
+    w = dev(c["w"])
+    tbs.qsa_kv4_weights(dev(q, dtype), dev(lse), *args, w, decay=0.5)
+    got = w.cpu().numpy().astype(np.float64)
+    ok = ~np.isnan(want)
+    assert np.array_equal(np.isnan(got), ~ok) and (np.abs(got - want)[ok] <= bound[ok]).all()
+    assert got[page, 0, 5] == 0.5 * c["w"][page, 0, 5] and np.isnan(got[page, 1, 5])
+
+
 @pytest.mark.parametrize("R", [11, 24, 31, 32])
 @pytest.mark.parametrize("n", [1, 5])
 def test_weights_many_heads_on_one(tbs, R, n):

@@ -77,6 +77,7 @@ template <class C>
 struct GroupRows {
   ItemInfo<C::RR> info;
   alignas(16) float c[C::RR], nl[C::RR];  // scale log2(e) times the unit of the row's terms; -lse log2(e)
+  alignas(8) uint8_t silent[8];           // of a query warp: a row of it has lse -inf, and gives no token any weight
 };
 
 template <class C>
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const AttendArgs& a = w.a;
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
 
+  if (tid < 2 * kGroups) *reinterpret_cast<uint64_t*>(s.rows[tid / kGroups][tid % kGroups].silent) = 0;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.k_full[i], 33);
@@ -264,7 +266,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             wait_or_stop(&s.s_full[wg][place], (unit >> 1) & 1, &s.stop, a.status);
             __syncwarp();
             tc_fence_after_sync();
-            const bool masks = pos + PAR - 1 > lo_pos;
+            // (A score that is not finite would leave NaN, not 0, of a silent row.)
+            const bool masks = pos + PAR - 1 > lo_pos || *reinterpret_cast<const uint64_t*>(rows.silent) != 0;
             // A token's rows at a time, of three terms half of 32. (All the code of a
             // unit for each token in turn: it has to stay in the instruction caches.)
             constexpr int kPart = C::RR <= 16 || C::T == 2 ? C::RR : 16;
@@ -422,6 +425,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int groups = min(per_pass, n_groups - pass * kGroups);
         // A warp's rows are of one group, and loaded together.
         constexpr int kRows = (kGroups * C::RR + kQueryWarps - 1) / kQueryWarps, kWarps = C::RR / kRows;
+        static_assert(kWarps <= 8, "warps of a group");
         const int gr = (warp - C::kFirstQuery) / kWarps, r0 = (warp - C::kFirstQuery) % kWarps * kRows, r = r0 + lane;
         if (gr < groups) {
           GroupRows<C>& rows = s.rows[buf][gr];
@@ -445,8 +449,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float t = rows.info.row_mul[r];
             rows.c[r] = gives ? t * w.c : 0.0f;
             rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
-            if (!there) rows.info.row_pos[r] = -1;
+            if (!gives) rows.info.row_pos[r] = -1;
           }
+          const bool silent = __any_sync(0xFFFFFFFFu, there && lse == -INFINITY);
+          if (lane == 0) rows.silent[(warp - C::kFirstQuery) % kWarps] = silent;
           __syncwarp();
         }
         // The first position that not all of the pass's rows see.
