@@ -36,3 +36,14 @@ def make_cache(lens, Hkv, block, D, seed=0, max_blocks=None, n_new=None, filled=
 
 def copy_cache(c):
     return {k: None if v is None else v.copy() for k, v in c.items()}
+
+
+def roomy(c, rows):
+    """Page tables with room (of pages that there are not) for 10 x 2^20 rows x tokens:
+    calls over these take the form of many rows."""
+    block = c["k"].shape[2]
+    blocks = -(-(10 << 20) // (rows * block))
+    t = np.full((c["table"].shape[0], max(blocks, c["table"].shape[1])), -7, np.int32)
+    t[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = t
+    return c

@@ -283,7 +283,16 @@ MANY = [([256 + 37], 128, 16, 2, 128, "f16"), ([700], 130, 16, 2, 64, "bf16"), (
 @pytest.mark.parametrize("lens,n,Hq,Hkv,D,dtype", MANY, ids=[str(i) for i in range(len(MANY))])
 @pytest.mark.parametrize("block", [16, 64, 128])
 def test_attend_many_rows(tbs, lens, n, Hq, Hkv, D, dtype, block):
-    check_attend(tbs, lens, n, Hq, Hkv, D, block, dtype, plan="kv4_attend_many_kernel")
+    c = kc.roomy(kc.make_cache(lens, Hkv, block, D), len(lens) * n * Hq)
+    check_attend(tbs, lens, n, Hq, Hkv, D, block, dtype, plan="kv4_attend_many_kernel", c=c)
+
+
+@pytest.mark.parametrize("D,few,many", [(64, 2000, 2048), (128, 5000, 5120)])
+def test_attend_many_rows_by_room(tbs, D, few, many):
+    """2,048 rows: a table's room decides, not what it holds."""
+    for room, plan in ((few, "kv4_attend_kernel"), (many, "kv4_attend_many_kernel")):
+        c = kc.make_cache([300], 1, 16, D, max_blocks=room // 16)
+        check_attend(tbs, [300], 128, 16, 1, D, 16, "f16", plan=plan, c=c)
 
 
 @pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16")])
@@ -293,8 +302,8 @@ def test_attend_many_rows_nan_and_ragged(tbs, D, dtype):
         c["v_scale"][page, 0, off] = np.nan
         page, off = ko.place(c, 1, 60)
         c["k_scale"][page, 1, off] = np.nan
-    check_attend(tbs, [200, 150], 128, 16, 2, D, 32, dtype, patch=patch, n_new=[128, 100], spread=4.0,
-                 plan="kv4_attend_many_kernel")
+    c = kc.roomy(kc.make_cache([200, 150], 2, 32, D, n_new=[128, 100], spread=4.0), 4096)
+    check_attend(tbs, [200, 150], 128, 16, 2, D, 32, dtype, patch=patch, plan="kv4_attend_many_kernel", c=c)
 
 
 # ----------------------------------------------------------------- weights

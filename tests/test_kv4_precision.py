@@ -55,8 +55,10 @@ def expected(c, q, b, slot, scale, dtype):
 def check_norm(tbs, c, q, dtype, scale, kernel, seed=0):  # noqa: F811
     """The error's norm over 40 rows is that of the bounds' uniform errors and of
     the result's rounding, give or take a quarter."""
-    args, _ = on_gpu(c)
     B, n, R, _ = q.shape
+    if "many" in kernel:
+        kc.roomy(c, B * n * R)
+    args, _ = on_gpu(c)
     got = tbs.qsa_kv4_attend(dev(q, dtype), *args, scale=scale)
     assert kernel + " " in tbs.qsa_arm() + " "
     got = got.double().cpu().numpy()

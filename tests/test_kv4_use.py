@@ -201,6 +201,8 @@ def test_strided_pages_and_rows(tbs, D, dtype, n, Hq):  # noqa: F811
     """Pages with room between them, queries of a wider projection."""
     lens = [n + 90, n + 1]
     c = kc.make_cache(lens, 1, 32, D, seed=2)
+    if n > 1:
+        kc.roomy(c, 2 * n * Hq)
     args, _ = on_gpu(c)
     for i in (0, 1):
         wide = torch.full((args[i].shape[0], 3, 32, D // 2), 0xFF, dtype=torch.uint8, device="cuda")
@@ -241,7 +243,7 @@ def test_offsets_past_32_bits(tbs):  # noqa: F811
     v = torch.empty_like(k)
     ks = torch.empty((pages, Hkv, block), dtype=torch.bfloat16, device="cuda")
     vs, w = torch.empty_like(ks), torch.empty((pages, Hkv, block), device="cuda")
-    c = kc.make_cache([300], Hkv, block, D, seed=1, filled=False)
+    c = kc.roomy(kc.make_cache([300], Hkv, block, D, seed=1, filled=False), 129 * 2 * Hkv)
     near, _ = on_gpu(c)
     table, lens = dev(c["table"] + (pages - 20)), dev(c["lens"])
     far = [k, v, ks, vs, table, lens]
@@ -285,13 +287,26 @@ def test_longer_than_the_page_table(tbs, D, n, Hq):  # noqa: F811
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(args, before))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_longer_than_the_page_table(tbs, D):  # noqa: F811
+    """6,000 tokens, a table for 5,120."""
+    c = kc.make_cache([6000], 1, 128, D, seed=4)
+    c["table"] = np.ascontiguousarray(c["table"][:, :40])
+    args, _ = on_gpu(c)
+    q = kc.as_f16(np.random.default_rng(1).standard_normal((1, 128, 16, D)))
+    got = tbs.qsa_kv4_attend(dev(q, "f16"), *args)
+    assert "kv4_attend_many_kernel" in tbs.qsa_arm() and tbs.qsa_device_status(clear=True) == (1, 32)
+    want, _, bound = ko.attend(c, q[:, -3:], D ** -0.5, np.array([[[list(range(40))] * 3]], np.int32))
+    close(got[:, -3:], want, bound, "f16")
+
+
 @pytest.mark.parametrize("block", [16, 64, 128])
 @pytest.mark.parametrize("D", [64, 128])
 def test_pages_outside(tbs, block, D):  # noqa: F811
     """One page id outside the cache, at each of the blocks in turn."""
     blocks = 256 // block + 2
     L = blocks * block - 3
-    c = kc.make_cache([L], 1, block, D, seed=block)
+    c = kc.roomy(kc.make_cache([L], 1, block, D, seed=block), 130 * 16)
     args, _ = on_gpu(c)
     q = kc.as_f16(np.random.default_rng(2).standard_normal((1, 130, 16, D)))
     for i in range(blocks):

@@ -34,7 +34,7 @@ SOURCES = ["qsa_runtime.cu", "score_tc.cu", "select.cu", "convert.cu", "fused.cu
            "split_reduce.cu", "split_reduce_static.cu", "kv_append.cu", "kv_attend.cu",
            "kv_attend_many.cu", "kv_attend_d64_t2.cu", "kv_attend_d64_t3.cu", "kv_attend_d128_t2.cu", "kv_attend_d128_t3.cu",
            "kv4_append.cu", "kv4_evict.cu", "kv4_attend_d64_t2.cu", "kv4_attend_d64_t3.cu", "kv4_attend_d128_t2.cu",
-           "kv4_attend_d128_t3.cu", "kv4_weights.cu", "qsa_api.cpp"]
+           "kv4_attend_d128_t3.cu", "kv4_attend_many.cu", "kv4_weights.cu", "qsa_api.cpp"]
 HEADERS = ["qsa_device.cuh", "qsa_internal.h", "select_row.cuh", "select_warp.cuh", "fused_kernel.cuh",
            "kv_internal.h", "kv_rows.cuh", "kv4_codes.cuh",
            "kv_attend_kernel.cuh", "kv_attend_many.cuh"]

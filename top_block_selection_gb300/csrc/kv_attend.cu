@@ -99,7 +99,21 @@ __global__ void __launch_bounds__(32 * kCombineRows) kv_combine_kernel(const __g
   if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
+// 4-bit cache: the join is a launch of its own, about 4 us of a call in a stream, as
+// long as so many tiles of a CTA. Where a CTA for each item is no more than that
+// behind equal shares, nothing is split (one token over 1,000 tokens 6.9 us instead
+// of 8.1, 32 requests with 64 chosen blocks 20.4 instead of 25.1; 4 and 16 tiles were
+// no better).
 constexpr int kJoinTiles = 8;
+// 4-bit cache: tiles of a CTA up to which the heads of an item are split in two where
+// one item's columns would need the form of 32, which takes 1.8 to 2 times as long a
+// tile as that of 16 but has half of the tiles. us (split | whole), 32 heads on each
+// of 2 KV heads, 128 dimensions, fp16: 64 requests of 2,000 tokens (13 tiles a CTA)
+// 34.0 | 39.2, 2 of 131,073 (27) 45.2 | 47.5, 32 of 8,000 (27) 45.3 | 45.8, 64 of 8,000
+// (53) 83.9 | 77.7, 16 of 40,000 (66) 97.9 | 83.7; bf16 31.8 | 33.0, 38.3 | 39.9,
+// 40.1 | 38.6, 70.2 | 65.6, 78.2 | 70.8. (16 heads of 64 dimensions: 64 of 8,000
+// 43.7 | 46.0, 128 of 8,000 75.8 | 79.7, bf16 72.8 | 69.7.)
+constexpr int kSplitTiles = 32;
 
 // Whether kv_attend_many_kernel takes a call over the whole cache: where a tile
 // of its rows is full, and there are so many rows in all that joining parts of
@@ -112,6 +126,23 @@ constexpr int kJoinTiles = 8;
 // not measured.
 bool takes_many(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
   return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 2048;
+}
+
+// The same for the 4-bit cache, where it takes `tokens` into account, those that a
+// table has room for. us (many | kv_attend_kernel), fp16, 128 dimensions: 1 x 512 rows
+// over 32,768 tokens 40.0 | 41.8, over 131,072 68.5 | 126; 1 x 1,024 over 8,192 30.5 | 29.4,
+// over 32,768 44.3 | 71.0; 8 x 128 over 8,192 32.4 | 28.0, over 32,768 60.1 | 70.8;
+// 2 x 1,024 over 1,024 21.5 | 11.4, over 4,096 29.1 | 31.0, over 8,192 35.1 | 45.0; 8 x 512
+// over 1,024 26.1 | 27.8. 64 dimensions: 1 x 512 over 8,192 24.8 | 19.4, over 32,768
+// 31.8 | 39.2; 1 x 1,024 over 4,096 21.3 | 20.8, over 8,192 22.6 | 27.4; 2 x 1,024 over
+// 1,024 16.7 | 18.7, over 4,096 21.8 | 30.7. The first form costs 6 to 10 us more for
+// any call and, of rows times tokens, a third of the time.
+bool may_take_many4(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
+  return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 512;
+}
+bool takes_many4(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D, int64_t tokens) {
+  return may_take_many4(B, n, Hq, Hkv) &&
+         static_cast<double>(B) * n * Hq * tokens >= (D == 128 ? 10.0 : 4.0) * (1 << 20);
 }
 
 // Rows of the instantiation for `rows` of them.
@@ -130,9 +161,9 @@ bool encode_cache_map(CUtensorMap* tm, const uint8_t* base, const KvCacheArgs& c
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
+size_t workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D, bool four) {
   if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kKvMaxGroup || (D != 64 && D != 128)) return 0;
-  const size_t rows = takes_many(B, n, Hq, Hkv) ? 2 * kManyRows : kKvMaxGroup;
+  const size_t rows = (four ? may_take_many4 : takes_many)(B, n, Hq, Hkv) ? 2 * kManyRows : kKvMaxGroup;
   return sizeof(float) * 2 * kKvMaxCtas * rows * (static_cast<size_t>(D) + 2) + 4 * sizeof(int32_t) * kKvMaxCtas;
 }
 
@@ -158,40 +189,45 @@ cudaError_t launch(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t
   // holds too much state for its threads and takes more than twice as long a
   // tile) or two of up to 128. A row of the 4-bit cache's 64 dimensions has a
   // column for each of the two tokens in an operand row.
-  const bool many = !p.ids && takes_many(p.cache.B, p.n, p.Hq, p.cache.Hkv);
-  const int columns = four && !many ? 128 / p.cache.D : 1;
+  const KvCacheArgs& c = p.cache;
+  const bool many = !p.ids && (four ? takes_many4(c.B, p.n, p.Hq, c.Hkv, c.D, static_cast<int64_t>(c.max_blocks) * c.block)
+                                    : takes_many(c.B, p.n, p.Hq, c.Hkv));
+  const int columns = four && !many ? 128 / c.D : 1;
+  a.tile_log2 = columns == 2 ? 8 : 7;
+  a.spt = (1 << a.tile_log2) / c.block;
+  a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
+  const int64_t item_tiles = a.fixed > 0 ? a.fixed : (c.max_blocks - 1) / a.spt + 1;
+  const int ctas = std::min(dev.sm_count, kKvMaxCtas);
+  // Whether a CTA has an item each. (Lists are known here; of whole contexts only
+  // that none has more than item_tiles.)
+  auto an_item_each = [&](int64_t items) {
+    return four && !many && items <= ctas &&
+           (p.ids ? item_tiles * (ctas - items) <= kJoinTiles * ctas : item_tiles <= kJoinTiles);
+  };
   if (four && !many && a.R * columns > 16) {
-    // The form of 32 columns takes four times as long a tile as that of 16: the heads
-    // are split over two items (or more, where two equal parts do not do it or there
-    // are none), which read the same tiles at about the same time, from L2.
+    // Split (where two equal parts of 16 columns or fewer make an item of up to 32)
+    // items read the same tiles, at about the same time while there are few of them.
     const int fine = head_split(a.R, columns, 16), least = head_split(a.R, columns, 32);
-    a.split = fine <= 2 * least ? fine : least;
+    const int64_t items = static_cast<int64_t>(c.B) * p.n * c.Hkv;  // of one query each
+    const bool pays = an_item_each(items * fine) ||
+                      (!an_item_each(items * least) && items * least * item_tiles <= kSplitTiles * ctas);
+    a.split = fine <= 2 * least && pays ? fine : least;
     a.R /= a.split;
   }
-  a.heads = p.cache.Hkv * a.split;
-  a.tile_log2 = columns == 2 ? 8 : 7;
-  a.spt = (1 << a.tile_log2) / p.cache.block;
+  a.heads = c.Hkv * a.split;
   a.qt = p.ids ? 1 : many ? 2 * (kManyRows / a.R) : std::max(1, std::min(p.n, 16 / (a.R * columns)));
   a.n_qt = (p.n + a.qt - 1) / a.qt;
-  a.fixed = p.ids ? (p.k + a.spt - 1) / a.spt : 0;
   const int rt = rows_form(a.qt * a.R * columns);
   // One CTA an SM, or one a tile where the lists or tables allow fewer tiles.
-  const int64_t item_tiles = a.fixed > 0 ? a.fixed : (p.cache.max_blocks - 1) / a.spt + 1;
-  const int64_t items = static_cast<int64_t>(p.cache.B) * a.n_qt * a.heads, most = items * item_tiles;
-  const int ctas = std::min(dev.sm_count, kKvMaxCtas);
-  // The join is a launch of its own, about 4 us of a call in a stream and as long as
-  // kJoinTiles tiles of a CTA: where a CTA for each item is no more than that behind
-  // equal shares, nothing is split. (Lists are known here; of whole contexts only
-  // that none has more than item_tiles.)
-  a.per_item = four && !many && items <= ctas &&
-               (p.ids ? item_tiles * (ctas - items) <= kJoinTiles * ctas : item_tiles <= kJoinTiles);
+  const int64_t items = static_cast<int64_t>(c.B) * a.n_qt * a.heads, most = items * item_tiles;
+  a.per_item = an_item_each(items);
   const int grid = static_cast<int>(a.per_item ? items : std::min<int64_t>(ctas, most));
   // (No item costs more than another where a CTA has a tile or two.)
   a.item_cost = many ? kManyItemCost : p.ids || a.per_item || most <= 2 * grid ? 0 : kItemCost;
   a.jobs = static_cast<int32_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(a.jobs + 4 * kKvMaxCtas);
 
-  if (many) return launch_attend_many(a, grid, item_tiles > 1, dev.id, stream);
+  if (many) return (four ? launch_attend4_many : launch_attend_many)(a, grid, item_tiles > 1, dev.id, stream);
 
   CUtensorMap tk, tv;
   const auto encode = four ? encode_cache_map4 : encode_cache_map;
@@ -233,10 +269,10 @@ int head_split(int R, int per_row, int columns) {
 }
 
 size_t kv_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
-  return workspace_bytes(B, n, Hq, Hkv, D);
+  return workspace_bytes(B, n, Hq, Hkv, D, false);
 }
 size_t kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D) {
-  return workspace_bytes(B, n, Hq, Hkv, D);
+  return workspace_bytes(B, n, Hq, Hkv, D, true);
 }
 
 cudaError_t launch_kv_attend(const KvAttendProblem& p, const DeviceInfo& dev, cudaStream_t stream) {

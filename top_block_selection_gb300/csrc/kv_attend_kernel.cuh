@@ -1251,8 +1251,10 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 // than it has, in front of them; lo is given as the first tile's place. Every item of a list has the same
 // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
 // to the calling threads: kThreads of them, whole warps from kFirst on (by way
-// of scan and shared, in shared memory, and barrier kBarrier).
-template <int kThreads, int kFirst, int kBarrier>
+// of scan and shared, in shared memory, and barrier kBarrier). Without kItems,
+// a.per_item is not looked at: kernels of which no call has it would pay for the
+// code (kv_attend_many_kernel 2%, of 4,096 queries over 32,768 tokens).
+template <int kThreads, int kFirst, int kBarrier, bool kItems>
 __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, Start& shared, Start& start,
                                            int64_t& total, int64_t& lo, int64_t& hi, int& grid) {
   const int tid = threadIdx.x - kFirst, warp = tid / 32, lane = tid % 32;
@@ -1277,7 +1279,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     start.walk.t = static_cast<int32_t>(lo - at - h * each) - a.item_cost;
     start.entry = en;
   };
-  if (a.per_item) {
+  if (kItems && a.per_item) {
     const int e = static_cast<int>(blockIdx.x) / heads;
     start.walk.e = e;
     start.walk.h = static_cast<int32_t>(blockIdx.x) - e * heads;
@@ -1407,7 +1409,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     Start start{};
     int64_t total, lo, hi;
     int grid;
-    find_share<C::kThreads - kService, kService, 10>(a, s.scan, s.share.start, start, total, lo, hi, grid);
+    find_share<C::kThreads - kService, kService, 10, C::kFour>(a, s.scan, s.share.start, start, total, lo, hi, grid);
     if (tid == kService) {
       s.share.start = start;
       s.share.lo = lo;

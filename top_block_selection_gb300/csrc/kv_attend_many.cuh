@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv_attend_many_kernel(const _
       if (threadIdx.x == 256) a.jobs[4 * blockIdx.x] = -1;
       Share found{};
       int grid;
-      find_share<128, 256, 1>(a, s.scan, s.share.start, found.start, found.total, found.lo, found.hi, grid);
+      find_share<128, 256, 1, false>(a, s.scan, s.share.start, found.start, found.total, found.lo, found.hi, grid);
       if (threadIdx.x == 256) {
         found.grid = grid;
         s.share = found;
@@ -1046,7 +1046,46 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_combine_many_kernel(const 
   if (a.lse && d0 == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
-// kv_attend_many.cu; one CTA an SM, then the join where items may be split.
+// One CTA an SM, then the join where items may be split.
+// One cache's launches (kv_attend_many.cu, kv4_attend_many.cu).
+template <int D, bool BF16, bool FOUR>
+cudaError_t many_form(const AttendArgs& a, int grid, bool split, int device, cudaStream_t stream) {
+  constexpr int smem = 1024 + 6 * kKvTile * D * 2 + static_cast<int>(sizeof(ManyShared<D, FOUR>));
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << device;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv_attend_many_kernel<D, BF16, FOUR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  cudaError_t e = launch_pdl(kv_attend_many_kernel<D, BF16, FOUR>, dim3(grid), dim3(kManyThreads), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  plan_add(FOUR ? "kv4_attend_many_kernel" : "kv_attend_many_kernel");
+  if (!split) return cudaSuccess;
+  const int64_t items = static_cast<int64_t>(a.c.B) * a.n_qt * a.c.Hkv;
+  // Few items have many parts each: more CTAs an item read them.
+  constexpr int kRowGroups = 2 * kManyRows / 32;
+  if (items * 4 < grid)
+    e = launch_pdl(kv_combine_many_kernel<D, 2>, dim3(grid, D / (2 * kJoinWarps), kRowGroups), dim3(32 * kJoinWarps), 0,
+                   stream, a);
+  else
+    e = launch_pdl(kv_combine_many_kernel<D, 8>, dim3(grid, D / (8 * kJoinWarps), kRowGroups), dim3(32 * kJoinWarps), 0,
+                   stream, a);
+  if (e == cudaSuccess) plan_add("kv_combine_many_kernel");
+  return e;
+}
+
+template <bool FOUR>
+cudaError_t launch_many(const AttendArgs& a, int grid, bool split, int device, cudaStream_t stream) {
+  if (a.c.D == 64)
+    return a.bf16 ? many_form<64, true, FOUR>(a, grid, split, device, stream)
+                  : many_form<64, false, FOUR>(a, grid, split, device, stream);
+  return a.bf16 ? many_form<128, true, FOUR>(a, grid, split, device, stream)
+                : many_form<128, false, FOUR>(a, grid, split, device, stream);
+}
 cudaError_t launch_attend_many(const AttendArgs& a, int grid, bool split, int device, cudaStream_t stream);
+cudaError_t launch_attend4_many(const AttendArgs& a, int grid, bool split, int device, cudaStream_t stream);
 
 }  // namespace qsa
