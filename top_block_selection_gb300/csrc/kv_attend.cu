@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kCombineRows = 4;   // rows of a CTA, a warp each
 constexpr int kCombineAhead = 4;  // parts whose values are asked for before their number is known
+constexpr int kCombineLoads = 12;  // parts after these, asked for together (4: 2 x 131,073 tokens of 8 bits 53.4 us, not 52.5)
 // What an item costs beside its tiles, in tiles: a batch of 32 requests of 100
 // tokens and 32 of 16,384 takes 168 us instead of 484 at 0, 256 requests of 64 to
 // 829 tokens 50 us instead of 114, 64 requests of 1,000 to 16,384 tokens 175 at
@@ -76,17 +77,18 @@ __global__ void __launch_bounds__(32 * kCombineRows) kv_combine_kernel(const __g
 #pragma unroll
   for (int i = 0; i < kCombineAhead; ++i)
     if (i < parts) add(v[i], __shfl_sync(0xFFFFFFFFu, f, i));
-  for (int i0 = kCombineAhead; i0 < parts; i0 += 4) {
+  for (int i0 = kCombineAhead; i0 < parts; i0 += kCombineLoads) {
+    float2 u[kCombineLoads][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kCombineLoads; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (i0 + i < parts && k < per) v[i][k] = *reinterpret_cast<const float2*>(part(i0 + i) + 64 * k + 2 * lane);
+        if (i0 + i < parts && k < per) u[i][k] = *reinterpret_cast<const float2*>(part(i0 + i) + 64 * k + 2 * lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kCombineLoads; ++i) {
       if (i0 + i >= parts) break;
       if ((i0 + i) % 32 == 0) f = i0 + i + lane < parts ? exp2_approx(part(i0 + i + lane)[D] - m) : 0.0f;
-      add(v[i], __shfl_sync(0xFFFFFFFFu, f, (i0 + i) % 32));
+      add(u[i], __shfl_sync(0xFFFFFFFFu, f, (i0 + i) % 32));
     }
   }
   const int64_t at = (static_cast<int64_t>(b) * a.n + j) * a.Hq + h * a.R + r % a.R;

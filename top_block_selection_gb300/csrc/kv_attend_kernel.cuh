@@ -113,6 +113,11 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 struct Entry {
   int32_t b, j0, nq, first_pos, last_pos, tiles;
 };
+//
+// FOUR, here and below: kv_attend_kernel over the 4-bit cache. The others have tiles
+// of 128 tokens, as many items as KV heads and none to a CTA each, and do not look
+// at what says so (kv_attend_many_kernel took 2% longer with that code).
+template <bool FOUR>
 __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
   Entry t;
   t.b = a.n_qt > 1 ? e / a.n_qt : e;
@@ -125,7 +130,7 @@ __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int e) {
     t.tiles = a.fixed;
   } else {
     const int keys = min(t.last_pos + 1, a.c.max_blocks * a.c.block);
-    t.tiles = keys > 0 ? ((keys - 1) >> a.tile_log2) + 1 : 1;
+    t.tiles = keys > 0 ? ((keys - 1) >> (FOUR ? a.tile_log2 : 7)) + 1 : 1;
   }
   return t;
 }
@@ -500,7 +505,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
   int en_of = w.e;
   while (w.left > 0 && ok) {
     if (en_of != w.e) {
-      en = entry_of(a, w.e);
+      en = entry_of<C::kFour>(a, w.e);
       en_of = w.e;
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
@@ -611,7 +616,7 @@ __device__ void attend_produce(const AttendArgs& a, const CUtensorMap* tm_k, con
     }
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, kErrCacheIndex);
     g0 += part;
-    step(w, part, en.tiles, a.heads, a.item_cost);
+    step(w, part, en.tiles, C::kFour ? a.heads : a.c.Hkv, a.item_cost);
   }
   if (!ok) {  // let the copies in flight land before the CTA gives its memory back
     const uint32_t n = min(last, static_cast<uint32_t>(C::kStages / W));
@@ -747,7 +752,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       break;
     }
     if (en_of != w.e) {
-      en = entry_of(a, w.e);
+      en = entry_of<C::kFour>(a, w.e);
       en_of = w.e;
     }
     const int part = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
@@ -760,7 +765,7 @@ __device__ void attend_queries(const AttendArgs& a, AttendShared<C>& s, uint8_t*
       if (lane == 0) mbar_arrive(&s.q_full[buf]);
     }
     at += w.t + part + a.item_cost;
-    step(w, part, en.tiles, a.heads, a.item_cost);
+    step(w, part, en.tiles, C::kFour ? a.heads : a.c.Hkv, a.item_cost);
   }
 }
 
@@ -1251,14 +1256,12 @@ __device__ void attend_consume(const AttendArgs& a, AttendShared<C>& s, uint8_t*
 // than it has, in front of them; lo is given as the first tile's place. Every item of a list has the same
 // tiles; up to 32 query tiles are one to a lane of every warp; more are dealt
 // to the calling threads: kThreads of them, whole warps from kFirst on (by way
-// of scan and shared, in shared memory, and barrier kBarrier). Without kItems,
-// a.per_item is not looked at: kernels of which no call has it would pay for the
-// code (kv_attend_many_kernel 2%, of 4,096 queries over 32,768 tokens).
-template <int kThreads, int kFirst, int kBarrier, bool kItems>
+// of scan and shared, in shared memory, and barrier kBarrier).
+template <int kThreads, int kFirst, int kBarrier, bool FOUR>
 __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, Start& shared, Start& start,
                                            int64_t& total, int64_t& lo, int64_t& hi, int& grid) {
   const int tid = threadIdx.x - kFirst, warp = tid / 32, lane = tid % 32;
-  const int entries = a.c.B * a.n_qt, heads = a.heads;
+  const int entries = a.c.B * a.n_qt, heads = FOUR ? a.heads : a.c.Hkv;
   auto share = [&](int64_t tiles) {
     total = tiles * heads;
     grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
@@ -1279,12 +1282,12 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     start.walk.t = static_cast<int32_t>(lo - at - h * each) - a.item_cost;
     start.entry = en;
   };
-  if (kItems && a.per_item) {
+  if (FOUR && a.per_item) {
     const int e = static_cast<int>(blockIdx.x) / heads;
     start.walk.e = e;
     start.walk.h = static_cast<int32_t>(blockIdx.x) - e * heads;
     start.walk.t = 0;
-    start.entry = entry_of(a, e);
+    start.entry = entry_of<FOUR>(a, e);
     grid = static_cast<int>(gridDim.x);
     lo = 0;
     hi = total = start.walk.left = start.entry.tiles;
@@ -1292,10 +1295,10 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     const int64_t each = static_cast<int64_t>(a.fixed) * heads;
     share(static_cast<int64_t>(entries) * a.fixed);
     const int64_t e = divide(lo, each);
-    begin(static_cast<int>(e), entry_of(a, static_cast<int>(e)), e * each);
+    begin(static_cast<int>(e), entry_of<FOUR>(a, static_cast<int>(e)), e * each);
   } else if (entries <= 32) {
     Entry mine{};
-    if (lane < entries) mine = entry_of(a, lane);
+    if (lane < entries) mine = entry_of<FOUR>(a, lane);
     const int units = lane < entries ? mine.tiles + a.item_cost : 0;
     int64_t before = units;
 #pragma unroll
@@ -1320,7 +1323,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
     int64_t sum = 0;
     Entry mine{};
     for (int64_t e = e0; e < e1; ++e) {
-      mine = entry_of(a, static_cast<int>(e));
+      mine = entry_of<FOUR>(a, static_cast<int>(e));
       sum += mine.tiles + a.item_cost;
     }
     int64_t before = sum;
@@ -1344,7 +1347,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* scan, S
       int64_t e = e0;
       if (per > 1)
         for (;; ++e) {
-          mine = entry_of(a, static_cast<int>(e));
+          mine = entry_of<FOUR>(a, static_cast<int>(e));
           const int64_t units = static_cast<int64_t>(mine.tiles + a.item_cost) * heads;
           if (lo < at + units) break;
           at += units;

@@ -160,13 +160,13 @@ __device__ __forceinline__ void many_items(const AttendArgs& a, const Start& sta
   int64_t at = lo - w.t;
   while (w.left > 0) {
     if (en_of != w.e) {
-      en = entry_of(a, w.e);
+      en = entry_of<false>(a, w.e);
       en_of = w.e;
     }
     const int tiles = static_cast<int>(min(static_cast<int64_t>(en.tiles - w.t), w.left));
     f(en, ManyItem{w.e, w.h, w.t, tiles, at});
     at += en.tiles + a.item_cost;
-    step(w, tiles, en.tiles, a.heads, a.item_cost);
+    step(w, tiles, en.tiles, a.c.Hkv, a.item_cost);
   }
 }
 // Until the CTA's share is known and the accumulators' memory is there.
