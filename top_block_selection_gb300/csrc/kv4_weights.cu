@@ -19,8 +19,13 @@
 // cycles a tile beside its waits.) More rows than that go over the share's tiles of the item again
 // (from L2), adding to what the pass before left.
 //
-// What bounds it: for a decode step the keys and weights from HBM; for many rows
-// the exponentials.
+// What bounds it: for a decode step the keys and weights from HBM (64 requests over
+// 1,000 to 16,384 tokens, 8 KV heads: 60.7 us, 5.4 TB/s, 81% of a plain copy's rate; the
+// rest is the start, the first tiles' chain of lengths, pages and loads). For many
+// rows no unit is near its rate (64 rows over 32,805 tokens, 32 heads on 8 KV heads:
+// 32.7 us, 524 TFLOP/s; exponentials and products 20% of the cycles each): a
+// warpgroup's chain of tensor memory read, exponentials and sums is what a tile
+// takes, and the queries' terms are made before the first.
 #include "kv_attend_kernel.cuh"
 
 #include <algorithm>
