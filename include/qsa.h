@@ -542,7 +542,9 @@ qsa_status qsa_kv4_read(const qsa_kv4_cache* cache, int32_t n, qsa_dtype dtype, 
  * NULL) or over chosen blocks. Everything is as for qsa_kv_attend, with slots
  * for positions, but a NaN scale makes every dimension of the rows that see its
  * token NaN; of 64 dimensions "the last 3,000 (1,500) or so" tokens are twice as
- * many; and in calls of many rows keys whose scale is below 2^-25 of the largest among
+ * many; calls of few rows are those with ids, with Hq / Hkv * n < 128, with
+ * B * n * Hq < 512 or with B * n * Hq * max_blocks * block < 10 * 2^20 (4 * 2^20 of
+ * 64 dimensions); and in calls of many rows keys whose scale is below 2^-25 of the largest among
  * slots 16 i to 16 i + 15 are held to 2^-37 of what that one stands for.
  */
 size_t qsa_kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
