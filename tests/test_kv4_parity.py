@@ -213,6 +213,15 @@ def test_attend_many_heads_on_one(tbs, R, D, dtype):
     check_attend(tbs, [300, 45], 1, 2 * R, 2, D, 32, dtype, ids=(2, 3), seed=R)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,R", [(64, 12), (64, 16), (64, 32), (128, 24), (128, 32)])
+@pytest.mark.parametrize("room", [4096, 1300000])
+def test_attend_heads_split_or_whole(tbs, D, R, dtype, room):
+    """More than 16 columns, over tables with room for few tiles a CTA and for many."""
+    c = kc.make_cache([4000, 100], 1, 128, D, seed=R, max_blocks=room // 128)
+    check_attend(tbs, [4000, 100], 1, R, 1, D, 128, dtype, plan="kv_combine_kernel", c=c)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attend_rows_that_are_not_there(tbs, D):
     check_attend(tbs, [70, 41, 3, 0, 130], 9, 4, 1, D, 64, "f16", n_new=[0, 4, 9, 9, 1])
