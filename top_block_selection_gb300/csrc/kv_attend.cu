@@ -138,7 +138,8 @@ bool takes_many(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
 // over 1,024 26.1 | 27.8. 64 dimensions: 1 x 512 over 8,192 24.8 | 19.4, over 32,768
 // 31.8 | 39.2; 1 x 1,024 over 4,096 21.3 | 20.8, over 8,192 22.6 | 27.4; 2 x 1,024 over
 // 1,024 16.7 | 18.7, over 4,096 21.8 | 30.7. The first form costs 6 to 10 us more for
-// any call and, of rows times tokens, a third of the time.
+// any call and, of rows times tokens, a third of the time. (Under 512 rows, where
+// only contexts past 32,768 tokens would gain, calls keep the small workspace.)
 bool may_take_many4(int32_t B, int32_t n, int32_t Hq, int32_t Hkv) {
   return static_cast<int64_t>(n) * (Hq / Hkv) >= kManyRows && static_cast<int64_t>(B) * n * Hq >= 512;
 }
