@@ -350,14 +350,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) continue;
             const uint32_t there = __ballot_sync(0xFFFFFFFFu, my_k == i && page >= 0);
+            const int64_t row0 = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
+            // The rows go ahead of the elected lane's arrival, which publishes them: the
+            // asynchronous arrivals below only stand for the copies ahead of them.
+            if (my_k == i) s.row0[st][my_slot] = row0;
+            __syncwarp();
             // Codes count as they are packed, half of a slab's bytes.
             if (elect_one()) mbar_arrive_expect_tx(&s.k_full[st], __popc(there) * (slab / 2));
             __syncwarp();
-            const int64_t row0 = page >= 0 ? (static_cast<int64_t>(page) * a.c.Hkv + h) * a.c.block : -1;
-            if (my_k == i) {  // each lane of the tile brings its own block's keys
-              s.row0[st][my_slot] = row0;
-              if (page >= 0) tma_load_3d(ring + st * kTile + my_slot * slab, &tm_k, 0, y, page, &s.k_full[st]);
-            }
+            // Each lane of the tile brings its own block's keys.
+            if (my_k == i && page >= 0) tma_load_3d(ring + st * kTile + my_slot * slab, &tm_k, 0, y, page, &s.k_full[st]);
             // Scales and weights by 16-byte copies of all lanes: bulk copies of a
             // block's few bytes took 700 cycles a tile to issue.
             {
