@@ -82,7 +82,7 @@ template <class C>
 struct GroupRows {
   ItemInfo<C::RR> info;
   alignas(16) float c[C::RR], nl[C::RR];  // scale log2(e) times the unit of the row's terms; -lse log2(e)
-  alignas(8) uint8_t silent[8];           // of a query warp: a row of it has lse -inf, and gives no token any weight
+  alignas(8) uint8_t silent[8];           // of a query warp: a row of it (with lse -inf, or not there) gives no token any weight
 };
 
 template <class C>
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             rows.nl[r] = gives ? lse * -1.4426950408889634f : -INFINITY;
             if (!gives) rows.info.row_pos[r] = -1;
           }
-          const bool silent = __any_sync(0xFFFFFFFFu, there && lse == -INFINITY);
+          // (Rows that are not there too: a group of them alone is masked as a silent one is.)
+          const bool silent = __any_sync(0xFFFFFFFFu, lane < kRows && row < a.qt * a.R && en.j0 + j < a.n && lse == -INFINITY);
           if (lane == 0) rows.silent[(warp - C::kFirstQuery) % kWarps] = silent;
           __syncwarp();
         }
