@@ -592,7 +592,9 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
  *            qsa_kv4_append takes it. May be neither lens nor lens_out.
  *   workspace  device, 16-byte aligned, at least
  *            qsa_kv4_evict_workspace_bytes bytes; needs no initialisation.
- *            Calls that may run at the same time need separate ones.
+ *            Calls that may run at the same time need separate ones. A budget of
+ *            max_blocks * block or more, the longest sequence that there can be,
+ *            takes nothing out and needs none (NULL).
  * Slots from `budget` on keep what they held. A page may hold tokens of one
  * sequence only, and appear once in its table row. Block keys are not made anew
  * (qsa_kv4_read gives the keys to make them of). A sequence

@@ -713,7 +713,7 @@ def qsa_kv4_weights(q, lse, k_cache, v_cache, k_scale, v_scale, page_table, lens
 
 
 def qsa_kv4_evict_workspace_bytes(B: int, Hkv: int, budget: int) -> int:
-    """Bytes of workspace qsa_kv4_evict needs."""
+    """Bytes of workspace qsa_kv4_evict needs for a budget below what the page table has room for."""
     return int(load_library().qsa_kv4_evict_workspace_bytes(B, Hkv, budget))
 
 
@@ -724,7 +724,9 @@ def qsa_kv4_evict(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights,
     those of the largest weights (equal ones: the lowest slot first), in their
     order. offset, an optional int32 [B], grows by the tokens that went. Returns
     lens_out int32 [B], min(lens, budget) (a tensor other than lens, allocated
-    here when not given)."""
+    here when not given). workspace: a CUDA uint8 tensor of
+    qsa_kv4_evict_workspace_bytes, allocated here when not given; a budget of
+    the page table's tokens or more takes nothing out and needs none."""
     r = (_KV or _kv_binding()).evict4(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, budget, sink,
                                       recent, offset, lens_out, workspace)
     if r.__class__ is int:

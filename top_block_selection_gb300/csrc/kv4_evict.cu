@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kv4_evict_kernel(const _
     }
   };
 
-  int32_t* const list = a.list + static_cast<int64_t>(item) * a.budget;
+  int32_t* const list = a.list + static_cast<int64_t>(item) * a.budget;  // (there is one: the budget is below some length)
   if (keep > 0) {
     __syncthreads();  // the histograms are clear
     // Four slots a load, the first aligned; four such loads of a thread together.

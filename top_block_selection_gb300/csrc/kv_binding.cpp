@@ -386,7 +386,7 @@ PyObject* evict4(PyObject*, PyObject* const* a, Py_ssize_t count) {
       const Tensor& t = tensor(a[12], "workspace");
       bytes = static_cast<size_t>(t.numel());
       ws = plain(t, ScalarType::Byte, {t.numel()}, dev, "workspace");
-    } else {
+    } else if (size[0] < static_cast<int64_t>(c.max_blocks) * c.block) {  // else nothing goes, and none is needed
       bytes = g_evict4_bytes(c.B, c.Hkv, static_cast<int32_t>(size[0]));
       room = at::empty({static_cast<int64_t>(std::max<size_t>(bytes, 16))}, lens.options().dtype(ScalarType::Byte));
       ws = room.data_ptr();
