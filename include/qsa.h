@@ -587,9 +587,9 @@ qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_
  *
  *   weights  f32 [n_pages, Hkv, block], 16-byte aligned.
  *   budget   >= 1; sink, recent >= 0, sink + recent <= budget.
- *   lens_out int32 [B]: min(lens, budget). May not be lens itself.
+ *   lens_out int32 [B]: min(lens, budget). May not overlap lens.
  *   offset   optional int32 [B]: grows by the number of tokens that went, as
- *            qsa_kv4_append takes it. May be neither lens nor lens_out.
+ *            qsa_kv4_append takes it. May overlap neither lens nor lens_out.
  *   workspace  device, 16-byte aligned, at least
  *            qsa_kv4_evict_workspace_bytes bytes; needs no initialisation.
  *            Calls that may run at the same time need separate ones. A budget of

@@ -35,3 +35,9 @@ def test_takes_nothing_out(budget, sink, recent):
         x = t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
         assert np.array_equal(x, c[name], equal_nan=x.dtype == np.float32), name
     assert tbs.qsa_device_status(clear=True) == (0, 0)
+
+
+def test_lengths_and_offsets_that_overlap_are_refused(lib):  # noqa: F811
+    for kw in (dict(lens=A), dict(lens=A + 4), dict(lens=A - 4), dict(offset=A + 4), dict(offset=2 * A - 4),
+               dict(offset=2 * A + 4), dict(offset=2 * A), dict(lens=A + 4, offset=4 * A)):
+        assert host.evict(lib, **kw) == INVALID, kw

@@ -723,8 +723,8 @@ def qsa_kv4_evict(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights,
     head keeps its first sink tokens, its last recent ones, and of the others
     those of the largest weights (equal ones: the lowest slot first), in their
     order. offset, an optional int32 [B], grows by the tokens that went. Returns
-    lens_out int32 [B], min(lens, budget) (a tensor other than lens, allocated
-    here when not given). workspace: a CUDA uint8 tensor of
+    lens_out int32 [B], min(lens, budget) (a tensor that overlaps neither lens nor
+    offset, allocated here when not given). workspace: a CUDA uint8 tensor of
     qsa_kv4_evict_workspace_bytes, allocated here when not given; a budget of
     the page table's tokens or more takes nothing out and needs none."""
     r = (_KV or _kv_binding()).evict4(k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, budget, sink,

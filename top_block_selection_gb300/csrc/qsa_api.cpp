@@ -732,14 +732,20 @@ qsa_status qsa_kv4_evict(const qsa_kv4_cache* cache, float* weights, int32_t bud
   if (cache->B == 0) return QSA_OK;
   if ((st = check_cache_pointers(cache)) != QSA_OK) return st;
   if (cache->n_pages < 1 || cache->max_blocks < 1) return QSA_ERR_INVALID_ARG;
-  if (!weights || !lens_out || lens_out == cache->lens || lens_out == offset || offset == cache->lens)
-    return QSA_ERR_INVALID_ARG;
+  if (!weights || !lens_out) return QSA_ERR_INVALID_ARG;
   // (No sequence is longer than its page table.)
   if (budget < cache->max_blocks * cache->block &&
       (!workspace || workspace_bytes < qsa::kv4_evict_workspace_bytes(cache->B, cache->Hkv, budget)))
     return QSA_ERR_INVALID_ARG;
   if (!aligned(weights, 16) || !aligned(lens_out, 4) || !aligned(offset, 4) || !aligned(workspace, 16))
     return QSA_ERR_MISALIGNED;
+  // Each sequence's length is read while others' are written.
+  const uintptr_t ints[3] = {reinterpret_cast<uintptr_t>(cache->lens), reinterpret_cast<uintptr_t>(lens_out),
+                             reinterpret_cast<uintptr_t>(offset)};
+  for (int i = 0; i < 3; ++i) {
+    const uintptr_t x = ints[i], y = ints[(i + 1) % 3];
+    if (x && y && (x > y ? x - y : y - x) < sizeof(int32_t) * static_cast<uintptr_t>(cache->B)) return QSA_ERR_INVALID_ARG;
+  }
   const qsa::Kv4EvictProblem p{cache_args(cache), weights,  budget, sink,
                                recent,            lens_out, offset, static_cast<int32_t*>(workspace)};
   const DeviceInfo* dev = nullptr;
