@@ -545,7 +545,8 @@ qsa_status qsa_kv4_read(const qsa_kv4_cache* cache, int32_t n, qsa_dtype dtype, 
  * many; calls of few rows are those with ids, with Hq / Hkv * n < 128, with
  * B * n * Hq < 512 or with B * n * Hq * max_blocks * block < 10 * 2^20 (4 * 2^20 of
  * 64 dimensions); and in calls of many rows keys whose scale is below 2^-25 of the largest among
- * slots 16 i to 16 i + 15 are held to 2^-37 of what that one stands for.
+ * slots 16 i to 16 i + 15 are held to 2^-37 of what that one stands for, and of bf16 calls a
+ * query's elements below 2^-24 of its largest to 2^-32 of that (or to 2^-125).
  */
 size_t qsa_kv4_attend_workspace_bytes(int32_t B, int32_t n, int32_t Hq, int32_t Hkv, int32_t D);
 qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,
@@ -562,16 +563,20 @@ qsa_status qsa_kv4_attend(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t
  * every token when decay is 0 (w is then not read).
  *
  *   q, n, Hq, dtype, scale  as for qsa_kv4_attend.
- *   lse    f32 [B, n, Hq], as qsa_kv4_attend wrote it for the same rows; a row
- *          with -inf gives no token any weight.
+ *   lse    f32 [B, n, Hq], as qsa_kv4_attend wrote it for the same rows over the
+ *          whole cache; a row with -inf gives no token any weight. (The lse of a call
+ *          with ids is of the blocks chosen there alone. The sum runs over every
+ *          token here, so that what it gives for such rows are no attention weights
+ *          and have no bound.)
  *   decay  finite, not negative.
  *   weights  f32 [n_pages, Hkv, block], 16-byte aligned. The tokens of the
  *          call's sequences are updated, every other slot keeps its value.
  * A page may hold tokens of one sequence only, and appear once in its table row.
- * Scores and sums are fp32, a query's elements held as by qsa_kv4_attend. Results
- * do not depend on timing. cache->v and v_scale are not read and may be NULL. A
+ * Scores and sums are fp32, a query's elements held as by qsa_kv4_attend for few rows.
+ * Results do not depend on timing. cache->v and v_scale are not read and may be NULL. A
  * key scale of NaN makes its token's weight NaN where a row with another lse than
- * -inf sees it. With n = 0 nothing changes.
+ * -inf sees it. A sequence without new rows (n_new 0) has its weights multiplied by decay;
+ * a call with n = 0 changes nothing.
  * Errors as for qsa_kv4_attend (QSA_ERR_INVALID_ARG for a bad decay).
  */
 qsa_status qsa_kv4_weights(const qsa_kv4_cache* cache, const qsa_rows* q, int32_t n, int32_t Hq,

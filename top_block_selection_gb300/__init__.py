@@ -704,7 +704,8 @@ def qsa_kv4_weights(q, lse, k_cache, v_cache, k_scale, v_scale, page_table, lens
     what the attention of q [B, n, Hq, D] gives it, summed over the rows and the
     query heads of its KV head, after multiplying it by decay; the call's own new
     tokens start from 0, and so does every token when decay is 0. lse f32
-    [B, n, Hq] is what qsa_kv4_attend wrote for these rows. Returns weights."""
+    [B, n, Hq] is what qsa_kv4_attend wrote for these rows over the whole cache
+    (without ids). Returns weights."""
     r = (_KV or _kv_binding()).weights4(q, lse, k_cache, v_cache, k_scale, v_scale, page_table, lens, weights, scale,
                                         n_new, decay)
     if r.__class__ is int:
