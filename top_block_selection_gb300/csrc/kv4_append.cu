@@ -209,7 +209,9 @@ struct ReadArgs {
 };
 
 // TPT threads a row (token, head, K or V), of 16 elements each; a row's code
-// times scale is exact in fp32 and rounded once. Bound by bytes.
+// times scale is exact in fp32 and rounded once. 4,096 tokens take twice the time of
+// their bytes at a plain copy's rate (6.6 us, 3.1): each thread has one chain of loads
+// (lengths, page, codes), and no unit is above 45% (issue slots 55%).
 template <int TPT, bool BF16>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ ReadArgs a) {
   pdl_wait();

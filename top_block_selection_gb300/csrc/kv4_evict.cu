@@ -13,10 +13,12 @@
 // chunk's stores touch no later chunk's sources; within a chunk all CTAs load
 // before any stores, until the chunks come from beyond the budget altogether.
 //
-// What bounds it: bytes for many items (64 sequences of 4,160 tokens to 4,096, 8 heads:
-// 86 us in a stream of calls, the time of their bytes at a plain copy's rate); for few, the chain of a
-// chunk's dependent loads (list, page, codes), its cluster barrier and the three
-// histograms' (8 heads of 131,072 tokens to 32,768: 38.8 us, 1.9 TB/s).
+// What bounds it: bytes for many items (64 sequences of 4,160 tokens to 4,096, 8 heads,
+// with weights that no eviction has seen: 118 us, 72% of a plain copy's rate); for few,
+// the chain of a chunk's dependent loads (list, page, codes), its cluster barrier and the
+// three histograms' (8 heads of 131,072 tokens to 32,768: 50 us, 1.5 TB/s). The same
+// sequences shortened over and over take 86 and 38.8 us, the basis of the figures below:
+// fewer tokens change their place then, and those lie side by side.
 #include <algorithm>
 #include <atomic>
 
@@ -466,6 +468,9 @@ cudaError_t launch_kv4_evict(const Kv4EvictProblem& p, const DeviceInfo& dev, cu
   const int64_t longest = static_cast<int64_t>(p.cache.max_blocks) * p.cache.block;
   a.ctas = kMaxCluster;
   while (a.ctas > 1 && (items * a.ctas > 2 * dev.sm_count || longest < 1024 * a.ctas)) a.ctas /= 2;
+  // (Keys by the table's room: past some 22,500 tokens a CTA of the first form has no
+  // other beside it on its SM. The 64 sequences of 4,160 tokens take 118 us with tables
+  // of that length, 129 with room for 16,384 tokens, 175 for 32,832, 185 for 131,072.)
   a.cap = static_cast<int32_t>(std::min<int64_t>((longest + a.ctas - 1) / a.ctas, kMaxKeys));
   // Many items: small CTAs, two an SM, whose phases overlap (64 x 8 items of 4,160
   // tokens 120 us; four an SM with half the pieces 159, one of 512 threads 138). Few:

@@ -103,9 +103,10 @@ __global__ void __launch_bounds__(32 * kCombineRows) kv_combine_kernel(const __g
 
 // 4-bit cache: the join is a launch of its own, about 4 us of a call in a stream, as
 // long as so many tiles of a CTA. Where a CTA for each item is no more than that
-// behind equal shares, nothing is split (one token over 1,000 tokens 6.9 us instead
-// of 8.1, 32 requests with 64 chosen blocks 20.4 instead of 25.1; 4 and 16 tiles were
-// no better).
+// behind equal shares, nothing is split (one token over 1,000 tokens 7.2 us instead
+// of 8.3, replayed by a graph, 32 requests with 64 chosen blocks 20.4 instead of 25.1;
+// 4 and 16 tiles were no better). Of whole contexts the table's room decides, as lengths
+// are on the device: the same token with a table for 131,072 takes the 8.3 us.
 constexpr int kJoinTiles = 8;
 // 4-bit cache: tiles of a CTA up to which the heads of an item are split in two where
 // one item's columns would need the form of 32, which takes 1.8 to 2 times as long a
